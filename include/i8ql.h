@@ -47,7 +47,10 @@ enum {
     I8QL_ERR_TIMEOUT = 4,      /* a kernel's bounded wait gave up (sticky word)        */
     I8QL_ERR_BAD_OFFSETS = 5,  /* grouped offsets not 0 .. T_total, non-decreasing     */
     I8QL_ERR_NO_DEVICE = 6,    /* no CUDA device, or not an sm_103 device              */
-    I8QL_ERR_WORKSPACE_LIMIT = 7 /* w8a8_gemm_noalloc: problem exceeds its fixed array  */
+    I8QL_ERR_WORKSPACE_LIMIT = 7,/* w8a8_gemm_noalloc: problem exceeds its fixed array;
+                                    kv_cache_attention: workspace too small            */
+    I8QL_ERR_BAD_INDEX = 8       /* a cache slot, page, length or query offset is out of
+                                    range (sticky word)                                */
 };
 
 /* Largest K whose worst-case int8 dot product fits int32:
@@ -403,6 +406,110 @@ i8ql_status moe_expert_mlp_w8a16(const i8ql_bf16* x, const float* logits, int64_
                                  int64_t I, void* stream);
 
 /*
+ * The quantized key/value cache: keys and values are quantized as they are
+ * written, read back, and attended over without being widened in memory.
+ *
+ * The cache is a pool of num_pages pages of page_size tokens (a power of
+ * two, I8QL_KV_MIN_PAGE .. I8QL_KV_MAX_PAGE), for H heads of D channels
+ * (64 or 128) in `bits` bits (4 or 8):
+ *   codes  uint8 [num_pages, 2, H, page_size, D * bits / 8]  (0: keys, 1:
+ *          values; 4 bits: two codes per byte, the even channel in the low
+ *          nibble), 16-byte aligned
+ *   params bf16 [num_pages, 2, H, page_size, 2]  (scale, low), 16-byte
+ *          aligned
+ * A row (one token of one head) stands for low + scale * code[d], codes
+ * 0 .. L with L = 2^bits - 1.  Unsupported sizes return
+ * I8QL_ERR_UNSUPPORTED.  Every offset into the cache is 64 bits wide.
+ */
+#define I8QL_KV_MIN_PAGE 16
+#define I8QL_KV_MAX_PAGE 256
+
+/*
+ * Quantizes keys and values into the cache.
+ *
+ * No counterpart on the pages, which quantize weights and activations only.
+ * The arithmetic is theirs for activations (dynamic, one scale per token;
+ * here per token and head), asymmetric as 4 bits want it:
+ *   lo = min_d x[d], hi = max_d x[d], r = fl32(fl32(hi - lo) / L),
+ *   scale = the smallest bf16 >= r, low = lo (a bf16 value),
+ *   code[d] = rint(fl32(fl32(x[d] - lo) / scale)) (IEEE fp32 divisions, ties
+ *   to even), or 0 when scale = 0.
+ * Rounding the scale up keeps every code inside 0 .. L: the value read back
+ * is within scale / 2 of x[d], and the row's lowest value exact.
+ *
+ * k and v: bf16 [T, H, D], the H * D values of a token contiguous, tokens
+ * k_stride and v_stride elements apart (>= H * D, multiples of 8; so slices
+ * of a fused projection need no copy), 16-byte aligned.  slots int64 [T]:
+ * token t goes to page slots[t] / page_size, place slots[t] % page_size; a
+ * negative slot writes nothing; a slot past the cache writes nothing and
+ * records I8QL_ERR_BAD_INDEX.  Slots must differ.  T * H < 2^30.  Values
+ * must be finite and below 2^126 in magnitude; others give unspecified codes
+ * and params of their own row.
+ */
+i8ql_status kv_cache_store(const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_stride, int64_t v_stride,
+                           const int64_t* slots, uint8_t* codes, i8ql_bf16* params, int64_t T, int64_t H, int64_t D,
+                           int64_t bits, int64_t page_size, int64_t num_pages, void* stream);
+
+/*
+ * Reads keys and values back: k and v bf16 [T, H, D] (dense) receive
+ * bf16_rne(low + scale * code) of the rows at slots[t], zeros where the slot
+ * is negative (or, recording I8QL_ERR_BAD_INDEX, past the cache).
+ *
+ * No counterpart on the pages.  Arguments as kv_cache_store.
+ */
+i8ql_status kv_cache_load(const uint8_t* codes, const i8ql_bf16* params, const int64_t* slots, i8ql_bf16* k,
+                          i8ql_bf16* v, int64_t T, int64_t H, int64_t D, int64_t bits, int64_t page_size,
+                          int64_t num_pages, void* stream);
+
+/*
+ * Causal attention of B sequences over the cache: single tokens, short
+ * drafts and prompt chunks, with grouped query heads.
+ *
+ * No counterpart on the pages.  Sequence b has kv_lens[b] tokens in the
+ * cache, token j in page page_table[b, j / page_size]; its n query tokens
+ * are the last n of them: rows q_offsets[b] .. q_offsets[b+1]-1 of q, the
+ * i-th at position p = kv_lens[b] - n + i, seeing the tokens j <= p, and with
+ * window > 0 only those with j > p - window.  With G = Hq / H query heads per
+ * cache head, query head h attends over cache head h / G:
+ *   a_j = softmax_scale * sum_d q[d] k_j[d];  out[d] = bf16(sum_j e^a_j v_j[d] / sum_j e^a_j)
+ * (k, v: low + scale * code, not rounded to bf16 on the way with at most 32
+ * query rows a head group; see the sources).  A row that sees no token
+ * (p < 0: more queries than tokens) is 0.  fp32 logits, sums and softmax.
+ *
+ * Inputs: q bf16, token t's Hq * D values contiguous at t * q_stride (>= Hq *
+ * D, a multiple of 8), 16-byte aligned; page_table int32 [B, table_width]
+ * (entries that no visible token needs are not read as pages: any value);
+ * kv_lens int32 [B]; q_offsets int32 [B+1] from 0 to T_q, non-decreasing, or
+ * NULL for one query token per sequence (T_q = B).  max_q: an upper bound of
+ * the query tokens of one sequence; it only chooses the kernel.  Output: out
+ * bf16 [T_q, Hq, D] (dense).  What the cache holds behind a sequence's end
+ * is never used.  Lengths, offsets or pages out of range record
+ * I8QL_ERR_BAD_INDEX and leave unspecified rows.
+ *
+ * workspace: I8QL_ERR_WORKSPACE_LIMIT when smaller than
+ * i8ql_kv_attention_workspace reports for these sizes; 16-byte aligned; it
+ * need not be cleared, and belongs to the call until its work is done.
+ * Limits: B, num_pages < 2^31, T_q * G < 2^30, table_width * page_size <=
+ * 2^31 - 65536.  The result does not depend on timing: the same inputs give
+ * the same bits on the same device.
+ */
+i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8_t* codes, const i8ql_bf16* params,
+                               const int32_t* page_table, int64_t table_width, const int32_t* kv_lens,
+                               const int32_t* q_offsets, i8ql_bf16* out, int64_t B, int64_t T_q, int64_t Hq, int64_t H,
+                               int64_t D, int64_t bits, int64_t page_size, int64_t num_pages, int64_t max_q,
+                               int64_t window, float softmax_scale, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Workspace of a kv_cache_attention call of these sizes on the current
+ * device, in bytes (*bytes is a HOST pointer; 0: none is needed).  No
+ * counterpart on the pages.  Depends on sizes only, so a caller can keep one
+ * buffer for the largest call.
+ */
+i8ql_status i8ql_kv_attention_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
+                                        int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes);
+
+/*
  * W8A8 GEMM that allocates nothing.
  *
  * No counterpart on the pages: this entry point exists for callers that
@@ -491,8 +598,9 @@ i8ql_status i8ql_w8a8_linear_launches(int64_t M, int64_t N, int64_t K, int32_t* 
 
 /*
  * Waits for `stream`, then reads and clears the current device's sticky
- * kernel-error word.  Returns I8QL_OK, I8QL_ERR_TIMEOUT or
- * I8QL_ERR_BAD_OFFSETS (the first fault recorded since the last read), or
+ * kernel-error word.  Returns I8QL_OK, I8QL_ERR_TIMEOUT,
+ * I8QL_ERR_BAD_OFFSETS or I8QL_ERR_BAD_INDEX (a fault recorded since the
+ * last read; the first of this list when there were several), or
  * I8QL_ERR_CUDA if the wait itself failed.  No counterpart on the pages:
  * the failure signal of the kernels' bounded waits and offset checks.
  */

@@ -12,11 +12,16 @@ from .capi import (  # noqa: F401
     i8ql_early_weight_loads,
     i8ql_fp8_plan,
     i8ql_get_device_error,
+    i8ql_kv_attention_workspace,
     i8ql_set_early_weight_loads,
     i8ql_version,
     i8ql_w8a8_linear_launches,
     i8ql_w8a8_noalloc_plan,
     i8ql_w8a8_plan,
+    kv_cache_alloc,
+    kv_cache_attention,
+    kv_cache_load,
+    kv_cache_store,
     moe_combine,
     moe_expert_mlp_w8a16,
     moe_route_topk,

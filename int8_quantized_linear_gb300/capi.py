@@ -26,12 +26,15 @@ I8QL_ERR_TIMEOUT = 4
 I8QL_ERR_BAD_OFFSETS = 5
 I8QL_ERR_NO_DEVICE = 6
 I8QL_ERR_WORKSPACE_LIMIT = 7
+I8QL_ERR_BAD_INDEX = 8
 I8QL_MAX_K = 133144
 I8QL_NOALLOC_MAX_ELEMENTS = 16 * 1024 * 1024
+I8QL_KV_MIN_PAGE = 16
+I8QL_KV_MAX_PAGE = 256
 I8QL_W8A8_DECODE_MAX_M = 32  # w8a8_gemm runs the decode kernel up to this M
 
 # Every symbol the C header declares, with its ctypes signature.
-_P, _I64, _S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_P, _I64, _S, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 SIGNATURES = {
     "quantize_weight_per_channel_int8": (_S, [_P, _I64, _I64, _P, _P, _P]),
     "quantize_act_per_token_int8": (_S, [_P, _I64, _I64, _P, _P, _P]),
@@ -60,6 +63,10 @@ SIGNATURES = {
     "moe_route_topk": (_S, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "grouped_w8a16_silu_mul": (_S, [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P]),
     "moe_combine": (_S, [_P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "kv_cache_store": (_S, [_P, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P]),
+    "kv_cache_load": (_S, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P]),
+    "kv_cache_attention": (_S, [_P, _I64, _P, _P, _P, _I64, _P, _P, _P, *[_I64] * 10, _F, _P, _I64, _P]),
+    "i8ql_kv_attention_workspace": (_S, [*[_I64] * 9, _P]),
     "moe_expert_mlp_w8a16": (_S, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
 }
 
@@ -490,4 +497,137 @@ def moe_expert_mlp_w8a16(x, logits, top_k, n_shared, qw_gate_up, sw_gate_up, qw_
     _check(lib().moe_expert_mlp_w8a16(_ptr(x), _ptr(logits), e_r, top_k, n_shared, _ptr(qw_gate_up),
                                       _ptr(sw_gate_up), _ptr(qw_down), _ptr(sw_down), _ptr(out), t, hid, inter,
                                       _stream(stream)), "moe_expert_mlp_w8a16")
+    return out
+
+
+# ---------------------------------------------------------------- quantized key/value cache
+
+def kv_cache_alloc(num_pages, heads, page_size, head_dim, bits=4, device="cuda"):
+    """An empty cache of num_pages pages: codes uint8 [num_pages, 2, heads,
+    page_size, head_dim * bits / 8] and params bf16 [num_pages, 2, heads,
+    page_size, 2] (scale, low); index 0 of the second axis holds the keys."""
+    if bits not in (4, 8):
+        raise ValueError("bits must be 4 or 8")
+    codes = torch.empty((num_pages, 2, heads, page_size, head_dim * bits // 8), dtype=torch.uint8, device=device)
+    params = torch.empty((num_pages, 2, heads, page_size, 2), dtype=torch.bfloat16, device=device)
+    return codes, params
+
+
+def _kv_cache(codes: torch.Tensor, params: torch.Tensor, head_dim: int) -> tuple[int, int, int, int]:
+    """(num_pages, heads, page_size, bits) of a cache for rows of head_dim channels."""
+    if codes.dim() != 5 or codes.shape[1] != 2:
+        raise ValueError("codes must be [num_pages, 2, heads, page_size, head_dim * bits / 8]")
+    pages, _, heads, page, row = codes.shape
+    bits = 4 if 2 * row == head_dim else 8
+    _need(codes, torch.uint8, (pages, 2, heads, page, head_dim * bits // 8), "codes")
+    _need(params, torch.bfloat16, (pages, 2, heads, page, 2), "params")
+    return pages, heads, page, bits
+
+
+def _need_heads(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
+    """Checks bf16 [T, heads, head_dim] whose tokens are dense (tokens may lie
+    apart: a slice of a fused projection's rows); returns their distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must have shape [T, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if t.numel() and not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    step, head_step, one = t.stride()
+    if t.shape[0] and (one != 1 or (heads > 1 and head_step != head_dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return step if t.shape[0] > 1 else heads * head_dim
+
+
+def kv_cache_store(k, v, slots, codes, params, stream=None):
+    """Quantizes keys and values, bf16 [T, heads, head_dim] (slices of a fused
+    projection are fine), into the cache rows slots (int64 [T]: page *
+    page_size + place; negative: skipped).  Returns (codes, params)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [T, heads, head_dim]")
+    t, h, d = k.shape
+    pages, heads, page, bits = _kv_cache(codes, params, d)
+    k_step = _need_heads(k, heads, d, "k")
+    v_step = _need_heads(v, heads, d, "v")
+    if v.shape[0] != t:
+        raise ValueError("k and v disagree on T")
+    _need(slots, torch.int64, (t,), "slots")
+    _check(lib().kv_cache_store(_ptr(k), _ptr(v), k_step, v_step, _ptr(slots), _ptr(codes), _ptr(params), t, h, d,
+                                bits, page, pages, _stream(stream)), "kv_cache_store")
+    return codes, params
+
+
+def kv_cache_load(codes, params, slots, head_dim, k=None, v=None, stream=None):
+    """(k, v) bf16 [T, heads, head_dim]: the cache rows at slots, bf16(low +
+    scale * code); zeros where the slot is negative."""
+    pages, heads, page, bits = _kv_cache(codes, params, head_dim)
+    t = slots.shape[0]
+    _need(slots, torch.int64, (t,), "slots")
+    if k is None:
+        k = torch.empty((t, heads, head_dim), dtype=torch.bfloat16, device=codes.device)
+    if v is None:
+        v = torch.empty((t, heads, head_dim), dtype=torch.bfloat16, device=codes.device)
+    _need(k, torch.bfloat16, (t, heads, head_dim), "k")
+    _need(v, torch.bfloat16, (t, heads, head_dim), "v")
+    _check(lib().kv_cache_load(_ptr(codes), _ptr(params), _ptr(slots), _ptr(k), _ptr(v), t, heads, head_dim, bits,
+                               page, pages, _stream(stream)), "kv_cache_load")
+    return k, v
+
+
+def i8ql_kv_attention_workspace(batch, tokens, q_heads, heads, head_dim, bits, page_size, table_width, max_q=1) -> int:
+    """Bytes of workspace a kv_cache_attention call of these sizes takes on
+    the current device."""
+    n = ctypes.c_int64(0)
+    _check(lib().i8ql_kv_attention_workspace(batch, tokens, q_heads, heads, head_dim, bits, page_size, table_width,
+                                             max_q, ctypes.byref(n)), "i8ql_kv_attention_workspace")
+    return n.value
+
+
+def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, max_q=None, window=0, scale=None,
+                       out=None, workspace=None, stream=None):
+    """Causal attention of bf16 q [T, q_heads, head_dim] over the cache.
+
+    Sequence b has kv_lens[b] (int32 [B]) tokens in the pages page_table[b]
+    (int32 [B, width]) and the query rows q_offsets[b] .. q_offsets[b+1]
+    (int32 [B+1]; None: one row each), its last tokens.  max_q: an upper bound
+    of one sequence's query rows, when known (it chooses the kernel).  window:
+    how many tokens a query sees, itself included (0: all).  scale: the
+    softmax scale, head_dim ** -0.5 by default.  workspace: uint8, at least
+    i8ql_kv_attention_workspace bytes (taken from torch when None).  Returns
+    bf16 [T, q_heads, head_dim]."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, head_dim]")
+    t, hq, d = q.shape
+    pages, heads, page, bits = _kv_cache(codes, params, d)
+    q_step = _need_heads(q, hq, d, "q")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width]")
+    b, width = page_table.shape
+    _need(page_table, torch.int32, (b, width), "page_table")
+    _need(kv_lens, torch.int32, (b,), "kv_lens")
+    if q_offsets is not None:
+        _need(q_offsets, torch.int32, (b + 1,), "q_offsets")
+    if max_q is None:
+        max_q = 1 if q_offsets is None else max(t, 1)
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=codes.device)
+    _need(out, torch.bfloat16, (t, hq, d), "out")
+    if workspace is None:
+        size = i8ql_kv_attention_workspace(b, t, hq, heads, d, bits, page, width, max_q)
+        # allocated with the call's stream current, so that the allocator knows which stream uses it
+        if stream is not None and size:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(int(stream))):
+                workspace = torch.empty((size,), dtype=torch.uint8, device=codes.device)
+        else:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=codes.device)
+    else:
+        _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
+        size = workspace.numel()
+    _check(lib().kv_cache_attention(_ptr(q), q_step, _ptr(codes), _ptr(params), _ptr(page_table), width,
+                                    _ptr(kv_lens), _ptr(q_offsets), _ptr(out), b, t, hq, heads, d, bits, page, pages,
+                                    max_q, window, d ** -0.5 if scale is None else scale, _ptr(workspace), size,
+                                    _stream(stream)), "kv_cache_attention")
     return out

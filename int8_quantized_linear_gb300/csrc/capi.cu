@@ -9,7 +9,10 @@
 #include <atomic>
 #include <mutex>
 
+#include <cmath>
+
 #include "common.cuh"
+#include "kv_schedule.cuh"
 
 namespace i8ql {
 
@@ -419,6 +422,143 @@ i8ql_status moe_expert_mlp_w8a16(const i8ql_bf16* x, const float* logits, int64_
                                     out, T, H, I, env));
 }
 
+namespace {
+
+// Sizes every call on the key/value cache checks.
+i8ql_status check_kv(int64_t H, int64_t D, int64_t bits, int64_t page_size, int64_t num_pages) {
+    if (H <= 0 || D <= 0 || num_pages <= 0 || page_size <= 0) return I8QL_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || (bits != 4 && bits != 8) || H > 65535 || num_pages >= kMaxRows ||
+        page_size < kKvMinPage || page_size > kKvMaxPage || (page_size & (page_size - 1)) != 0)
+        return I8QL_ERR_UNSUPPORTED;
+    return I8QL_OK;
+}
+
+// Token rows of n values, `stride` elements apart.
+i8ql_status check_strided(const void* p, int64_t rows, int64_t n, int64_t stride) {
+    if (stride < n || stride % 8 != 0) return I8QL_ERR_INVALID_ARG;
+    return check_matrix(p, rows);
+}
+
+KvCache make_kv_cache(const uint8_t* codes, const i8ql_bf16* params, int64_t H, int64_t page_size, int64_t num_pages) {
+    KvCache c;
+    c.codes = const_cast<uint8_t*>(codes);
+    c.params = reinterpret_cast<uint32_t*>(const_cast<i8ql_bf16*>(params));
+    c.pages = num_pages;
+    c.H = (int)H;
+    c.page_shift = 0;
+    while (((int64_t)1 << c.page_shift) < page_size) ++c.page_shift;
+    return c;
+}
+
+i8ql_status check_kv_attention(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t page_size, int64_t table_width,
+                               int64_t max_q) {
+    if (B < 0 || T_q < 0 || Hq <= 0 || Hq % H != 0 || table_width <= 0 || max_q <= 0) return I8QL_ERR_INVALID_ARG;
+    if (B >= kMaxRows || Hq > 65535 || T_q >= ((int64_t)1 << 30) || T_q * (Hq / H) >= ((int64_t)1 << 30) ||
+        table_width > (kMaxRows - 65536) / page_size)
+        return I8QL_ERR_UNSUPPORTED;
+    return I8QL_OK;
+}
+
+}  // namespace
+
+i8ql_status kv_cache_store(const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_stride, int64_t v_stride,
+                           const int64_t* slots, uint8_t* codes, i8ql_bf16* params, int64_t T, int64_t H, int64_t D,
+                           int64_t bits, int64_t page_size, int64_t num_pages, void* stream) {
+    I8QL_TRY(check_rows(T));
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    if (T * H >= ((int64_t)1 << 30)) return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_strided(k, T, H * D, k_stride));
+    I8QL_TRY(check_strided(v, T, H * D, v_stride));
+    I8QL_TRY(check_vec(slots, T, 8));
+    I8QL_TRY(check_matrix(codes, T));
+    I8QL_TRY(check_matrix(params, T));
+    if (T == 0) return I8QL_OK;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    return from_cuda(launch_kv_store(k, v, k_stride, v_stride, slots, make_kv_cache(codes, params, H, page_size, num_pages),
+                                     T, D, bits, env));
+}
+
+i8ql_status kv_cache_load(const uint8_t* codes, const i8ql_bf16* params, const int64_t* slots, i8ql_bf16* k,
+                          i8ql_bf16* v, int64_t T, int64_t H, int64_t D, int64_t bits, int64_t page_size,
+                          int64_t num_pages, void* stream) {
+    I8QL_TRY(check_rows(T));
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    if (T * H >= ((int64_t)1 << 30)) return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_vec(slots, T, 8));
+    I8QL_TRY(check_matrix(codes, T));
+    I8QL_TRY(check_matrix(params, T));
+    I8QL_TRY(check_matrix(k, T));
+    I8QL_TRY(check_matrix(v, T));
+    if (T == 0) return I8QL_OK;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    return from_cuda(launch_kv_load(make_kv_cache(codes, params, H, page_size, num_pages), slots, k, v, T, D, bits, env));
+}
+
+i8ql_status i8ql_kv_attention_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
+                                        int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes) {
+    I8QL_TRY(check_kv(H, D, bits, page_size, 1));
+    I8QL_TRY(check_kv_attention(B, T_q, Hq, H, page_size, table_width, max_q));
+    if (bytes == nullptr) return I8QL_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (B == 0 || T_q == 0) return I8QL_OK;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(nullptr, &env, &s)) return s;
+    *bytes = (int64_t)kv_attention_workspace(B, T_q, Hq / H, H, D, bits, table_width * page_size, max_q, env.sm_count);
+    return I8QL_OK;
+}
+
+i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8_t* codes, const i8ql_bf16* params,
+                               const int32_t* page_table, int64_t table_width, const int32_t* kv_lens,
+                               const int32_t* q_offsets, i8ql_bf16* out, int64_t B, int64_t T_q, int64_t Hq, int64_t H,
+                               int64_t D, int64_t bits, int64_t page_size, int64_t num_pages, int64_t max_q,
+                               int64_t window, float softmax_scale, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    I8QL_TRY(check_kv_attention(B, T_q, Hq, H, page_size, table_width, max_q));
+    if (window < 0 || !std::isfinite(softmax_scale)) return I8QL_ERR_INVALID_ARG;
+    if (q_offsets == nullptr && T_q != B) return I8QL_ERR_INVALID_ARG;
+    I8QL_TRY(check_strided(q, T_q, Hq * D, q_stride));
+    I8QL_TRY(check_matrix(codes, T_q));
+    I8QL_TRY(check_matrix(params, T_q));
+    I8QL_TRY(check_vec(page_table, T_q, 4));
+    I8QL_TRY(check_vec(kv_lens, T_q, 4));
+    if (q_offsets != nullptr && !aligned(q_offsets, 4)) return I8QL_ERR_INVALID_ARG;
+    I8QL_TRY(check_matrix(out, T_q));
+    if (T_q == 0) return I8QL_OK;
+    if (B == 0) return I8QL_ERR_INVALID_ARG;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    const int64_t G = Hq / H;
+    const int64_t need =
+        (int64_t)kv_attention_workspace(B, T_q, G, H, D, bits, table_width * page_size, max_q, env.sm_count);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return I8QL_ERR_WORKSPACE_LIMIT;
+        if (!aligned(workspace, 16)) return I8QL_ERR_INVALID_ARG;
+    }
+    KvAttnParams p = {};
+    p.cache = make_kv_cache(codes, params, H, page_size, num_pages);
+    p.q = q;
+    p.q_stride = q_stride;
+    p.table = page_table;
+    p.table_width = table_width;
+    p.kv_lens = kv_lens;
+    p.q_offsets = q_offsets;
+    p.out = out;
+    p.B = B;
+    p.T_q = T_q;
+    p.G = (int)G;
+    p.window = window;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.err = env.err;
+    return from_cuda(launch_kv_attention(p, D, bits, max_q, workspace, env));
+}
+
 i8ql_status i8ql_get_device_error(void* stream) {
     LaunchEnv env;
     i8ql_status s;
@@ -434,6 +574,7 @@ i8ql_status i8ql_get_device_error(void* stream) {
     }
     if (word & kErrBitTimeout) return I8QL_ERR_TIMEOUT;
     if (word & kErrBitBadOffsets) return I8QL_ERR_BAD_OFFSETS;
+    if (word & kErrBitBadIndex) return I8QL_ERR_BAD_INDEX;
     return I8QL_OK;
 }
 
@@ -512,7 +653,9 @@ const char* i8ql_status_string(i8ql_status status) {
         case I8QL_ERR_BAD_OFFSETS: return "grouped offsets are not 0..T_total and non-decreasing";
         case I8QL_ERR_NO_DEVICE: return "no usable sm_103 CUDA device";
         case I8QL_ERR_WORKSPACE_LIMIT:
-            return "problem too large for the fixed workspace of w8a8_gemm_noalloc (M * K > 16 Mi for M > 32)";
+            return "workspace too small (w8a8_gemm_noalloc: M * K > 16 Mi for M > 32 exceeds its fixed array; "
+                   "kv_cache_attention: less than i8ql_kv_attention_workspace reports)";
+        case I8QL_ERR_BAD_INDEX: return "a cache slot, page, length or query offset is out of range";
         default: return "unknown status";
     }
 }

@@ -16,6 +16,7 @@ namespace i8ql {
 // Sticky per-device kernel fault word.  Kernels OR a status bit into it:
 constexpr unsigned kErrBitTimeout = 1u;
 constexpr unsigned kErrBitBadOffsets = 2u;
+constexpr unsigned kErrBitBadIndex = 4u;
 
 // Largest supported sizes (indices stay well inside 64-bit arithmetic and
 // grid limits).
@@ -191,6 +192,21 @@ cudaError_t launch_quant_w4(const uint16_t* w, int64_t N, int64_t K, uint8_t* pa
                             const LaunchEnv& env);
 cudaError_t launch_w4a16(const uint16_t* x, const uint8_t* q, const uint16_t* s, uint16_t* y, int64_t M, int64_t N,
                          int64_t K, const LaunchEnv& env);
+// The quantized key/value cache (kv_common.cuh): written and read back by
+// slot, attended over through a page table.
+struct KvCache;
+struct KvAttnParams;
+cudaError_t launch_kv_store(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                            const int64_t* slots, const KvCache& cache, int64_t T, int64_t D, int64_t bits,
+                            const LaunchEnv& env);
+cudaError_t launch_kv_load(const KvCache& cache, const int64_t* slots, uint16_t* k, uint16_t* v, int64_t T, int64_t D,
+                           int64_t bits, const LaunchEnv& env);
+// Workspace bytes launch_kv_attention wants for these sizes, and the launch:
+// the parts' addresses in `p` are set from `workspace`.
+size_t kv_attention_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t D, int64_t bits, int64_t max_kv,
+                              int64_t max_q, int sms);
+cudaError_t launch_kv_attention(KvAttnParams p, int64_t D, int64_t bits, int64_t max_q, void* workspace,
+                                const LaunchEnv& env);
 cudaError_t launch_fp8_linear(const uint16_t* x, const uint8_t* qw, const float* sw, const uint16_t* bias,
                               uint16_t* y, uint8_t* qx, float* sx, int64_t M, int64_t N, int64_t K,
                               const LaunchEnv& env);
