@@ -4,35 +4,40 @@
 //
 //   a_j = c * sum_d q_d k_jd   (c = softmax scale * log2 e, j over the visible tokens)
 //   o_d = sum_j w_j v_jd / sum_j w_j,   w_j = 2^(a_j - max a)
-// with k_jd = low_j + s_j code_jd (and v the same), so that
-//   sum_d q_d k_jd = s_j sum_d q_d (code_jd + z) + (low_j - z s_j) sum_d q_d
-//   sum_j w_j v_jd = sum_j (w_j s_j) (code_jd + z) + sum_j w_j (low_j - z s_j)
-// for any z: the products run on the codes themselves (small integers, exact
-// in bf16) with the scales outside.  For keys z = 128 (4 bits: the biased
-// nibble in the mantissa of 128, no subtraction) or -128 (8 bits: the signed
-// byte); at most 8 MMA steps accumulate, so the shift costs no precision that
-// the logits would show (about 1e-4 of their unit).  For values the sum runs
-// over the whole context and z centres the codes (-8 or -128): left
-// uncentred, sums far larger than the result would cancel.
+// with k_jd = low_j + s_j code_jd (and v the same), so that with centred
+// codes c = code - z (z = 8 or 128)
+//   sum_d q_d k_jd = s_j sum_d q_d c_jd + (low_j + z s_j) sum_d q_d
+//   sum_j w_j v_jd = sum_j (w_j s_j) c_jd + sum_j w_j (low_j + z s_j):
+// the products run on the codes themselves (small integers, exact in fp16)
+// with the scales outside.  Centred, because sums of uncentred codes over a
+// long context would be far larger than the result that is left of them.
 //
-// Precision: logits, maxima, totals and accumulators in fp32; w_j s_j is
-// rounded to bf16 for the tensor cores (2^-9 relative and independent per
-// token, the same as any bf16 attention), q and the codes not at all.
+// Precision: logits, maxima, totals and accumulators in fp32.  fp16 holds q
+// exactly after a power of two per row has put its largest element near 2^8
+// (elements 2^32 times smaller round), and w_j s_j to 2^-11 after a power of
+// two S per warp, raised as larger scales appear, has put the largest
+// possible weight at 2^14: eight times finer than bf16, and weights down to
+// 2^-38 of the largest are kept.
 //
 // Bound by the bytes of the cache: 136 bytes a token and head (4 bits, 128
-// channels, K and V), against which a warp's unpacking is the next cost, so
-// the layout of the MMA operands is chosen to unpack with the fewest
-// instructions:
-//  * the 16-row A operand is the head group's queries (8 or 16 rows; a
-//    sequence with more rows takes several blocks), the tokens are N;
+// channels, K and V).  Against them stands the unpacking, which is bound by
+// the integer pipe (half rate), so the layout of the MMA operands is chosen
+// to unpack with the fewest integer instructions:
+//  * the cache is the 16-row A operand and the head group's queries are N (8
+//    rows, or twice 8; a sequence with more takes several blocks): single
+//    tokens of a group of up to 8 waste no MMA rows and no accumulators.
+//    Q K^T comes out as tokens x queries, and one transpose of 8 x 8 halves
+//    per 8 tokens makes it the B operand of P V;
+//  * fp16 rather than bf16: its 10-bit mantissa takes a nibble at bits 0-3 or
+//    4-7 as it lies (1024 + c, 1024 + 16 c), so a word of 8 codes needs one
+//    shift, and the subtraction runs on the other (half-precision) pipe;
 //  * the channel order of a sum over channels is free: a lane takes D / 4
-//    neighbouring channels of a key row, and pairs code i with code i + 4 (4
-//    bits) or i + 2 (8 bits), which one mask yields; q is permuted alike;
-//  * the token order of a sum over tokens is free too: values are paired
-//    across two rows by byte permutes, and P stays in the registers in which
-//    Q K^T left it;
-//  * lane g of a value operand holds D / 8 neighbouring channels, which are
-//    then 2 D / 8 neighbouring output channels of a lane.
+//    neighbouring channels of a key row, and pairs code i with code i + 4,
+//    which one mask yields (4 bits), or i + 1 (8 bits); q is permuted alike;
+//  * values are paired across two tokens by byte permutes, and a lane's
+//    channels of an output are neighbours (g D / 8 ..);
+//  * a lane turns the scale and low value of one token into the four factors
+//    the warp needs, and shares them through shared memory.
 // A block is four such warps over 32 tokens of a 128-token tile each, with
 // their own running maximum, and one warp that keeps 3 tiles of bulk copies
 // in flight (about 50 KB a block, three blocks an SM).
@@ -41,6 +46,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kv_schedule.cuh"
 #include "quant_math.cuh"
@@ -57,19 +63,19 @@ constexpr int kStages = 3;
 
 template <int D, int BITS, int ROWS>
 struct Cfg {
+    static constexpr int kBlocks = ROWS == 8 && BITS == 4 ? 3 : 2;  // resident blocks per SM
     static constexpr int kRowBytes = D * BITS / 8;
     static constexpr int kCodes = kTile * kRowBytes;
     static constexpr int kStageBytes = 2 * kCodes + 2 * kTile * 4;
-    // a merge row: D floats, 4 more after every lane's share (no bank conflicts)
-    static constexpr int kMergeRow = D + 16;
+    // a merge row: D floats, 4 more after every 32 (spreads a warp's stores over the banks)
+    static constexpr int kMergeRow = D + D / 8;
     static constexpr int kMergeBytes = 2 * ROWS * kMergeRow * 4;
     static constexpr int kSmem = kStages * kStageBytes + kMergeBytes;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -87,47 +93,89 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Pairs of bf16 from a word of codes: 4 bits: nibbles (j, j + 4) as 128 +
-// code; 8 bits: bytes (j, j + 2) as code - 128 (the low seven bits as 128 + u
-// plus -128 or -256, all exact).
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// The transpose of a warp's 8 x 8 matrix of halves (lane (g, t): row g, columns 2t and 2t + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// What is subtracted from a code.
 template <int BITS>
-__device__ __forceinline__ void unpack_biased(uint32_t w, uint32_t (&pair)[16 / BITS]) {
+constexpr float kCentre = BITS == 4 ? 8.0f : 128.0f;
+
+// (w & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
+}
+
+// Eight nibbles as four pairs of fp16 (nibbles j and j + 4), less 8: exact.
+__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&pair)[4]) {
+    const uint32_t u = w >> 8;
+    pair[0] = sub_f16x2(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);               // 1024 + c - 1032
+    pair[1] = fma_f16x2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // (1024 + 16 c) / 16 - 72
+    pair[2] = sub_f16x2(and_or(u, 0x000f000fu, 0x64006400u), 0x64086408u);
+    pair[3] = fma_f16x2(and_or(u, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+}
+
+// Two bytes as a pair of fp16, less 128: exact.
+__device__ __forceinline__ uint32_t unpack_bytes(uint32_t w, uint32_t select) {
+    return sub_f16x2(__byte_perm(w, 0x64646464u, select), 0x64806480u);  // 1024 + c - 1152
+}
+
+// A word of a key row as pairs along the channels: (j, j + 4) of 8 codes, or
+// (2j, 2j + 1) of 4.
+template <int BITS>
+__device__ __forceinline__ void unpack_key(uint32_t w, uint32_t (&pair)[16 / BITS]) {
     if constexpr (BITS == 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pair[j] = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+        unpack_nibbles(w, pair);
     } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t u = w >> (8 * j);
-            pair[j] = add_bf16x2((u & 0x007f007fu) | 0x43004300u, (u & 0x00800080u) ^ 0xc380c380u);
-        }
+        pair[0] = unpack_bytes(w, 0x5150);
+        pair[1] = unpack_bytes(w, 0x5352);
     }
 }
 
-// What unpack_biased adds to a code, and the same for centred codes.
+// Words of two value rows as pairs along the tokens, one per channel.
 template <int BITS>
-constexpr float kBiased = BITS == 4 ? 128.0f : -128.0f;
-template <int BITS>
-constexpr float kCentred = BITS == 4 ? -8.0f : -128.0f;
-
-template <int BITS>
-__device__ __forceinline__ void unpack_centred(uint32_t w, uint32_t (&pair)[16 / BITS]) {
-    unpack_biased<BITS>(w, pair);
+__device__ __forceinline__ void unpack_values(uint32_t a, uint32_t b, uint32_t (&pair)[32 / BITS]) {
     if constexpr (BITS == 4) {
+        uint32_t lo[4], hi[4];
+        unpack_nibbles(__byte_perm(a, b, 0x5410), lo);
+        unpack_nibbles(__byte_perm(a, b, 0x7632), hi);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pair[j] = sub_bf16x2(pair[j], 0x43084308u);  // 136
+        for (int j = 0; j < 4; ++j) {
+            pair[j] = lo[j];
+            pair[4 + j] = hi[j];
+        }
+    } else {
+        const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);  // a0 b0 a1 b1, a2 b2 a3 b3
+        pair[0] = unpack_bytes(lo, 0x5150);
+        pair[1] = unpack_bytes(lo, 0x5352);
+        pair[2] = unpack_bytes(hi, 0x5150);
+        pair[3] = unpack_bytes(hi, 0x5352);
     }
 }
 
@@ -162,13 +210,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
 template <int D, int BITS, int HALVES>
-__global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv_attention_kernel(const KvAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
+    kv_attention_kernel(const KvAttnParams p) {
     constexpr int ROWS = 8 * HALVES;
     using C = Cfg<D, BITS, ROWS>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ KvLocate locate;
+    __shared__ KvCursor cursors[kWarps];  // (kept out of the registers of the main loop)
+    __shared__ KvRange range;
     __shared__ float merge_ml[kWarps][ROWS][2];
+    __shared__ float4 factors[kWarps][kWarpTokens];  // of a token: K scale and offset, V scale and offset
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -182,13 +234,14 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
     }
     pdl_wait();
     pdl_launch_dependents();
-    KvCursor c;
-    const KvRange range = kv_locate<ROWS, kTile, kThreads>(p, locate, c);  // (its barriers also publish the mbarriers)
-    int64_t left = range.end - range.begin;
     int stage = 0;
     uint32_t parity = 0;
+    KvCursor start;
+    const KvRange found = kv_locate<ROWS, kTile, kThreads>(p, locate, start);  // (its barriers also publish the mbarriers)
 
     if (warp == kWarps) {
+        KvCursor& c = start;
+        int64_t left = found.end - found.begin;
         // ---------------------------------------------------------- producer
         // One lane per copy: four arrays (K and V codes and params) of up to
         // eight pieces of a tile (a piece is a page, or the tile's part of one).
@@ -202,12 +255,24 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
         bool ok = true;
         while (left > 0 && ok) {
             const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+            const int32_t* table = p.table + c.b * p.table_width;
+            const int first = (c.span.first + c.tile) * kTile + at;  // this lane's token of the item's next tile
+            auto needed = [&](int i) {
+                const int token = first + i * kTile;
+                return i < n && at < kTile && token < c.span.end && token + piece > c.span.begin;
+            };
+            // pages are looked up two tiles ahead, so that no copy waits for its address
+            int32_t ahead[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ahead[i] = needed(i) ? __ldg(table + ((first + i * kTile) >> p.cache.page_shift)) : 0;
             for (int i = 0; i < n && ok; ++i) {
-                const int token = (c.span.first + c.tile + i) * kTile + at;
-                const bool need = at < kTile && token < c.span.end && token + piece > c.span.begin;
+                const int token = first + i * kTile;
+                const bool need = needed(i);
+                int64_t page = ahead[0];
+                ahead[0] = ahead[1];
+                ahead[1] = needed(i + 2) ? __ldg(table + ((token + 2 * kTile) >> p.cache.page_shift)) : 0;
                 const uint8_t* src = nullptr;
                 if (need) {
-                    int64_t page = __ldg(p.table + c.b * p.table_width + (token >> p.cache.page_shift));
                     if (page < 0 || page >= p.cache.pages) {
                         record_fault(p.err, kErrBitBadIndex);
                         page = 0;
@@ -229,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
                 }
             }
             left -= n;
-            c.tile += n - 1;
             kv_next_item<ROWS, kTile>(p, c);
         }
         if (!ok) {
@@ -250,199 +314,259 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
     // -------------------------------------------------------------- consumers
     constexpr int kKeyWords = D * BITS / 128;     // words of a key row per lane
     constexpr int kValWords = D * BITS / 256;     // words of a value row per lane
-    constexpr int kOut = D / 8;                   // n-tiles of the output: channels per lane of a value row
+    constexpr int kOut = D / 16;                  // 16-channel tiles of the output
     constexpr int kPairs = 16 / BITS;             // pairs per word
     constexpr int kSteps = D / 16;
     const int g = lane / 4, t = lane % 4;
-    const int key_row = g ^ ((g >> 1) & 1);  // the token of column g: rows of both parities in every load (banks)
-    const int tok0 = (2 * t) ^ (t & 1), tok1 = (2 * t + 1) ^ (t & 1);  // the tokens of columns 2t and 2t + 1
+    const int row_g = g ^ ((g >> 1) & 1);  // the token of row g (of 8): rows of both parities in every load (banks)
+    const int tok0 = (2 * t) ^ (t & 1), tok1 = (2 * t + 1) ^ (t & 1);  // the same for rows 2t and 2t + 1
     float* merge = reinterpret_cast<float*>(smem + kStages * C::kStageBytes);
 
-    int split_rows = 0;
-    while (left > 0) {
-        const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+    KvCursor& c = cursors[warp];
+    if (lane == 0) c = start;
+    if (threadIdx.x == 0) range = found;
+    consumer_sync();
+    int64_t done = 0;
+    bool split = false;
+    while (done < range.end - range.begin) {
+        const int n = (int)min(range.end - range.begin - done, (int64_t)(c.span.tiles - c.tile));
         const int row0 = c.rb * ROWS;
         const int rows = min(ROWS, c.seq.nq * p.G - row0);
         const int base = c.seq.len - c.seq.nq;
-        // this lane's rows of Q (A operand), permuted as the keys' unpacking pairs channels
-        uint32_t qf[kSteps][2 * HALVES];
-        float q_sum[HALVES];
-        int hi[HALVES], lo[HALVES];  // the tokens a row sees: lo .. hi
+        // this lane's rows of Q (B operand: rows g, g + 8), permuted as the
+        // keys' unpacking pairs channels, times 2^8 / (the power of two below
+        // the row's largest element)
+        uint32_t qf[kSteps][HALVES][2];
+        // of the rows 2t and 2t + 1 (+ 8), whose logits the lane holds:
+        float q_sum[HALVES][2];   // the scaled row's sum
+        float q_unit[HALVES][2];  // what a scaled logit counts, in log2 units
+        int hi[HALVES][2], lo[HALVES][2];  // the tokens the row sees: lo .. hi
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) {
             const int r = g + 8 * x;
             const bool live = r < rows;
             const int i = (row0 + (live ? r : 0)) / p.G;
             const int head = c.h * p.G + (row0 + (live ? r : 0)) - i * p.G;
-            hi[x] = live ? base + i : INT32_MAX;
-            lo[x] = live && p.window > 0 ? (int)max(base + i + 1 - p.window, (int64_t)0) : 0;
             const uint4* src = reinterpret_cast<const uint4*>(p.q + (c.seq.q0 + i) * p.q_stride + (int64_t)head * D +
                                                               t * (D / 4));
+            uint4 v[D / 32];
+            uint32_t top = 0;  // largest finite magnitude, as bits
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                v[w] = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                const uint32_t words[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
+                    top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+                }
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max((int)(top >> 23), 9) - 127;
+            const float f = pow2(8 - e);
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
-                const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                sum += ((lo_bf16(v.x) + hi_bf16(v.x)) + (lo_bf16(v.y) + hi_bf16(v.y))) +
-                       ((lo_bf16(v.z) + hi_bf16(v.z)) + (lo_bf16(v.w) + hi_bf16(v.w)));
-                uint32_t (&f0)[2 * HALVES] = qf[2 * w], (&f1)[2 * HALVES] = qf[2 * w + 1];
+                const float y[8] = {lo_bf16(v[w].x) * f, hi_bf16(v[w].x) * f, lo_bf16(v[w].y) * f, hi_bf16(v[w].y) * f,
+                                    lo_bf16(v[w].z) * f, hi_bf16(v[w].z) * f, lo_bf16(v[w].w) * f, hi_bf16(v[w].w) * f};
+                sum += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+                uint32_t (&f0)[2] = qf[2 * w][x], (&f1)[2] = qf[2 * w + 1][x];
                 if constexpr (BITS == 4) {  // 8 channels: (0,4) (1,5) | (2,6) (3,7)
-                    f0[x] = __byte_perm(v.x, v.z, 0x5410);
-                    f0[HALVES + x] = __byte_perm(v.x, v.z, 0x7632);
-                    f1[x] = __byte_perm(v.y, v.w, 0x5410);
-                    f1[HALVES + x] = __byte_perm(v.y, v.w, 0x7632);
-                } else {  // twice 4 channels: (0,2) (1,3)
-                    f0[x] = __byte_perm(v.x, v.y, 0x5410);
-                    f0[HALVES + x] = __byte_perm(v.x, v.y, 0x7632);
-                    f1[x] = __byte_perm(v.z, v.w, 0x5410);
-                    f1[HALVES + x] = __byte_perm(v.z, v.w, 0x7632);
+                    f0[0] = pack_f16(y[0], y[4]);
+                    f0[1] = pack_f16(y[1], y[5]);
+                    f1[0] = pack_f16(y[2], y[6]);
+                    f1[1] = pack_f16(y[3], y[7]);
+                } else {  // twice 4 channels: (0,1) (2,3)
+                    f0[0] = pack_f16(y[0], y[1]);
+                    f0[1] = pack_f16(y[2], y[3]);
+                    f1[0] = pack_f16(y[4], y[5]);
+                    f1[1] = pack_f16(y[6], y[7]);
                 }
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            q_sum[x] = sum * p.scale_log2;
+            const float unit = pow2(e - 8) * p.scale_log2;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int from = 4 * (2 * t + y);  // a lane that loaded row 2t + y
+                q_sum[x][y] = __shfl_sync(0xffffffffu, sum, from);
+                q_unit[x][y] = __shfl_sync(0xffffffffu, unit, from);
+                const int j = __shfl_sync(0xffffffffu, i, from);
+                const bool there = 8 * x + 2 * t + y < rows;
+                hi[x][y] = there ? base + j : INT32_MAX;
+                lo[x][y] = there && p.window > 0 ? (int)max(base + j + 1 - p.window, (int64_t)0) : 0;
+            }
         }
         // tokens [all_lo, all_hi] are seen by every row
         const int all_hi = base + row0 / p.G;
         const int all_lo = p.window > 0 ? (int)max(base + (row0 + rows - 1) / p.G + 1 - p.window, (int64_t)0) : 0;
 
-        float o[kOut][4];
-#pragma unroll
-        for (int i = 0; i < kOut; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m[HALVES], l[HALVES], z[HALVES];  // running maximum; this lane's share of the total and of sum w (low - z s)
+        // O^T: channels g D/8 + 2i (+ 1) x rows 2t, 2t + 1 (+ 8)
+        float o[kOut][HALVES][4];
+        // running maximum; this lane's share of the total and of sum w (low + z s)
+        float m[HALVES][2], l[HALVES][2], z[HALVES][2];
+        int unit = 14;  // S = 2^(unit - 126) is above every value scale so far
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) {
-            m[x] = -INFINITY;
-            l[x] = z[x] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) o[i][x][0] = o[i][x][1] = o[i][x][2] = o[i][x][3] = 0.0f;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                m[x][y] = -INFINITY;
+                l[x][y] = z[x][y] = 0.0f;
+            }
         }
+
+        // One warp's 32 tokens of a stage.  EDGE: some row does not see some of them.
+        auto step = [&](const uint8_t* st, int token, auto edge_tag) {
+            constexpr bool EDGE = decltype(edge_tag)::value;
+            // this lane's token: its scales and low values
+            {
+                const uint32_t* params = reinterpret_cast<const uint32_t*>(st + 2 * C::kCodes) + warp * kWarpTokens + lane;
+                uint32_t pk = params[0], pv = params[kTile];
+                if (EDGE && (token + lane >= c.span.end || token + lane < c.span.begin)) pk = pv = 0;  // may be anything
+                const float ks = kv_scale(pk), vs = kv_scale(pv);
+                const uint32_t bits = __float_as_uint(vs);
+                const int e = (int)(__reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u) >> 23);
+                if (e > unit) {
+                    const float f = e - unit > 126 ? 0.0f : pow2(unit - e);
+                    unit = e;
+#pragma unroll
+                    for (int j = 0; j < kOut; ++j)
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) o[j][x][y] *= f;
+                }
+                factors[warp][lane] = make_float4(ks, fmaf(ks, kCentre<BITS>, kv_low(pk)), vs * pow2(140 - unit),
+                                                  fmaf(vs, kCentre<BITS>, kv_low(pv)));
+                __syncwarp();
+            }
+            // logits: s[i]: tokens row_g + 16 i (+ 8) x rows 2t, 2t + 1
+            float s[2][HALVES][4];
+            const uint8_t* keys = st + (warp * kWarpTokens + row_g) * C::kRowBytes + t * (kKeyWords * 4);
+            uint32_t kw[4][kKeyWords];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds<kKeyWords>(keys + i * 8 * C::kRowBytes, kw[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x) s[i][x][0] = s[i][x][1] = s[i][x][2] = s[i][x][3] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kKeyWords; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t a[kPairs], b[kPairs];
+                    unpack_key<BITS>(kw[2 * i][k], a);
+                    unpack_key<BITS>(kw[2 * i + 1][k], b);
+#pragma unroll
+                    for (int j = 0; j < kPairs; j += 2)
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x) {
+                            const uint32_t (&q)[2] = qf[(k * kPairs + j) / 2][x];
+                            mma_f16(s[i][x], a[j], b[j], a[j + 1], b[j + 1], q[0], q[1]);
+                        }
+                }
+            float top[HALVES][2];
+            float4 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = factors[warp][row_g + 8 * i];
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    top[x][y] = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& a = s[i / 2][x][2 * (i & 1) + y];
+                        a = fmaf(a, f[i].x, f[i].y * q_sum[x][y]) * q_unit[x][y];
+                        const int tok = token + row_g + 8 * i;
+                        if (EDGE && (tok > hi[x][y] || tok < lo[x][y])) a = -INFINITY;
+                        top[x][y] = fmaxf(top[x][y], a);
+                    }
+                }
+            // softmax weights against the running maximum
+            bool grew = false;
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) top[x][y] = fmaxf(top[x][y], __shfl_xor_sync(0xffffffffu, top[x][y], k));
+                    grew |= top[x][y] > m[x][y];
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float to = fmaxf(m[x][y], top[x][y]);
+                        const float by = to == -INFINITY ? 1.0f : exp2_approx(m[x][y] - to);
+                        m[x][y] = to;
+                        l[x][y] *= by;
+                        z[x][y] *= by;
+#pragma unroll
+                        for (int j = 0; j < kOut; ++j) {
+                            o[j][x][y] *= by;
+                            o[j][x][2 + y] *= by;
+                        }
+                    }
+            }
+            uint32_t pr[4][HALVES];  // P^T as B operand: tokens of rows 2t, 2t + 1 (+ 8 i) x row g
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x) {
+                float shift[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) shift[y] = m[x][y] == -INFINITY ? 0.0f : m[x][y];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float wgt[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float a = s[i / 2][x][2 * (i & 1) + y];
+                        const float w = exp2_approx(a - shift[y]);
+                        l[x][y] += w;
+                        // a token a row does not see may hold anything: no product with it
+                        const bool skip = EDGE && a == -INFINITY;
+                        z[x][y] = skip ? z[x][y] : fmaf(w, f[i].w, z[x][y]);
+                        wgt[y] = skip ? 0.0f : w * f[i].z;
+                    }
+                    pr[i][x] = transpose8(pack_f16(wgt[0], wgt[1]));
+                }
+            }
+            // o += (w s 2^14 / S) (codes of V)
+            const uint8_t* vals = st + C::kCodes + warp * kWarpTokens * C::kRowBytes + g * (kValWords * 4);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[4][kValWords];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    lds<kValWords>(vals + (16 * half + 8 * (r >> 1) + ((r & 1) ? tok1 : tok0)) * C::kRowBytes, v[r]);
+#pragma unroll
+                for (int k = 0; k < kValWords; ++k) {
+                    uint32_t a[2 * kPairs], b[2 * kPairs];
+                    unpack_values<BITS>(v[0][k], v[1][k], a);
+                    unpack_values<BITS>(v[2][k], v[3][k], b);
+#pragma unroll
+                    for (int j = 0; j < 2 * kPairs; j += 2)
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x)
+                            mma_f16(o[k * kPairs + j / 2][x], a[j], a[j + 1], b[j], b[j + 1], pr[2 * half][x],
+                                    pr[2 * half + 1][x]);
+                }
+            }
+        };
 
         for (int i = 0; i < n; ++i) {
             const bool ok = tc::warp_wait(&full[stage], parity, &abort_flag, p.err);
             const uint8_t* st = smem + stage * C::kStageBytes;
             const int token = (c.span.first + c.tile + i) * kTile + warp * kWarpTokens;
             if (ok) {
-                // logits
-                float s[4][4];
-                const uint8_t* keys = st + (warp * kWarpTokens + key_row) * C::kRowBytes + t * (kKeyWords * 4);
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    uint32_t w[kKeyWords];
-                    lds<kKeyWords>(keys + nt * 8 * C::kRowBytes, w);
-                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kKeyWords; ++k) {
-                        uint32_t b[kPairs];
-                        unpack_biased<BITS>(w[k], b);
-#pragma unroll
-                        for (int j = 0; j < kPairs; j += 2) {
-                            const uint32_t (&a)[2 * HALVES] = qf[(k * kPairs + j) / 2];
-                            if constexpr (HALVES == 1)
-                                mma_bf16(s[nt], a[0], 0u, a[1], 0u, b[j], b[j + 1]);
-                            else
-                                mma_bf16(s[nt], a[0], a[1], a[2], a[3], b[j], b[j + 1]);
-                        }
-                    }
-                }
-                const uint32_t* kp = reinterpret_cast<const uint32_t*>(st + 2 * C::kCodes) + warp * kWarpTokens;
-                float top[HALVES];
-#pragma unroll
-                for (int x = 0; x < HALVES; ++x) top[x] = -INFINITY;
-                const bool edge = token + kWarpTokens - 1 > all_hi || token < all_lo;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int tok = 8 * nt + (e ? tok1 : tok0);
-                        const uint32_t param = kp[tok];
-                        const float ks = kv_scale(param);
-                        const float off = fmaf(ks, -kBiased<BITS>, kv_low(param));
-                        const float kc = ks * p.scale_log2;
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) {
-                            float a = fmaf(s[nt][2 * x + e], kc, off * q_sum[x]);
-                            if (edge && (token + tok > hi[x] || token + tok < lo[x])) a = -INFINITY;
-                            s[nt][2 * x + e] = a;
-                            top[x] = fmaxf(top[x], a);
-                        }
-                    }
-                // softmax weights against the running maximum
-                bool grew = false;
-                float shift[HALVES];
-#pragma unroll
-                for (int x = 0; x < HALVES; ++x) {
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-                    grew |= top[x] > m[x];
-                }
-                if (__any_sync(0xffffffffu, grew)) {
-                    float f[HALVES];
-#pragma unroll
-                    for (int x = 0; x < HALVES; ++x) {
-                        const float to = fmaxf(m[x], top[x]);
-                        f[x] = to == -INFINITY ? 1.0f : exp2_approx(m[x] - to);
-                        m[x] = to;
-                        l[x] *= f[x];
-                        z[x] *= f[x];
-                    }
-#pragma unroll
-                    for (int j = 0; j < kOut; ++j)
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) {
-                            o[j][2 * x] *= f[x];
-                            o[j][2 * x + 1] *= f[x];
-                        }
-                }
-#pragma unroll
-                for (int x = 0; x < HALVES; ++x) shift[x] = m[x] == -INFINITY ? 0.0f : m[x];
-                const uint32_t* vp = kp + kTile;
-                uint32_t pr[4][HALVES];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    float wgt[2][HALVES];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t param = vp[8 * nt + (e ? tok1 : tok0)];
-                        const float vs = kv_scale(param);
-                        const float off = fmaf(vs, -kCentred<BITS>, kv_low(param));
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) {
-                            const float a = s[nt][2 * x + e];
-                            const float w = exp2_approx(a - shift[x]);
-                            l[x] += w;
-                            // a token a row does not see may hold anything: no product with it
-                            const bool skip = edge && a == -INFINITY;
-                            z[x] = skip ? z[x] : fmaf(w, off, z[x]);
-                            wgt[e][x] = skip ? 0.0f : w * vs;
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < HALVES; ++x) pr[nt][x] = pack_bf16(wgt[0][x], wgt[1][x]);
-                }
-                // o += (w s) (codes of V)
-                const uint8_t* vals = st + C::kCodes + warp * kWarpTokens * C::kRowBytes + g * (kValWords * 4);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t v[4][kValWords];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        lds<kValWords>(vals + (16 * half + 8 * (r >> 1) + ((r & 1) ? tok1 : tok0)) * C::kRowBytes, v[r]);
-#pragma unroll
-                    for (int k = 0; k < kValWords; ++k)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t b0[kPairs], b1[kPairs];
-                            unpack_centred<BITS>(__byte_perm(v[0][k], v[1][k], y ? 0x7632 : 0x5410), b0);
-                            unpack_centred<BITS>(__byte_perm(v[2][k], v[3][k], y ? 0x7632 : 0x5410), b1);
-#pragma unroll
-                            for (int j = 0; j < kPairs; ++j) {
-                                float (&acc)[4] = o[(2 * k + y) * kPairs + j];
-                                const uint32_t (&a)[HALVES] = pr[2 * half], (&b)[HALVES] = pr[2 * half + 1];
-                                if constexpr (HALVES == 1)
-                                    mma_bf16(acc, a[0], 0u, b[0], 0u, b0[j], b1[j]);
-                                else
-                                    mma_bf16(acc, a[0], a[1], b[0], b[1], b0[j], b1[j]);
-                            }
-                        }
-                }
+                if (token + kWarpTokens - 1 > all_hi || token < all_lo)
+                    step(st, token, std::true_type{});
+                else
+                    step(st, token, std::false_type{});
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[stage]);
@@ -454,42 +578,47 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
 
         // join the four warps: totals over the lanes of a row, then one common maximum
 #pragma unroll
-        for (int x = 0; x < HALVES; ++x) {
+        for (int x = 0; x < HALVES; ++x)
 #pragma unroll
-            for (int k = 1; k < 4; k <<= 1) {
-                l[x] += __shfl_xor_sync(0xffffffffu, l[x], k);
-                z[x] += __shfl_xor_sync(0xffffffffu, z[x], k);
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) {
+                    l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], k);
+                    z[x][y] += __shfl_xor_sync(0xffffffffu, z[x][y], k);
+                }
+                if (g == 0) {
+                    merge_ml[warp][8 * x + 2 * t + y][0] = m[x][y];
+                    merge_ml[warp][8 * x + 2 * t + y][1] = l[x][y];
+                }
             }
-            if (t == 0) {
-                merge_ml[warp][g + 8 * x][0] = m[x];
-                merge_ml[warp][g + 8 * x][1] = l[x];
-            }
-        }
         consumer_sync();
 #pragma unroll
-        for (int x = 0; x < HALVES; ++x) {
-            float top = merge_ml[0][g + 8 * x][0];
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][g + 8 * x][0]);
-            const float f = m[x] == -INFINITY ? 0.0f : exp2_approx(m[x] - top);
+        for (int x = 0; x < HALVES; ++x)
 #pragma unroll
-            for (int j = 0; j < kOut; ++j) {
-                o[j][2 * x] = f == 0.0f ? 0.0f : (o[j][2 * x] + z[x]) * f;
-                o[j][2 * x + 1] = f == 0.0f ? 0.0f : (o[j][2 * x + 1] + z[x]) * f;
+            for (int y = 0; y < 2; ++y) {
+                const int r = 8 * x + 2 * t + y;
+                float top = merge_ml[0][r][0];
+                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][r][0]);
+                const float f = m[x][y] == -INFINITY ? 0.0f : exp2_approx(m[x][y] - top);
+#pragma unroll
+                for (int j = 0; j < kOut; ++j)
+#pragma unroll
+                    for (int k = y; k < 4; k += 2)
+                        o[j][x][k] = f == 0.0f ? 0.0f : fmaf(o[j][x][k], pow2(unit - 140), z[x][y]) * f;
             }
-        }
-        // lane (g, t) holds channels 2t D/8 .. (2t + 2) D/8 of rows g and g + 8
-        float* mine = merge + (warp & 1) * ROWS * C::kMergeRow + g * C::kMergeRow + t * (2 * kOut + 4);
+        // a lane holds D / 8 channels from g D / 8 on of rows 2t and 2t + 1 (+ 8)
+        const int at = g * (D / 8) + 4 * (g * (D / 8) / 32);
         for (int turn = 0; turn < 2; ++turn) {
             if (warp / 2 == 1 - turn) {
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int j = 0; j < kOut; j += 4) {
-                            float4* dst = reinterpret_cast<float4*>(mine + 8 * x * C::kMergeRow + e * kOut + j);
-                            float4 v = make_float4(o[j][2 * x + e], o[j + 1][2 * x + e], o[j + 2][2 * x + e],
-                                                   o[j + 3][2 * x + e]);
+                        for (int j = 0; j < kOut; j += 2) {
+                            float4* dst = reinterpret_cast<float4*>(
+                                merge + ((warp & 1) * ROWS + 8 * x + 2 * t + y) * C::kMergeRow + at + 2 * j);
+                            float4 v = make_float4(o[j][x][y], o[j][x][2 + y], o[j + 1][x][y], o[j + 1][x][2 + y]);
                             if (turn == 1) {
                                 const float4 u = *dst;
                                 v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
@@ -505,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
         if (store) {
             for (int k = tid; k < rows * (D / 8); k += kWarps * 32) {
                 const int r = k / (D / 8), d = (k % (D / 8)) * 8;
-                const float* src = merge + r * C::kMergeRow + d + 4 * (d / (2 * kOut));
+                const float* src = merge + r * C::kMergeRow + d + 4 * (d / 32);
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
@@ -537,27 +666,25 @@ __global__ void __launch_bounds__(kThreads, HALVES == 1 && BITS == 4 ? 3 : 2) kv
                 }
             }
             if (begins && !ends) {
-                split_rows = rows;
+                split = true;
                 if (tid == 0) {
                     KvSplitItem it;
                     it.q_row = c.seq.q0;
                     it.row0 = row0;
                     it.rows = rows;
                     it.h = c.h;
-                    it.last_cta = kv_owner(range.total, range.ctas, range.end - left + c.span.tiles - 1);
+                    it.last_cta = kv_owner(range.total, range.ctas, range.begin + done + c.span.tiles - 1);
                     it.pad = 0;
                     p.split[blockIdx.x] = it;
                 }
             }
         }
-        left -= n;
-        if (left > 0) {
-            c.tile += n - 1;
-            kv_next_item<ROWS, kTile>(p, c);
-            consumer_sync();  // the merge rows are free again
-        }
+        done += n;
+        __syncwarp();
+        if (lane == 0) kv_next_item<ROWS, kTile>(p, c);
+        consumer_sync();  // the cursor is at the next item, and the merge rows are free again
     }
-    if (threadIdx.x == 0 && p.split != nullptr && split_rows == 0) p.split[blockIdx.x].rows = 0;
+    if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
 }
 
 // Joins the parts of an item cut between CTAs, in their order: a group of
