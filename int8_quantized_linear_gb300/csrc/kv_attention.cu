@@ -48,9 +48,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "kv_schedule.cuh"
-#include "quant_math.cuh"
-#include "tc_common.cuh"
+#include "kv_math.cuh"
 
 namespace i8ql {
 namespace {
@@ -60,6 +58,7 @@ constexpr int kWarps = 4;                    // consumer warps
 constexpr int kWarpTokens = kTile / kWarps;  // tokens of a stage per warp
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kStages = 3;
+constexpr int64_t kFewRows = 32;  // query rows of a sequence's head group up to which this kernel runs
 
 template <int D, int BITS, int ROWS>
 struct Cfg {
@@ -81,130 +80,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-
 // The transpose of a warp's 8 x 8 matrix of halves (lane (g, t): row g, columns 2t and 2t + 1).
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
-}
-
-// 2^e for -126 <= e <= 127.
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// What is subtracted from a code.
-template <int BITS>
-constexpr float kCentre = BITS == 4 ? 8.0f : 128.0f;
-
-// (w & mask) | bits in one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
-    return r;
-}
-
-// Eight nibbles as four pairs of fp16 (nibbles j and j + 4), less 8: exact.
-__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&pair)[4]) {
-    const uint32_t u = w >> 8;
-    pair[0] = sub_f16x2(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);               // 1024 + c - 1032
-    pair[1] = fma_f16x2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // (1024 + 16 c) / 16 - 72
-    pair[2] = sub_f16x2(and_or(u, 0x000f000fu, 0x64006400u), 0x64086408u);
-    pair[3] = fma_f16x2(and_or(u, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
-}
-
-// Two bytes as a pair of fp16, less 128: exact.
-__device__ __forceinline__ uint32_t unpack_bytes(uint32_t w, uint32_t select) {
-    return sub_f16x2(__byte_perm(w, 0x64646464u, select), 0x64806480u);  // 1024 + c - 1152
-}
-
-// A word of a key row as pairs along the channels: (j, j + 4) of 8 codes, or
-// (2j, 2j + 1) of 4.
-template <int BITS>
-__device__ __forceinline__ void unpack_key(uint32_t w, uint32_t (&pair)[16 / BITS]) {
-    if constexpr (BITS == 4) {
-        unpack_nibbles(w, pair);
-    } else {
-        pair[0] = unpack_bytes(w, 0x5150);
-        pair[1] = unpack_bytes(w, 0x5352);
-    }
-}
-
-// Words of two value rows as pairs along the tokens, one per channel.
-template <int BITS>
-__device__ __forceinline__ void unpack_values(uint32_t a, uint32_t b, uint32_t (&pair)[32 / BITS]) {
-    if constexpr (BITS == 4) {
-        uint32_t lo[4], hi[4];
-        unpack_nibbles(__byte_perm(a, b, 0x5410), lo);
-        unpack_nibbles(__byte_perm(a, b, 0x7632), hi);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            pair[j] = lo[j];
-            pair[4 + j] = hi[j];
-        }
-    } else {
-        const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);  // a0 b0 a1 b1, a2 b2 a3 b3
-        pair[0] = unpack_bytes(lo, 0x5150);
-        pair[1] = unpack_bytes(lo, 0x5352);
-        pair[2] = unpack_bytes(hi, 0x5150);
-        pair[3] = unpack_bytes(hi, 0x5352);
-    }
-}
-
-// N words from shared memory (N = 1, 2 or a multiple of 4; aligned to min(N, 4) words).
-template <int N>
-__device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[N]) {
-    if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
-            w[i] = v.x;
-            w[i + 1] = v.y;
-            w[i + 2] = v.z;
-            w[i + 3] = v.w;
-        }
-    }
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     tc::smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-                 : "memory");
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
@@ -299,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
         if (!ok) {
             // giving up: let the copies in flight land before the block's
             // shared memory can go to another
-            int none = 0;
             for (int i = 0; i < min(issued, kStages); ++i) {
+                int none = 0;
                 if (--stage < 0) {
                     stage = kStages - 1;
                     parity ^= 1;
@@ -599,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                 const int r = 8 * x + 2 * t + y;
                 float top = merge_ml[0][r][0];
                 for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][r][0]);
-                const float f = m[x][y] == -INFINITY ? 0.0f : exp2_approx(m[x][y] - top);
+                const float f = l[x][y] == 0.0f ? 0.0f : exp2_approx(m[x][y] - top);  // (0: saw nothing)
 #pragma unroll
                 for (int j = 0; j < kOut; ++j)
 #pragma unroll
@@ -649,11 +529,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                 for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][r][0]);
                 float total = 0.0f;
                 for (int w = 0; w < kWarps; ++w)
-                    total += merge_ml[w][r][0] == -INFINITY ? 0.0f : merge_ml[w][r][1] * exp2_approx(merge_ml[w][r][0] - top);
+                    total += merge_ml[w][r][1] == 0.0f ? 0.0f : merge_ml[w][r][1] * exp2_approx(merge_ml[w][r][0] - top);
                 if (begins && ends) {
                     const int i = (row0 + r) / p.G;
                     const int head = c.h * p.G + row0 + r - i * p.G;
-                    const float inv = top == -INFINITY ? 0.0f : 1.0f / total;
+                    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
                     *reinterpret_cast<uint4*>(p.out + ((c.seq.q0 + i) * ((int64_t)p.cache.H * p.G) + head) * D + d) =
                         make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
                                    pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
@@ -693,14 +573,14 @@ constexpr int kJoinWarps = 32;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnParams p) {
-    constexpr int kPer = kJoinWarps / ROWS;  // warps per row
+    constexpr int kPer = ROWS < kJoinWarps ? kJoinWarps / ROWS : 1;  // warps per row
     constexpr int kVec = D / 32;             // channels per lane
     __shared__ float part[kJoinWarps][D];
     pdl_wait();
     const KvSplitItem it = p.split[blockIdx.x];
     if (it.rows == 0) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int r = warp / kPer, sub = warp % kPer;
+    const int r = blockIdx.y * kJoinWarps + warp / kPer, sub = warp % kPer;
     const int first = blockIdx.x, count = it.last_cta - first + 1;
     // part k: the beginning (slot 1 of the first CTA), then slot 0 of the following ones
     auto slot = [&](int k) { return ((int64_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r; };
@@ -709,28 +589,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnPa
         for (int k = lane; k < count; k += 32) top = fmaxf(top, p.part_ml[slot(k) * 2]);
 #pragma unroll
         for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        if (top != -INFINITY) {
-            for (int k = lane; k < count; k += 32) {
-                const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2);
-                total += ml.y * exp2_approx(ml.x - top);
-            }
+        // a part's weight; 0 where it saw nothing
+        auto weight = [&](float2 ml) { return ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - top); };
+        for (int k = lane; k < count; k += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2);
+            total += ml.y * weight(ml);
+        }
 #pragma unroll
-            for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
 #pragma unroll 4
-            for (int k = sub; k < count; k += kPer) {
-                const float f = exp2_approx(p.part_ml[slot(k) * 2] - top);
-                const float* src = p.part_o + slot(k) * D + lane * kVec;
-                if constexpr (kVec == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    acc[0] = fmaf(v.x, f, acc[0]);
-                    acc[1] = fmaf(v.y, f, acc[1]);
-                    acc[2] = fmaf(v.z, f, acc[2]);
-                    acc[3] = fmaf(v.w, f, acc[3]);
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    acc[0] = fmaf(v.x, f, acc[0]);
-                    acc[1] = fmaf(v.y, f, acc[1]);
-                }
+        for (int k = sub; k < count; k += kPer) {
+            const float f = weight(*reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2));
+            const float* src = p.part_o + slot(k) * D + lane * kVec;
+            if constexpr (kVec == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                acc[2] = fmaf(v.z, f, acc[2]);
+                acc[3] = fmaf(v.w, f, acc[3]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
             }
         }
     }
@@ -738,7 +618,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnPa
     for (int i = 0; i < kVec; ++i) part[warp][lane * kVec + i] = acc[i];
     __syncthreads();
     if (sub != 0 || r >= it.rows) return;
-    const float inv = top == -INFINITY ? 0.0f : 1.0f / total;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const int i = (it.row0 + r) / p.G;
     const int head = it.h * p.G + it.row0 + r - i * p.G;
     uint16_t* dst = p.out + ((it.q_row + i) * ((int64_t)p.cache.H * p.G) + head) * D + lane * kVec;
@@ -755,21 +635,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnPa
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0], v[1]);
 }
 
-// How a call runs: rows per block and the number of CTAs.
+template <int D, int ROWS>
+cudaError_t launch_join(const KvAttnParams& p, int64_t ctas, const LaunchEnv& env) {
+    return launch_kernel(kv_join_kernel<D, ROWS>, dim3((unsigned)ctas, std::max(ROWS / kJoinWarps, 1)),
+                         dim3(kJoinWarps * 32), 0, env.stream, kNoCluster, p);
+}
+
+// How a call runs: the query rows of a block, the CTAs, and whether an item
+// may be cut between CTAs.
 struct Plan {
-    int halves;
+    int rows;
     int64_t ctas;
-    bool split;  // an item may be cut between CTAs
+    bool split;
 };
 
 Plan make_plan(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int64_t bits, int sms) {
     Plan pl;
-    pl.halves = max_q * G <= 8 ? 1 : 2;
-    const int64_t rows = 8 * pl.halves;
-    const int64_t per_sm = pl.halves == 1 && bits == 4 ? 3 : 2;
+    pl.rows = max_q * G <= 8 ? 8 : max_q * G <= kFewRows ? 16 : kKvPromptRows;
+    const int64_t per_sm = pl.rows == kKvPromptRows ? 1 : pl.rows == 8 && bits == 4 ? 3 : 2;
     // no more CTAs than there can be tiles
-    const int64_t item_tiles = std::max<int64_t>((max_kv + kTile - 1) / kTile, 1);
-    const int64_t items = (T_q * G / rows + B) * H;
+    const int64_t tile = pl.rows == kKvPromptRows ? kKvPromptTile : kTile;
+    const int64_t item_tiles = std::max<int64_t>((max_kv + tile - 1) / tile, 1);
+    const int64_t items = (T_q * G / pl.rows + B) * H;
     pl.ctas = std::min<int64_t>(sms * per_sm, items > sms * per_sm ? sms * per_sm : items * item_tiles);
     pl.split = item_tiles > 1;
     return pl;
@@ -790,16 +677,22 @@ cudaError_t launch_form(const KvAttnParams& p, const Plan& pl, const LaunchEnv& 
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (set[dev & 63] != cudaSuccess) return set[dev & 63];
-    e = launch_kernel(kv_attention_kernel<D, BITS, HALVES>, dim3((unsigned)pl.ctas), dim3(kThreads), C::kSmem,
-                      env.stream, kNoCluster, p);
-    if (e != cudaSuccess || !pl.split) return e;
-    return launch_kernel(kv_join_kernel<D, 8 * HALVES>, dim3((unsigned)pl.ctas), dim3(kJoinWarps * 32), 0, env.stream,
-                         kNoCluster, p);
+    return launch_kernel(kv_attention_kernel<D, BITS, HALVES>, dim3((unsigned)pl.ctas), dim3(kThreads), C::kSmem,
+                         env.stream, kNoCluster, p);
 }
 
-template <int D, int BITS>
-cudaError_t launch_bits(const KvAttnParams& p, const Plan& pl, const LaunchEnv& env) {
-    return pl.halves == 1 ? launch_form<D, BITS, 1>(p, pl, env) : launch_form<D, BITS, 2>(p, pl, env);
+template <int D>
+cudaError_t launch_dim(const KvAttnParams& p, int64_t bits, const Plan& pl, const LaunchEnv& env) {
+    cudaError_t e;
+    if (pl.rows == kKvPromptRows)
+        e = launch_kv_prompt(p, D, bits, pl.ctas, env);
+    else if (bits == 4)
+        e = pl.rows == 8 ? launch_form<D, 4, 1>(p, pl, env) : launch_form<D, 4, 2>(p, pl, env);
+    else
+        e = pl.rows == 8 ? launch_form<D, 8, 1>(p, pl, env) : launch_form<D, 8, 2>(p, pl, env);
+    if (e != cudaSuccess || !pl.split) return e;
+    if (pl.rows == kKvPromptRows) return launch_join<D, kKvPromptRows>(p, pl.ctas, env);
+    return pl.rows == 8 ? launch_join<D, 8>(p, pl.ctas, env) : launch_join<D, 16>(p, pl.ctas, env);
 }
 
 }  // namespace
@@ -808,7 +701,7 @@ size_t kv_attention_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int6
                               int64_t max_q, int sms) {
     const Plan pl = make_plan(B, T_q, G, H, max_kv, max_q, bits, sms);
     if (!pl.split) return 0;
-    return part_bytes(pl.ctas, 8 * pl.halves, D) + (size_t)pl.ctas * sizeof(KvSplitItem);
+    return part_bytes(pl.ctas, pl.rows, D) + (size_t)pl.ctas * sizeof(KvSplitItem);
 }
 
 cudaError_t launch_kv_attention(KvAttnParams p, int64_t D, int64_t bits, int64_t max_q, void* workspace,
@@ -819,13 +712,12 @@ cudaError_t launch_kv_attention(KvAttnParams p, int64_t D, int64_t bits, int64_t
     p.part_ml = nullptr;
     p.split = nullptr;
     if (pl.split) {
-        const int64_t slots = pl.ctas * 2 * 8 * pl.halves;
+        const int64_t slots = pl.ctas * 2 * pl.rows;
         p.part_o = static_cast<float*>(workspace);
         p.part_ml = p.part_o + slots * D;
         p.split = reinterpret_cast<KvSplitItem*>(p.part_ml + slots * 2);
     }
-    if (D == 64) return bits == 4 ? launch_bits<64, 4>(p, pl, env) : launch_bits<64, 8>(p, pl, env);
-    return bits == 4 ? launch_bits<128, 4>(p, pl, env) : launch_bits<128, 8>(p, pl, env);
+    return D == 64 ? launch_dim<64>(p, bits, pl, env) : launch_dim<128>(p, bits, pl, env);
 }
 
 }  // namespace i8ql

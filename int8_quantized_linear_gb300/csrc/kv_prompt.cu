@@ -1,0 +1,693 @@
+// Attention over the quantized key/value cache for many query rows (prompt
+// chunks): the same result as kv_attention.cu on the tensor cores proper
+// (tcgen05, accumulators in TMEM).
+//
+// A block (one per SM) holds 256 query rows of one cache head (query tokens x
+// the head group's heads) as two M = 128 tiles, and walks the cache in tiles
+// of 128 tokens:
+//   S = Q K^T  (128 x 128, TMEM),  P = 2^(c S - m + 7) (fp16, back into S's
+//   columns),  O += P V  (128 x D, TMEM; P is the A operand from TMEM)
+// Bound by tensor throughput on paper (4 D flops a visible pair), in practice
+// by instruction issue: unpacking a tile costs as many instructions as the
+// softmax of 128 rows, which is why two M tiles share each unpacked tile.
+//
+// Roles: warps 0-3 and 4-7 the softmax of the two tiles (a thread a row: no
+// shuffles), warps 8-11 unpack codes into the swizzled operand tiles, warp 12
+// copies pages, warp 13 issues the MMAs.  While one tile's softmax runs, the
+// tensor cores work on the other's products.
+//
+// K and V become fp16 including scale and low value (one rounding of 2^-11
+// relative to the element: the products then need no factors per token), Q
+// and P as in kv_attention.cu.  Ranges: a row of Q is scaled to 2^8; a tile
+// of K by the power of two that brings its largest element to 2^7, undone in
+// c; V by one such power for all tiles so far, O being rescaled when it
+// grows; P's maximum m is only raised when a row exceeds it by 2^8 (the sums
+// are rescaled then), so P reaches at most 2^15 and keeps weights down to
+// 2^-31 of the largest.
+//
+// Operand layout: K-major, 128-byte swizzle.  The order of the channels is
+// free as long as Q and K agree, so key words are stored in the order in
+// which they unpack; V is stored transposed (channels x tokens), eight tokens
+// of a channel at a time, paired by byte permutes while unpacking.  Raw value
+// rows are copied eight tokens at a time to a stride 16 bytes longer, which
+// keeps the transposing reads off each other's banks.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "kv_math.cuh"
+
+namespace i8ql {
+namespace {
+
+constexpr int kTile = kKvPromptTile;  // cache tokens per tile
+constexpr int kRows = kKvPromptRows;  // query rows per block: two M tiles
+constexpr int kSoftmaxWarps = 8;
+constexpr int kUnpackWarps = 4;
+constexpr int kCopyWarp = kSoftmaxWarps + kUnpackWarps;
+constexpr int kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kKStages = 2;      // unpacked K tiles
+constexpr int kRawKeys = 2;      // raw K tiles (with the params of K and V)
+constexpr int kInfo = 4;         // tiles whose exponents are kept
+constexpr float kPShift = 7.0f;  // P = 2^(logit - m + kPShift)
+constexpr float kSlack = 8.0f;   // a row's maximum may exceed m by this (log2)
+
+template <int D, int BITS>
+struct Cfg {
+    static constexpr int kRowBytes = D * BITS / 8;
+    static constexpr int kKTile = kTile * D * 2;  // an operand tile of K, and of V
+    static constexpr int kVStages = BITS == 8 && D == 128 ? 1 : 2;
+    static constexpr int kGroupStride = 8 * kRowBytes + 16;  // eight raw value rows
+    static constexpr int kRawK = kTile * kRowBytes + 2 * kTile * 4;
+    static constexpr int kRawV = kTile / 8 * kGroupStride;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kRows * D * 2;
+    static constexpr int kOffV = kOffK + kKStages * kKTile;
+    static constexpr int kOffRawK = kOffV + kVStages * kKTile;
+    static constexpr int kOffRawV = kOffRawK + kRawKeys * kRawK;
+    static constexpr int kSmem = kOffRawV + kRawV + 1024;  // (aligned to 1024 by hand)
+};
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+#define I8QL_R8(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3]), "=r"((r)[(i) + 4]), \
+                      "=r"((r)[(i) + 5]), "=r"((r)[(i) + 6]), "=r"((r)[(i) + 7])
+#define I8QL_W8(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3]), "r"((r)[(i) + 4]), \
+                      "r"((r)[(i) + 5]), "r"((r)[(i) + 6]), "r"((r)[(i) + 7])
+
+// 32 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : I8QL_R8(r, 0), I8QL_R8(r, 8), I8QL_R8(r, 16), I8QL_R8(r, 24)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        I8QL_W8(r, 0), I8QL_W8(r, 8), I8QL_W8(r, 16), I8QL_W8(r, 24)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        I8QL_W8(r, 0), I8QL_W8(r, 8)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void unpack_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kUnpackWarps * 32) : "memory"); }
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Exponents of a tile, for the softmax.
+struct TileInfo {
+    int key_exp;  // K is held times 2^(134 - key_exp)
+    int val_exp;  // V is held times 2^(134 - val_exp), from this tile on
+};
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnParams p) {
+    using C = Cfg<D, BITS>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t raw_k_full[kRawKeys], raw_k_empty[kRawKeys], raw_v_full, raw_v_empty;
+    __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2];
+    __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], info_full[kInfo], drained;
+    __shared__ KvLocate locate;
+    __shared__ KvCursor cursors[kSoftmaxWarps];  // (kept out of the registers of the softmax)
+    __shared__ KvRange range;
+    __shared__ TileInfo infos[kInfo];
+    __shared__ uint32_t exp_red[2][kUnpackWarps][2];
+    __shared__ uint32_t key_factor[kTile][2];                // scale and centre, each twice, as halves
+    __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, centres
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t smem_at = tc::smem_u32(smem);
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kRawKeys; ++i) {
+            tc::mbar_init(&raw_k_full[i], 1);
+            tc::mbar_init(&raw_k_empty[i], kUnpackWarps);
+        }
+        tc::mbar_init(&raw_v_full, 1);
+        tc::mbar_init(&raw_v_empty, kUnpackWarps);
+        for (int i = 0; i < kKStages; ++i) {
+            tc::mbar_init(&k_full[i], kUnpackWarps * 32);
+            tc::mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&v_full[i], kUnpackWarps * 32);
+            tc::mbar_init(&v_empty[i], 1);
+            tc::mbar_init(&q_full[i], 128);
+            tc::mbar_init(&s_full[i], 1);
+            tc::mbar_init(&p_full[i], 128);
+            tc::mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < kInfo; ++i) tc::mbar_init(&info_full[i], 1);
+        tc::mbar_init(&drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
+    tc::tc_fence_before();
+    KvCursor start;
+    const KvRange found = kv_locate<kRows, kTile, kThreads>(p, locate, start);  // (its barriers publish the above)
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    bool dead = false;
+    // Waits of a whole warp; after one that gave up no work is done any more,
+    // but every loop and barrier runs to its end.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !tc::warp_wait(bar, parity, &abort_flag, p.err);
+    };
+
+    if (warp == kCopyWarp) {
+        // ------------------------------------------------------------ copies
+        KvCursor c = start;
+        int64_t left = found.end - found.begin;
+        const int page_tokens = 1 << p.cache.page_shift;
+        const int piece = min(page_tokens, kTile);
+        const int kind = lane & 3;  // K codes, K params, V params, none
+        const int at = (lane >> 2) * piece;
+        const int at_v = lane * 8;  // V codes: eight tokens
+        uint32_t kt = 0;            // tiles so far
+        while (left > 0 && !dead) {
+            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+            const int32_t* table = p.table + c.b * p.table_width;
+            const int first = (c.span.first + c.tile) * kTile;
+            auto needed = [&](int token, int tokens, int i) {
+                return i < n && token < c.span.end && token + tokens > c.span.begin;
+            };
+            auto need_k = [&](int i) { return kind < 3 && at < kTile && needed(first + i * kTile + at, piece, i); };
+            auto need_v = [&](int i) { return at_v < kTile && needed(first + i * kTile + at_v, 8, i); };
+            auto page_of = [&](bool need, int token) { return need ? __ldg(table + (token >> p.cache.page_shift)) : 0; };
+            auto checked = [&](int64_t page) {
+                if (page >= 0 && page < p.cache.pages) return page;
+                record_fault(p.err, kErrBitBadIndex);
+                return (int64_t)0;
+            };
+            // pages are looked up a tile ahead
+            int32_t next_k = page_of(need_k(0), first + at), next_v = page_of(need_v(0), first + at_v);
+            for (int i = 0; i < n && !dead; ++i) {
+                const int token = first + i * kTile;
+                const bool nk = need_k(i), nv = need_v(i);
+                const int64_t page_k = next_k, page_v = next_v;
+                next_k = page_of(need_k(i + 1), token + kTile + at);
+                next_v = page_of(need_v(i + 1), token + kTile + at_v);
+                const uint32_t slot = kt % kRawKeys;
+                const unsigned keys = __popc(__ballot_sync(0xffffffffu, nk && kind == 0));
+                const unsigned groups = __popc(__ballot_sync(0xffffffffu, nv));
+                wait(&raw_k_empty[slot], ((kt / kRawKeys) & 1) ^ 1);
+                if (!dead) {
+                    if (lane == 0) tc::mbar_expect_tx(&raw_k_full[slot], keys * piece * (C::kRowBytes + 8));
+                    __syncwarp();
+                    if (nk) {
+                        const int64_t row =
+                            kv_row(p.cache, checked(page_k), kind == 2, c.h, (token + at) & (page_tokens - 1));
+                        uint8_t* raw = smem + C::kOffRawK + slot * C::kRawK;
+                        if (kind == 0)
+                            bulk_load(raw + at * C::kRowBytes, p.cache.codes + row * C::kRowBytes,
+                                      piece * C::kRowBytes, &raw_k_full[slot]);
+                        else
+                            bulk_load(raw + kTile * C::kRowBytes + (kind - 1) * kTile * 4 + at * 4,
+                                      p.cache.params + row, piece * 4, &raw_k_full[slot]);
+                    }
+                }
+                wait(&raw_v_empty, (kt & 1) ^ 1);
+                if (!dead) {
+                    if (lane == 0) tc::mbar_expect_tx(&raw_v_full, groups * 8 * C::kRowBytes);
+                    __syncwarp();
+                    if (nv) {
+                        const int64_t row = kv_row(p.cache, checked(page_v), 1, c.h, (token + at_v) & (page_tokens - 1));
+                        bulk_load(smem + C::kOffRawV + lane * C::kGroupStride, p.cache.codes + row * C::kRowBytes,
+                                  8 * C::kRowBytes, &raw_v_full);
+                    }
+                    ++kt;
+                }
+            }
+            left -= n;
+            if (!dead) kv_next_item<kRows, kTile>(p, c);
+        }
+        if (dead) {
+            // giving up: let the copies in flight land before the block's
+            // shared memory can go to another (a wait for one that was never
+            // issued runs out)
+            for (uint32_t k = kt > kRawKeys ? kt - kRawKeys : 0; k <= kt; ++k) {
+                int none = 0;
+                tc::mbar_wait(&raw_k_full[k % kRawKeys], (k / kRawKeys) & 1, &none, p.err);
+            }
+            int none = 0;
+            if (kt > 0) tc::mbar_wait(&raw_v_full, (kt - 1) & 1, &none, p.err);
+        }
+    } else if (warp >= kSoftmaxWarps && warp < kCopyWarp) {
+        // ------------------------------------------------------------ unpacking
+        KvCursor c = start;
+        int64_t left = found.end - found.begin;
+        const int tid = threadIdx.x - kSoftmaxWarps * 32;  // 0 .. 127
+        const int w4 = warp - kSoftmaxWarps;
+        uint32_t kt = 0;
+        constexpr float kTop = BITS == 4 ? 15.0f : 255.0f;
+        constexpr int kLanesPerKey = C::kRowBytes / 16;
+        constexpr int kChunks = BITS == 4 ? 4 : 2;  // operand chunks (8 channels) per 16 raw bytes
+        constexpr int kValWords = D * BITS / 256;   // raw words of D / 8 channels
+        constexpr int kPerWord = 32 / BITS;         // channels per word
+        const int key_lane = tid % kLanesPerKey;
+        const int val_group = tid & 15, val_part = tid >> 4;  // eight tokens, D / 8 channels
+        while (left > 0) {
+            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+            int val_exp = 8;
+            for (int i = 0; i < n; ++i, ++kt) {
+                const int token = (c.span.first + c.tile + i) * kTile;
+                const uint32_t slot = kt % kRawKeys, stage = kt % kKStages;
+                const uint8_t* raw = smem + C::kOffRawK + slot * C::kRawK;
+                wait(&raw_k_full[slot], (kt / kRawKeys) & 1);
+                // one token's scales and low values; the tile's exponents
+                uint32_t pk = 0, pv = 0;
+                if (!dead && token + tid >= c.span.begin && token + tid < c.span.end) {
+                    const uint32_t* params = reinterpret_cast<const uint32_t*>(raw + kTile * C::kRowBytes) + tid;
+                    pk = params[0];
+                    pv = params[kTile];
+                }
+                auto magnitude = [](uint32_t param) {
+                    const float lo = kv_low(param);
+                    const uint32_t b = __float_as_uint(fmaxf(fabsf(lo), fabsf(fmaf(kv_scale(param), kTop, lo))));
+                    return b < 0x7f800000u ? b : 0u;
+                };
+                const uint32_t top_k = __reduce_max_sync(0xffffffffu, magnitude(pk));
+                const uint32_t top_v = __reduce_max_sync(0xffffffffu, magnitude(pv));
+                if (lane == 0) {
+                    exp_red[kt & 1][w4][0] = top_k;
+                    exp_red[kt & 1][w4][1] = top_v;
+                }
+                unpack_sync();
+                int key_exp = 8;
+                for (int w = 0; w < kUnpackWarps; ++w) {
+                    key_exp = max(key_exp, (int)(exp_red[kt & 1][w][0] >> 23));
+                    val_exp = max(val_exp, (int)(exp_red[kt & 1][w][1] >> 23));
+                }
+                const float fk = pow2(134 - key_exp), fv = pow2(134 - val_exp);
+                const float ks = kv_scale(pk) * fk, kc = fmaf(kv_scale(pk), kCentre<BITS>, kv_low(pk)) * fk;
+                const float vs = kv_scale(pv) * fv, vc = fmaf(kv_scale(pv), kCentre<BITS>, kv_low(pv)) * fv;
+                key_factor[tid][0] = pack_f16(ks, ks);
+                key_factor[tid][1] = pack_f16(kc, kc);
+                const uint32_t v2 = pack_f16(vs, vc);
+                val_factor[0][tid] = (uint16_t)v2;
+                val_factor[1][tid] = (uint16_t)(v2 >> 16);
+                if (tid == 0) {
+                    infos[kt % kInfo].key_exp = key_exp;
+                    infos[kt % kInfo].val_exp = val_exp;
+                    tc::mbar_arrive(&info_full[kt % kInfo]);
+                }
+                unpack_sync();
+                // K: 16 raw bytes of a token at a time
+                wait(&k_empty[stage], ((kt / kKStages) & 1) ^ 1);
+                if (!dead) {
+                    const uint32_t dst = smem_at + C::kOffK + stage * C::kKTile;
+#pragma unroll
+                    for (int r = 0; r < kLanesPerKey; ++r) {
+                        const int tok = tid / kLanesPerKey + r * (kTile / kLanesPerKey);
+                        uint32_t w[4];
+                        lds<4>(raw + tok * C::kRowBytes + key_lane * 16, w);
+                        const uint32_t s = key_factor[tok][0], o = key_factor[tok][1];
+                        const int chunk0 = key_lane * kChunks;  // of the row's D / 8
+                        const int block = chunk0 / 8, pos0 = chunk0 % 8;
+                        const int flip = block & 1;  // lanes of the two blocks take their chunks in opposite order (banks)
+                        const uint32_t row = dst + block * (kTile * 128) + tok * 128;
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            uint32_t h[4];
+                            if constexpr (BITS == 4) {
+                                unpack_nibbles(flip ? w[j ^ 1] : w[j], h);
+                            } else {
+                                const uint32_t a = flip ? w[2 * (j ^ 1)] : w[2 * j];
+                                const uint32_t b = flip ? w[2 * (j ^ 1) + 1] : w[2 * j + 1];
+                                h[0] = unpack_bytes(a, 0x5150);
+                                h[1] = unpack_bytes(a, 0x5352);
+                                h[2] = unpack_bytes(b, 0x5150);
+                                h[3] = unpack_bytes(b, 0x5352);
+                            }
+                            sts16(row + (((pos0 + (j ^ flip)) ^ (tok & 7)) << 4), fma_f16x2(h[0], s, o),
+                                  fma_f16x2(h[1], s, o), fma_f16x2(h[2], s, o), fma_f16x2(h[3], s, o));
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&k_full[stage]);
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&raw_k_empty[slot]);
+                // V, transposed: eight tokens of D / 8 channels
+                const uint32_t vstage = kt % C::kVStages;
+                wait(&raw_v_full, kt & 1);
+                wait(&v_empty[vstage], ((kt / C::kVStages) & 1) ^ 1);
+                if (!dead) {
+                    const uint8_t* src = smem + C::kOffRawV + val_group * C::kGroupStride + val_part * (kValWords * 4);
+                    uint32_t w[8][kValWords];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) lds<kValWords>(src + j * C::kRowBytes, w[j]);
+                    uint32_t s[4], o[4];
+                    lds<4>(reinterpret_cast<const uint8_t*>(&val_factor[0][val_group * 8]), s);
+                    lds<4>(reinterpret_cast<const uint8_t*>(&val_factor[1][val_group * 8]), o);
+                    const uint32_t dst = smem_at + C::kOffV + vstage * C::kKTile + (val_group / 8) * (D * 128);
+#pragma unroll
+                    for (int k = 0; k < kValWords; ++k) {
+                        uint32_t h[4][kPerWord];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) unpack_values<BITS>(w[2 * j][k], w[2 * j + 1][k], h[j]);
+#pragma unroll
+                        for (int e = 0; e < kPerWord; ++e) {
+                            const int ch = val_part * (D / 8) + k * kPerWord + e;
+                            sts16(dst + ch * 128 + (((val_group & 7) ^ (ch & 7)) << 4), fma_f16x2(h[0][e], s[0], o[0]),
+                                  fma_f16x2(h[1][e], s[1], o[1]), fma_f16x2(h[2][e], s[2], o[2]),
+                                  fma_f16x2(h[3][e], s[3], o[3]));
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&v_full[vstage]);
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&raw_v_empty);
+            }
+            left -= n;
+            kv_next_item<kRows, kTile>(p, c);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMAs
+        KvCursor c = start;
+        int64_t left = found.end - found.begin;
+        const uint32_t s_desc = tc::f16_idesc(kTile), o_desc = tc::f16_idesc(D);
+        uint32_t kt = 0, items[2] = {0, 0}, steps[2] = {0, 0};
+        auto qk = [&](int m, uint32_t tile) {
+            if (dead || lane != 0) return;
+            const uint32_t a = smem_at + C::kOffQ + m * (128 * D * 2);
+            const uint32_t b = smem_at + C::kOffK + (tile % kKStages) * C::kKTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                tc::mma_f16(tmem + m * kTile, tc::sw128_desc(a + (k / 4) * (128 * 128) + (k % 4) * 32),
+                            tc::sw128_desc(b + (k / 4) * (kTile * 128) + (k % 4) * 32), s_desc, k != 0);
+            tc::mma_commit(&s_full[m]);
+        };
+        auto pv = [&](int m, uint32_t tile, bool first) {
+            if (dead || lane != 0) return;
+            const uint32_t b = smem_at + C::kOffV + (tile % C::kVStages) * C::kKTile;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_f16_ts(tmem + 256 + m * D, tmem + m * kTile + k * 8,
+                           tc::sw128_desc(b + (k / 4) * (D * 128) + (k % 4) * 32), o_desc, !first || k != 0);
+        };
+        auto commit = [&](uint64_t* bar) {
+            if (!dead && lane == 0) tc::mma_commit(bar);
+        };
+        while (left > 0) {
+            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+            const int rows = min(kRows, c.seq.nq * p.G - c.rb * kRows);
+            const int tiles_m = rows > 128 ? 2 : 1;
+            for (int m = 0; m < tiles_m; ++m) {
+                wait(&q_full[m], items[m] & 1);
+                ++items[m];
+                if (m == 0) wait(&k_full[kt % kKStages], (kt / kKStages) & 1);
+                tc::tc_fence_after();
+                qk(m, kt);
+            }
+            commit(&k_empty[kt % kKStages]);
+            for (int i = 0; i < n; ++i, ++kt) {
+                for (int m = 0; m < tiles_m; ++m) {
+                    wait(&p_full[m], steps[m] & 1);
+                    ++steps[m];
+                    if (m == 0) wait(&v_full[kt % C::kVStages], (kt / C::kVStages) & 1);
+                    tc::tc_fence_after();
+                    pv(m, kt, i == 0);
+                    if (i + 1 < n) {
+                        if (m == 0) wait(&k_full[(kt + 1) % kKStages], ((kt + 1) / kKStages) & 1);
+                        tc::tc_fence_after();
+                        qk(m, kt + 1);
+                    } else {
+                        commit(&o_full[m]);
+                    }
+                }
+                commit(&v_empty[kt % C::kVStages]);
+                if (i + 1 < n) commit(&k_empty[(kt + 1) % kKStages]);
+            }
+            left -= n;
+            kv_next_item<kRows, kTile>(p, c);
+        }
+        // nothing may be in flight when the TMEM is given back
+        if (lane == 0) tc::mma_commit(&drained);
+        __syncwarp();
+        int none = 0;
+        tc::mbar_wait(&drained, 0, &none, p.err);
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int m = warp / 4;
+        const int r = m * 128 + (warp % 4) * 32 + lane;  // row of the block
+        const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + m * kTile, o_at = tmem + lanes + 256 + m * D;
+        KvCursor& c = cursors[warp];
+        if (lane == 0) c = start;
+        if (threadIdx.x == 0) range = found;
+        asm volatile("bar.sync 2, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
+        uint32_t kt = 0, items = 0, steps = 0;
+        int64_t done = 0;
+        bool split = false;
+        while (done < range.end - range.begin) {
+            const int n = (int)min(range.end - range.begin - done, (int64_t)(c.span.tiles - c.tile));
+            const int row0 = c.rb * kRows;
+            const int rows = min(kRows, c.seq.nq * p.G - row0);
+            const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
+            if (m == 0 || rows > 128) {
+                const int base = c.seq.len - c.seq.nq;
+                const bool live = r < rows;
+                const int i0 = (row0 + (live ? r : 0)) / p.G;
+                const int head = c.h * p.G + (row0 + (live ? r : 0)) - i0 * p.G;
+                const int hi = live ? base + i0 : INT32_MAX;
+                const int lo = live && p.window > 0 ? (int)max(base + i0 + 1 - p.window, (int64_t)0) : 0;
+                // tokens [all_lo, all_hi] are seen by every row of this M tile
+                const int all_hi = base + (row0 + m * 128) / p.G;
+                const int last = row0 + min(rows, m * 128 + 128) - 1;
+                const int all_lo = p.window > 0 ? (int)max(base + last / p.G + 1 - p.window, (int64_t)0) : 0;
+                float unit;  // what a scaled logit counts (times 2^(key_exp - 134)), in log2 units
+                {
+                    // the row of Q, scaled to 2^8 and permuted as the keys unpack, into its operand tile
+                    const uint4* src =
+                        reinterpret_cast<const uint4*>(p.q + (c.seq.q0 + i0) * p.q_stride + (int64_t)head * D);
+                    uint32_t top = 0;
+#pragma unroll 4
+                    for (int w = 0; w < D / 8; ++w) {
+                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
+                            top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+                        }
+                    }
+                    const int e = max((int)(top >> 23), 9) - 127;
+                    const float f = p.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
+                    unit = pow2(e - 8) * fabsf(p.scale_log2);
+                    const uint32_t dst = smem_at + C::kOffQ + m * (128 * D * 2) + (r & 127) * 128;
+#pragma unroll 4
+                    for (int w = 0; w < D / 8; ++w) {
+                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                        const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
+                                            lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
+                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r & 7)) << 4);
+                        if constexpr (BITS == 4)
+                            sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]),
+                                  pack_f16(y[3], y[7]));
+                        else
+                            sts16(at, pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]),
+                                  pack_f16(y[6], y[7]));
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&q_full[m]);
+                }
+                float top = -INFINITY;  // the maximum the sums stand at, in log2 units
+                float total = 0.0f;
+                int val_exp = 8;
+                for (int i = 0; i < n; ++i, ++steps) {
+                    const int token = (c.span.first + c.tile + i) * kTile;
+                    const uint32_t k = kt + i;
+                    wait(&info_full[k % kInfo], (k / kInfo) & 1);
+                    wait(&s_full[m], steps & 1);
+                    tc::tc_fence_after();
+                    if (!dead) {
+                        const TileInfo info = infos[k % kInfo];
+                        const float cst = unit * pow2(info.key_exp - 134);
+                        const bool edge = token + kTile - 1 > all_hi || token < all_lo;
+                        uint32_t v[32];
+                        float high = -INFINITY;
+#pragma unroll 1
+                        for (int q = 0; q < kTile / 32; ++q) {
+                            tmem_ld32(s_at + q * 32, v);
+                            tc::tmem_wait_ld();
+                            if (edge) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const int tok = token + q * 32 + j;
+                                    if (tok <= hi && tok >= lo) high = fmaxf(high, __uint_as_float(v[j]));
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(v[j]));
+                            }
+                        }
+                        const float a = high == -INFINITY ? -INFINITY : high * cst;
+                        const bool raise = a > top + kSlack;  // (the first time: from -infinity)
+                        if (__any_sync(0xffffffffu, raise) || info.val_exp != val_exp) {
+                            float f = 1.0f;
+                            if (raise) {
+                                f = exp2_approx(top - a);
+                                top = a;
+                                total *= f;
+                            }
+                            if (i > 0) {
+                                f *= info.val_exp - val_exp > 126 ? 0.0f : pow2(val_exp - info.val_exp);
+#pragma unroll 1
+                                for (int q = 0; q < D / 32; ++q) {
+                                    tmem_ld32(o_at + q * 32, v);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                                    tmem_st32(o_at + q * 32, v);
+                                }
+                            }
+                            val_exp = info.val_exp;
+                        }
+                        const float shift = top == -INFINITY ? 0.0f : kPShift - top;
+                        float sum[2] = {0.0f, 0.0f};
+#pragma unroll 1
+                        for (int q = 0; q < kTile / 32; ++q) {
+                            tmem_ld32(s_at + q * 32, v);
+                            tc::tmem_wait_ld();
+                            uint32_t h[16];
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                float x = exp2_approx(fmaf(__uint_as_float(v[j]), cst, shift));
+                                float y = exp2_approx(fmaf(__uint_as_float(v[j + 1]), cst, shift));
+                                if (edge) {
+                                    const int tok = token + q * 32 + j;
+                                    x = tok <= hi && tok >= lo ? x : 0.0f;
+                                    y = tok + 1 <= hi && tok + 1 >= lo ? y : 0.0f;
+                                }
+                                sum[0] += x;
+                                sum[1] += y;
+                                h[j / 2] = pack_f16(x, y);
+                            }
+                            tmem_st16(s_at + q * 16, h);
+                        }
+                        total += sum[0] + sum[1];
+                        tmem_wait_st();
+                    }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&p_full[m]);
+                }
+                wait(&o_full[m], items & 1);
+                ++items;
+                tc::tc_fence_after();
+                if (!dead) {
+                    const float back = pow2(val_exp - 134);
+                    const float by = begins && ends ? (total == 0.0f ? 0.0f : back / total) : back;
+                    const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows + r;
+                    uint16_t* out = p.out + ((c.seq.q0 + i0) * ((int64_t)p.cache.H * p.G) + head) * D;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t v[32];
+                        __syncwarp();
+                        tmem_ld32(o_at + q * 32, v);
+                        tc::tmem_wait_ld();
+                        float x[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = by == 0.0f ? 0.0f : __uint_as_float(v[j]) * by;
+                        if (!live) {
+                        } else if (begins && ends) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                *reinterpret_cast<uint4*>(out + q * 32 + j) =
+                                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
+                                               pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<float4*>(p.part_o + slot * D + q * 32 + j) =
+                                    make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                        }
+                    }
+                    if (live && !(begins && ends))
+                        *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, total);
+                    if (begins && !ends) {
+                        split = true;
+                        if (threadIdx.x == 0) {
+                            KvSplitItem it;
+                            it.q_row = c.seq.q0;
+                            it.row0 = row0;
+                            it.rows = rows;
+                            it.h = c.h;
+                            it.last_cta = kv_owner(range.total, range.ctas, range.begin + done + c.span.tiles - 1);
+                            it.pad = 0;
+                            p.split[blockIdx.x] = it;
+                        }
+                    }
+                }
+            }
+            kt += n;
+            done += n;
+            __syncwarp();
+            if (lane == 0) kv_next_item<kRows, kTile>(p, c);
+            __syncwarp();
+        }
+        if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int BITS>
+cudaError_t launch_form(const KvAttnParams& p, int64_t ctas, const LaunchEnv& env) {
+    using C = Cfg<D, BITS>;
+    static_assert(C::kSmem <= 227 * 1024 - 4096, "shared memory of a block");
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::call_once(once[dev & 63], [&] {
+        set[dev & 63] =
+            cudaFuncSetAttribute(kv_prompt_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (set[dev & 63] != cudaSuccess) return set[dev & 63];
+    return launch_kernel(kv_prompt_kernel<D, BITS>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, env.stream,
+                         kNoCluster, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(const KvAttnParams& p, int64_t D, int64_t bits, int64_t ctas, const LaunchEnv& env) {
+    if (D == 64) return bits == 4 ? launch_form<64, 4>(p, ctas, env) : launch_form<64, 8>(p, ctas, env);
+    return bits == 4 ? launch_form<128, 4>(p, ctas, env) : launch_form<128, 8>(p, ctas, env);
+}
+
+}  // namespace i8ql

@@ -17,6 +17,10 @@
 
 namespace i8ql {
 
+// Tiles of the kernel for many query rows (kv_prompt.cu).
+constexpr int kKvPromptTile = 128;
+constexpr int kKvPromptRows = 256;
+
 struct KvAttnParams {
     KvCache cache;
     const uint16_t* q;
@@ -46,6 +50,9 @@ struct KvSplitItem {
     int32_t last_cta;
     int64_t pad;
 };
+
+// The kernel for many query rows, without the join (D 64 or 128, bits 4 or 8).
+cudaError_t launch_kv_prompt(const KvAttnParams& p, int64_t D, int64_t bits, int64_t ctas, const LaunchEnv& env);
 
 namespace {
 

@@ -54,6 +54,9 @@ class Attended:
         self.weighted = np.zeros((n_q, hq, d))  # sum_j p_j |v_j - centre_j|: what rounding p_j s_j scales with
         self.size = np.zeros((n_q, hq, d))      # sum_j p_j |v_j|
         self.logit = np.zeros((n_q, hq))        # max_j softmax_scale sum_d |q_d| |k_jd|
+        self.flush = np.zeros((n_q, hq, 1))     # visible tokens times the largest magnitude of their value rows
+        self.mid = np.zeros((n_q, hq, 1))       # sum_j p_j |centre_j| of the values
+        self.mid_logit = np.zeros((n_q, hq))    # max_j softmax_scale sum_d |q_d| |centre_j| of the keys
         self.biased = np.zeros((n_q, hq))       # max_j softmax_scale (sum_d |q_d| s_j (c + 128) + |low_j - 128 s_j| |sum q|)
 
 
@@ -69,6 +72,7 @@ def attention(q, codes, scale, low, n_q, window, softmax_scale, centre=8) -> Att
     for h in range(hq):
         c = h // (hq // heads)
         k, v = kv[0, :, c], kv[1, :, c]
+        k_mid, v_mid = (np.abs(l64[x, :, c] + s64[x, :, c] * centre) for x in (0, 1))
         mid = np.abs(s64[1, :, c, None] * (codes[1, :, c].astype(np.float64) - centre))
         for i in range(n_q):
             p = n - n_q + i
@@ -82,8 +86,12 @@ def attention(q, codes, scale, low, n_q, window, softmax_scale, centre=8) -> Att
             a.out[i, h] = w @ v[see]
             a.weighted[i, h] = w @ mid[see]
             a.size[i, h] = w @ np.abs(v[see])
-            a.logit[i, h] = softmax_scale * (np.abs(k[see]) @ np.abs(q[i, h])).max()
+            a.mid[i, h] = w @ v_mid[see]
+            a.flush[i, h] = len(w) * np.abs(v[see]).max()
+            size = abs(softmax_scale)
+            a.logit[i, h] = size * (np.abs(k[see]) @ np.abs(q[i, h])).max()
+            a.mid_logit[i, h] = size * (k_mid[see] * np.abs(q[i, h]).sum()).max()
             bias = s64[0, see, c] * ((codes[0, see, c] + 128.0) @ np.abs(q[i, h])) + np.abs(
                 l64[0, see, c] - 128 * s64[0, see, c]) * abs(q[i, h].sum())
-            a.biased[i, h] = softmax_scale * bias.max()
+            a.biased[i, h] = size * bias.max()
     return a

@@ -13,6 +13,15 @@ Bars:
                                   D / 16 MMA steps and the scaling, 16 of
                                   2^-22 = 2^-18 of the summed magnitudes
      + 2^-14 sum_j p_j |v_j|      exp2 and the fp32 sums over tokens
+   with few query rows (max_q * G <= 32); with more, where K and V become
+   fp16 (2^-11) with scale and low value, and so do the centres c_j,
+     2^-8 |o| + 2^-11 sum_j p_j (2 |v_j| + |c_j|)   P, V and the centres of V
+     + 2 delta sum_j p_j |v_j| + 2^-14 sum_j p_j |v_j|
+     delta = 2^-11 (max_j sum_d |q_d| (|k_jd| + |c_j|)) + 2^-18 of the same
+   (times the softmax scale);
+   and in both cases 2^-32 n max_j |v_j| over the n tokens a row sees: weights
+   become fp16 after scaling, which rounds those under 2^-22 of the largest to
+   multiples of 2^-32 of it (only visible where a dominant token's value is 0);
    where p, v and o are the 64-bit oracle's; and the whole output within
    4e-3 relative Frobenius (two bf16 roundings, 1.7e-3 rms each, with room).
 """
@@ -183,6 +192,8 @@ class Problem:
 
     def run(self, window=0, scale=None, q=None, single=None, max_q="known", **kw):
         single = all(n == 1 for n in self.nqs) if single is None else single
+        hint = 1 if single else max(self.nqs + [1]) if max_q == "known" else max_q or self.q.shape[0]
+        self.wide = hint * self.q.shape[1] // self.codes.shape[2] > 32
         if not single:
             kw["q_offsets"] = self.offsets
             kw["max_q"] = max(self.nqs + [1]) if max_q == "known" else max_q
@@ -198,8 +209,13 @@ class Problem:
             a = oracle.attention(q[at:at + nq], c, s, low, nq, window, scale, centre=2 ** (self.bits - 1))
             got = y[at:at + nq]
             at += nq
-            bound = 2.0 ** -8 * (np.abs(a.out) + a.weighted) + a.size * (
-                2.0 ** -17 * a.biased[..., None] + 2.0 ** -14) + 1e-37
+            if self.wide:
+                bound = 2.0 ** -8 * np.abs(a.out) + 2.0 ** -11 * (2 * a.size + a.mid) + a.size * (
+                    2.0 ** -10 * (a.logit + a.mid_logit)[..., None] * (1 + 2.0 ** -7) + 2.0 ** -14) + 1e-37
+            else:
+                bound = 2.0 ** -8 * (np.abs(a.out) + a.weighted) + a.size * (
+                    2.0 ** -17 * a.biased[..., None] + 2.0 ** -14) + 1e-37
+            bound = bound + 2.0 ** -32 * a.flush
             off = np.abs(got - a.out)
             assert np.all(off <= bound), f"off by {np.max(off / bound):.3g} of the bound"
             err += np.sum(off ** 2)
@@ -256,6 +272,72 @@ def test_drafts(hq, h, d, bits, window):
     # rows that see nothing are exactly zero: the first queries of the sequences with 2 and 0 tokens
     start = np.concatenate([[0], np.cumsum(nqs)])
     assert not y[start[6]:start[6] + 2].any() and not y[start[7]:start[8]].any()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("hq,h,d", [(8, 2, 128), (8, 2, 64), (3, 3, 128), (7, 1, 64), (20, 1, 128)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_prompts(hq, h, d, bits, window):
+    """Prompt chunks: lengths around tiles and row blocks, whole prompts and chunks behind a cached prefix, beside
+    single tokens and empty sequences."""
+    nqs = [130, 64, 1, 0, 33, 129, 7]
+    p = Problem([130, 300, 411, 50, 33, 700, 5], nqs, hq, h, d, bits, 16, hq + bits + window)
+    y = p.run(window=window)
+    p.check(y, window=window)
+    assert torch.equal(p.run(window=window), y)
+    start = np.concatenate([[0], np.cumsum(nqs)])
+    assert not y[start[6]:start[6] + 2].any()  # five tokens, seven queries: the first two see nothing
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_prompt_over_a_long_prefix(page, bits):
+    """Few row blocks over many tiles: cut between CTAs and joined."""
+    p = Problem([5003, 900], [40, 70], 8, 2, 128, bits, page, page + bits)
+    y = p.run()
+    p.check(y)
+    assert torch.equal(p.run(), y)
+
+
+@pytest.mark.parametrize("spread,offset", [(8.0, 0.0), (1e-6, 0.0), (1.0, 30.0), (1e4, 0.0)])
+def test_prompt_value_ranges(spread, offset):
+    p = Problem([400, 300], [90, 70], 8, 2, 128, 4, 16, 14, spread=spread, offset=offset)
+    scale = p.d ** -0.5 / (spread if spread > 100 else 1)
+    p.check(p.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_prompt_negative_and_zero_scale(scale):
+    p = Problem([300], [80], 4, 2, 64, 8, 16, 18)
+    p.check(p.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_values_of_growing_size(nq):
+    """Scales that grow by far along the context: the sums are brought to the larger unit."""
+    p = Problem([1100], [nq], 8, 2, 128, 4, 16, 21)
+    c, s, low = p.seqs[0]
+    grow = np.exp2(np.arange(1100) // 64 * 3.0 - 30).astype(np.float32)[None, :, None]
+    grow = np.concatenate([np.ones_like(grow), grow])
+    p.seqs[0] = (c, s * grow, low * grow)
+    pages = p.table[0, :-(-1100 // 16)].long()
+    full = torch.ones(len(pages) * 16)
+    full[:1100] = torch.from_numpy(grow[1, :, 0])
+    p.params[pages, 1] = (p.params[pages, 1].float() * full.view(-1, 1, 16, 1).cuda()).to(torch.bfloat16)
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_non_finite_queries_stay_in_their_rows(nq):
+    p = Problem([200], [nq], 8, 2, 128, 4, 16, 22)
+    want = p.run()
+    q = p.q.clone()
+    q[0, 1, 7], q[-1, 5, 3] = float("nan"), float("inf")
+    y = p.run(q=q.cuda())
+    assert torch.isnan(y[0, 1]).all() and torch.isnan(y[-1, 5]).any()
+    keep = torch.ones(nq, 8, dtype=torch.bool)
+    keep[0, 1] = keep[-1, 5] = False
+    assert torch.equal(y.cpu()[keep], want.cpu()[keep])
 
 
 def test_max_q_only_chooses_the_kernel():
