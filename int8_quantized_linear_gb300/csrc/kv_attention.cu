@@ -58,6 +58,7 @@ constexpr int kWarps = 4;                    // consumer warps
 constexpr int kWarpTokens = kTile / kWarps;  // tokens of a stage per warp
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kStages = 3;
+constexpr int kCost = 1;  // tiles that beginning and ending an item counts
 constexpr int64_t kFewRows = 32;  // query rows of a sequence's head group up to which this kernel runs
 
 template <int D, int BITS, int ROWS>
@@ -117,11 +118,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     int stage = 0;
     uint32_t parity = 0;
     KvCursor start;
-    const KvRange found = kv_locate<ROWS, kTile, kThreads>(p, locate, start);  // (its barriers also publish the mbarriers)
+    const KvRange found = kv_locate<ROWS, kTile, kCost, kThreads>(p, locate, start);  // (its barriers also publish the mbarriers)
 
     if (warp == kWarps) {
         KvCursor& c = start;
-        int64_t left = found.end - found.begin;
         // ---------------------------------------------------------- producer
         // One lane per copy: four arrays (K and V codes and params) of up to
         // eight pieces of a tile (a piece is a page, or the tile's part of one).
@@ -133,8 +133,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
         const int dst = is_param ? 2 * C::kCodes + kv * kTile * 4 + at * 4 : kv * C::kCodes + at * C::kRowBytes;
         int issued = 0;
         bool ok = true;
-        while (left > 0 && ok) {
-            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+        while (const int n = ok ? kv_take<kCost>(p, c, found.end) : 0) {
             const int32_t* table = p.table + c.b * p.table_width;
             const int first = (c.span.first + c.tile) * kTile + at;  // this lane's token of the item's next tile
             auto needed = [&](int i) {
@@ -173,8 +172,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                     parity ^= 1;
                 }
             }
-            left -= n;
-            kv_next_item<ROWS, kTile>(p, c);
+            kv_next_item<ROWS, kTile, kCost>(p, c);
         }
         if (!ok) {
             // giving up: let the copies in flight land before the block's
@@ -206,10 +204,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     if (lane == 0) c = start;
     if (threadIdx.x == 0) range = found;
     consumer_sync();
-    int64_t done = 0;
     bool split = false;
-    while (done < range.end - range.begin) {
-        const int n = (int)min(range.end - range.begin - done, (int64_t)(c.span.tiles - c.tile));
+    while (const int n = kv_take<kCost>(p, c, range.end)) {
         const int row0 = c.rb * ROWS;
         const int rows = min(ROWS, c.seq.nq * p.G - row0);
         const int base = c.seq.len - c.seq.nq;
@@ -553,15 +549,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                     it.row0 = row0;
                     it.rows = rows;
                     it.h = c.h;
-                    it.last_cta = kv_owner(range.total, range.ctas, range.begin + done + c.span.tiles - 1);
+                    it.last_cta = kv_owner(range.total, range.ctas, c.at + kCost + c.span.tiles - 1);
                     it.pad = 0;
                     p.split[blockIdx.x] = it;
                 }
             }
         }
-        done += n;
         __syncwarp();
-        if (lane == 0) kv_next_item<ROWS, kTile>(p, c);
+        if (lane == 0) kv_next_item<ROWS, kTile, kCost>(p, c);
         consumer_sync();  // the cursor is at the next item, and the merge rows are free again
     }
     if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
@@ -657,7 +652,7 @@ Plan make_plan(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int
     const int64_t tile = pl.rows == kKvPromptRows ? kKvPromptTile : kTile;
     const int64_t item_tiles = std::max<int64_t>((max_kv + tile - 1) / tile, 1);
     const int64_t items = (T_q * G / pl.rows + B) * H;
-    pl.ctas = std::min<int64_t>(sms * per_sm, items > sms * per_sm ? sms * per_sm : items * item_tiles);
+    pl.ctas = items > sms * per_sm ? sms * per_sm : std::min<int64_t>(sms * per_sm, items * item_tiles);
     pl.split = item_tiles > 1;
     return pl;
 }

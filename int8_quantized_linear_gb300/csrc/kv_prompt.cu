@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kv_math.cuh"
 
@@ -51,6 +52,7 @@ constexpr int kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kKStages = 2;      // unpacked K tiles
 constexpr int kRawKeys = 2;      // raw K tiles (with the params of K and V)
+constexpr int kCost = 2;         // tiles that beginning and ending an item counts
 constexpr int kInfo = 4;         // tiles whose exponents are kept
 constexpr float kPShift = 7.0f;  // P = 2^(logit - m + kPShift)
 constexpr float kSlack = 8.0f;   // a row's maximum may exceed m by this (log2)
@@ -119,6 +121,35 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+    return pair_u32(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void split_f32(uint64_t p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Exponents of a tile, for the softmax.
 struct TileInfo {
     int key_exp;  // K is held times 2^(134 - key_exp)
@@ -174,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
     tc::tc_fence_before();
     KvCursor start;
-    const KvRange found = kv_locate<kRows, kTile, kThreads>(p, locate, start);  // (its barriers publish the above)
+    const KvRange found = kv_locate<kRows, kTile, kCost, kThreads>(p, locate, start);  // (its barriers publish the above)
     tc::tc_fence_after();
     const uint32_t tmem = tmem_base;
     bool dead = false;
@@ -187,15 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     if (warp == kCopyWarp) {
         // ------------------------------------------------------------ copies
         KvCursor c = start;
-        int64_t left = found.end - found.begin;
         const int page_tokens = 1 << p.cache.page_shift;
         const int piece = min(page_tokens, kTile);
         const int kind = lane & 3;  // K codes, K params, V params, none
         const int at = (lane >> 2) * piece;
         const int at_v = lane * 8;  // V codes: eight tokens
         uint32_t kt = 0;            // tiles so far
-        while (left > 0 && !dead) {
-            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+        while (const int n = dead ? 0 : kv_take<kCost>(p, c, found.end)) {
             const int32_t* table = p.table + c.b * p.table_width;
             const int first = (c.span.first + c.tile) * kTile;
             auto needed = [&](int token, int tokens, int i) {
@@ -248,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     ++kt;
                 }
             }
-            left -= n;
-            if (!dead) kv_next_item<kRows, kTile>(p, c);
+            if (!dead) kv_next_item<kRows, kTile, kCost>(p, c);
         }
         if (dead) {
             // giving up: let the copies in flight land before the block's
@@ -265,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     } else if (warp >= kSoftmaxWarps && warp < kCopyWarp) {
         // ------------------------------------------------------------ unpacking
         KvCursor c = start;
-        int64_t left = found.end - found.begin;
         const int tid = threadIdx.x - kSoftmaxWarps * 32;  // 0 .. 127
         const int w4 = warp - kSoftmaxWarps;
         uint32_t kt = 0;
@@ -276,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         constexpr int kPerWord = 32 / BITS;         // channels per word
         const int key_lane = tid % kLanesPerKey;
         const int val_group = tid & 15, val_part = tid >> 4;  // eight tokens, D / 8 channels
-        while (left > 0) {
-            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+        while (const int n = kv_take<kCost>(p, c, found.end)) {
             int val_exp = 8;
             for (int i = 0; i < n; ++i, ++kt) {
                 const int token = (c.span.first + c.tile + i) * kTile;
@@ -390,38 +416,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&raw_v_empty);
             }
-            left -= n;
-            kv_next_item<kRows, kTile>(p, c);
+            kv_next_item<kRows, kTile, kCost>(p, c);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMAs
         KvCursor c = start;
-        int64_t left = found.end - found.begin;
         const uint32_t s_desc = tc::f16_idesc(kTile), o_desc = tc::f16_idesc(D);
         uint32_t kt = 0, items[2] = {0, 0}, steps[2] = {0, 0};
+        // descriptors count in units of 16 bytes: 2 a step of 16 elements, and
+        // the rest of a row's swizzle atoms behind the first 64 elements
+        const uint64_t q_base = tc::sw128_desc(smem_at + C::kOffQ), k_base = tc::sw128_desc(smem_at + C::kOffK);
+        const uint64_t v_base = tc::sw128_desc(smem_at + C::kOffV);
         auto qk = [&](int m, uint32_t tile) {
             if (dead || lane != 0) return;
-            const uint32_t a = smem_at + C::kOffQ + m * (128 * D * 2);
-            const uint32_t b = smem_at + C::kOffK + (tile % kKStages) * C::kKTile;
+            const uint64_t a = q_base + m * (128 * D * 2 / 16);
+            const uint64_t b = k_base + (tile % kKStages) * (C::kKTile / 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                tc::mma_f16(tmem + m * kTile, tc::sw128_desc(a + (k / 4) * (128 * 128) + (k % 4) * 32),
-                            tc::sw128_desc(b + (k / 4) * (kTile * 128) + (k % 4) * 32), s_desc, k != 0);
+                tc::mma_f16(tmem + m * kTile, a + ((k / 4) * (128 * 128 / 16) + (k % 4) * 2),
+                            b + ((k / 4) * (kTile * 128 / 16) + (k % 4) * 2), s_desc, k != 0);
             tc::mma_commit(&s_full[m]);
         };
         auto pv = [&](int m, uint32_t tile, bool first) {
             if (dead || lane != 0) return;
-            const uint32_t b = smem_at + C::kOffV + (tile % C::kVStages) * C::kKTile;
+            const uint64_t b = v_base + (tile % C::kVStages) * (C::kKTile / 16);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-                mma_f16_ts(tmem + 256 + m * D, tmem + m * kTile + k * 8,
-                           tc::sw128_desc(b + (k / 4) * (D * 128) + (k % 4) * 32), o_desc, !first || k != 0);
+                mma_f16_ts(tmem + 256 + m * D, tmem + m * kTile + k * 8, b + ((k / 4) * (D * 128 / 16) + (k % 4) * 2),
+                           o_desc, !first || k != 0);
         };
         auto commit = [&](uint64_t* bar) {
             if (!dead && lane == 0) tc::mma_commit(bar);
         };
-        while (left > 0) {
-            const int n = (int)min(left, (int64_t)(c.span.tiles - c.tile));
+        while (const int n = kv_take<kCost>(p, c, found.end)) {
             const int rows = min(kRows, c.seq.nq * p.G - c.rb * kRows);
             const int tiles_m = rows > 128 ? 2 : 1;
             for (int m = 0; m < tiles_m; ++m) {
@@ -450,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 commit(&v_empty[kt % C::kVStages]);
                 if (i + 1 < n) commit(&k_empty[(kt + 1) % kKStages]);
             }
-            left -= n;
-            kv_next_item<kRows, kTile>(p, c);
+            kv_next_item<kRows, kTile, kCost>(p, c);
         }
         // nothing may be in flight when the TMEM is given back
         if (lane == 0) tc::mma_commit(&drained);
@@ -469,65 +495,77 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         if (threadIdx.x == 0) range = found;
         asm volatile("bar.sync 2, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
         uint32_t kt = 0, items = 0, steps = 0;
-        int64_t done = 0;
         bool split = false;
-        while (done < range.end - range.begin) {
-            const int n = (int)min(range.end - range.begin - done, (int64_t)(c.span.tiles - c.tile));
+        // What a thread knows of its row of an item.
+        struct Row {
+            bool active, live;   // the item has this M tile; the row exists
+            int hi, lo;          // the tokens it sees
+            int all_hi, all_lo;  // tokens [all_lo, all_hi] are seen by every row of the M tile
+            float unit;          // what a scaled logit counts (times 2^(key_exp - 134)), in log2 units
+            int64_t out;         // where its output goes
+        };
+        // Takes up the cursor's item: the row of Q, scaled to 2^8 and permuted
+        // as the keys unpack, goes into its operand tile (which the products
+        // of the item before have left by the time its last S is there).
+        auto take_up = [&](Row& row) {
             const int row0 = c.rb * kRows;
             const int rows = min(kRows, c.seq.nq * p.G - row0);
-            const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
-            if (m == 0 || rows > 128) {
-                const int base = c.seq.len - c.seq.nq;
-                const bool live = r < rows;
-                const int i0 = (row0 + (live ? r : 0)) / p.G;
-                const int head = c.h * p.G + (row0 + (live ? r : 0)) - i0 * p.G;
-                const int hi = live ? base + i0 : INT32_MAX;
-                const int lo = live && p.window > 0 ? (int)max(base + i0 + 1 - p.window, (int64_t)0) : 0;
-                // tokens [all_lo, all_hi] are seen by every row of this M tile
-                const int all_hi = base + (row0 + m * 128) / p.G;
-                const int last = row0 + min(rows, m * 128 + 128) - 1;
-                const int all_lo = p.window > 0 ? (int)max(base + last / p.G + 1 - p.window, (int64_t)0) : 0;
-                float unit;  // what a scaled logit counts (times 2^(key_exp - 134)), in log2 units
-                {
-                    // the row of Q, scaled to 2^8 and permuted as the keys unpack, into its operand tile
-                    const uint4* src =
-                        reinterpret_cast<const uint4*>(p.q + (c.seq.q0 + i0) * p.q_stride + (int64_t)head * D);
-                    uint32_t top = 0;
-#pragma unroll 4
-                    for (int w = 0; w < D / 8; ++w) {
-                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            row.active = m == 0 || rows > 128;
+            if (!row.active) return;
+            const int base = c.seq.len - c.seq.nq;
+            row.live = r < rows;
+            const int i = (row0 + (row.live ? r : 0)) / p.G;
+            const int head = c.h * p.G + (row0 + (row.live ? r : 0)) - i * p.G;
+            row.hi = row.live ? base + i : INT32_MAX;
+            row.lo = row.live && p.window > 0 ? (int)max(base + i + 1 - p.window, (int64_t)0) : 0;
+            row.all_hi = base + (row0 + m * 128) / p.G;
+            const int last = row0 + min(rows, m * 128 + 128) - 1;
+            row.all_lo = p.window > 0 ? (int)max(base + last / p.G + 1 - p.window, (int64_t)0) : 0;
+            row.out = ((c.seq.q0 + i) * ((int64_t)p.cache.H * p.G) + head) * D;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (c.seq.q0 + i) * p.q_stride + (int64_t)head * D);
+            uint32_t top = 0;
+#pragma unroll 8
+            for (int w = 0; w < D / 8; ++w) {
+                const uint4 v = row.live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
-                            top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
-                        }
-                    }
-                    const int e = max((int)(top >> 23), 9) - 127;
-                    const float f = p.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
-                    unit = pow2(e - 8) * fabsf(p.scale_log2);
-                    const uint32_t dst = smem_at + C::kOffQ + m * (128 * D * 2) + (r & 127) * 128;
-#pragma unroll 4
-                    for (int w = 0; w < D / 8; ++w) {
-                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                        const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
-                                            lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
-                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r & 7)) << 4);
-                        if constexpr (BITS == 4)
-                            sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]),
-                                  pack_f16(y[3], y[7]));
-                        else
-                            sts16(at, pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]),
-                                  pack_f16(y[6], y[7]));
-                    }
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&q_full[m]);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
+                    top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
                 }
-                float top = -INFINITY;  // the maximum the sums stand at, in log2 units
-                float total = 0.0f;
-                int val_exp = 8;
+            }
+            const int e = max((int)(top >> 23), 9) - 127;
+            const float f = p.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
+            row.unit = pow2(e - 8) * fabsf(p.scale_log2);
+            const uint32_t dst = smem_at + C::kOffQ + m * (128 * D * 2) + (r & 127) * 128;
+#pragma unroll 4
+            for (int w = 0; w < D / 8; ++w) {
+                const uint4 v = row.live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
+                                    lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
+                const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r & 7)) << 4);
+                if constexpr (BITS == 4)
+                    sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]), pack_f16(y[3], y[7]));
+                else
+                    sts16(at, pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&q_full[m]);
+        };
+        Row row = {};
+        int n = kv_take<kCost>(p, c, range.end);
+        if (n > 0) take_up(row);
+        while (n > 0) {
+            const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
+            float top = -INFINITY;  // the maximum the sums stand at, in log2 units
+            float total = 0.0f;
+            int val_exp = 8;
+            if (row.active) {
+                const int hi = row.hi, lo = row.lo;
+                const float unit = row.unit;
+                const int first = (c.span.first + c.tile) * kTile;
                 for (int i = 0; i < n; ++i, ++steps) {
-                    const int token = (c.span.first + c.tile + i) * kTile;
+                    const int token = first + i * kTile;
                     const uint32_t k = kt + i;
                     wait(&info_full[k % kInfo], (k / kInfo) & 1);
                     wait(&s_full[m], steps & 1);
@@ -535,24 +573,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     if (!dead) {
                         const TileInfo info = infos[k % kInfo];
                         const float cst = unit * pow2(info.key_exp - 134);
-                        const bool edge = token + kTile - 1 > all_hi || token < all_lo;
-                        uint32_t v[32];
-                        float high = -INFINITY;
-#pragma unroll 1
-                        for (int q = 0; q < kTile / 32; ++q) {
-                            tmem_ld32(s_at + q * 32, v);
-                            tc::tmem_wait_ld();
-                            if (edge) {
+                        const bool edge = token + kTile - 1 > row.all_hi || token < row.all_lo;
+                        // the tile's maximum; every load of S is one chunk ahead of its use
+                        auto maximum = [&](auto edge_tag) {
+                            constexpr bool EDGE = decltype(edge_tag)::value;
+                            uint32_t v[2][32];
+                            float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            tmem_ld32(s_at, v[0]);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const int tok = token + q * 32 + j;
-                                    if (tok <= hi && tok >= lo) high = fmaxf(high, __uint_as_float(v[j]));
+                            for (int q = 0; q < kTile / 32; ++q) {
+                                tc::tmem_wait_ld();
+                                if (q + 1 < kTile / 32) tmem_ld32(s_at + (q + 1) * 32, v[(q + 1) & 1]);
+                                const uint32_t (&x)[32] = v[q & 1];
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    float y = __uint_as_float(x[j]), z = __uint_as_float(x[j + 1]);
+                                    if (EDGE) {
+                                        const int tok = token + q * 32 + j;
+                                        y = tok <= hi && tok >= lo ? y : -INFINITY;
+                                        z = tok + 1 <= hi && tok + 1 >= lo ? z : -INFINITY;
+                                    }
+                                    high[(j / 2) & 3] = max3(high[(j / 2) & 3], y, z);
                                 }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(v[j]));
                             }
-                        }
+                            return max3(fmaxf(high[0], high[1]), high[2], high[3]);
+                        };
+                        const float high = edge ? maximum(std::true_type{}) : maximum(std::false_type{});
                         const float a = high == -INFINITY ? -INFINITY : high * cst;
                         const bool raise = a > top + kSlack;  // (the first time: from -infinity)
                         if (__any_sync(0xffffffffu, raise) || info.val_exp != val_exp) {
@@ -566,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                                 f *= info.val_exp - val_exp > 126 ? 0.0f : pow2(val_exp - info.val_exp);
 #pragma unroll 1
                                 for (int q = 0; q < D / 32; ++q) {
+                                    uint32_t v[32];
                                     tmem_ld32(o_at + q * 32, v);
                                     tc::tmem_wait_ld();
 #pragma unroll
@@ -575,87 +622,105 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                             }
                             val_exp = info.val_exp;
                         }
+                        const uint64_t cst2 = pair_f32(cst, cst);
                         const float shift = top == -INFINITY ? 0.0f : kPShift - top;
-                        float sum[2] = {0.0f, 0.0f};
-#pragma unroll 1
-                        for (int q = 0; q < kTile / 32; ++q) {
-                            tmem_ld32(s_at + q * 32, v);
-                            tc::tmem_wait_ld();
-                            uint32_t h[16];
+                        const uint64_t shift2 = pair_f32(shift, shift);
+                        auto weights = [&](auto edge_tag) {
+                            constexpr bool EDGE = decltype(edge_tag)::value;
+                            uint32_t v[2][32];
+                            uint64_t sum[2] = {0, 0};
+                            tmem_ld32(s_at, v[0]);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float x = exp2_approx(fmaf(__uint_as_float(v[j]), cst, shift));
-                                float y = exp2_approx(fmaf(__uint_as_float(v[j + 1]), cst, shift));
-                                if (edge) {
-                                    const int tok = token + q * 32 + j;
-                                    x = tok <= hi && tok >= lo ? x : 0.0f;
-                                    y = tok + 1 <= hi && tok + 1 >= lo ? y : 0.0f;
+                            for (int q = 0; q < kTile / 32; ++q) {
+                                tc::tmem_wait_ld();
+                                if (q + 1 < kTile / 32) tmem_ld32(s_at + (q + 1) * 32, v[(q + 1) & 1]);
+                                const uint32_t (&x)[32] = v[q & 1];
+                                uint32_t h[16];
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    float y, z;
+                                    split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), cst2, shift2), y, z);
+                                    y = exp2_approx(y);
+                                    z = exp2_approx(z);
+                                    if (EDGE) {
+                                        const int tok = token + q * 32 + j;
+                                        y = tok <= hi && tok >= lo ? y : 0.0f;
+                                        z = tok + 1 <= hi && tok + 1 >= lo ? z : 0.0f;
+                                    }
+                                    sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(y, z));
+                                    h[j / 2] = pack_f16(y, z);
                                 }
-                                sum[0] += x;
-                                sum[1] += y;
-                                h[j / 2] = pack_f16(x, y);
+                                // (columns of S that have been read: chunk q of P lies in chunk q / 2)
+                                tmem_st16(s_at + q * 16, h);
                             }
-                            tmem_st16(s_at + q * 16, h);
-                        }
-                        total += sum[0] + sum[1];
+                            float y, z;
+                            split_f32(add_f32x2(sum[0], sum[1]), y, z);
+                            return y + z;
+                        };
+                        total += edge ? weights(std::true_type{}) : weights(std::false_type{});
                         tmem_wait_st();
                     }
                     tc::tc_fence_before();
                     tc::mbar_arrive(&p_full[m]);
                 }
+            }
+            if (begins && !ends) {
+                split = true;
+                if (threadIdx.x == 0) {
+                    KvSplitItem it;
+                    it.q_row = c.seq.q0;
+                    it.row0 = c.rb * kRows;
+                    it.rows = min(kRows, c.seq.nq * p.G - it.row0);
+                    it.h = c.h;
+                    it.last_cta = kv_owner(range.total, range.ctas, c.at + kCost + c.span.tiles - 1);
+                    it.pad = 0;
+                    p.split[blockIdx.x] = it;
+                }
+            }
+            // the next item's Q and its first products, before this one's results are written
+            kt += n;
+            __syncwarp();
+            if (lane == 0) kv_next_item<kRows, kTile, kCost>(p, c);
+            __syncwarp();
+            Row next = {};
+            n = kv_take<kCost>(p, c, range.end);
+            if (n > 0) take_up(next);
+            if (row.active) {
                 wait(&o_full[m], items & 1);
                 ++items;
                 tc::tc_fence_after();
-                if (!dead) {
-                    const float back = pow2(val_exp - 134);
-                    const float by = begins && ends ? (total == 0.0f ? 0.0f : back / total) : back;
-                    const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows + r;
-                    uint16_t* out = p.out + ((c.seq.q0 + i0) * ((int64_t)p.cache.H * p.G) + head) * D;
+            }
+            if (row.active && !dead) {
+                const float back = pow2(val_exp - 134);
+                const float by = begins && ends ? (total == 0.0f ? 0.0f : back / total) : back;
+                const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows + r;
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t v[32];
-                        __syncwarp();
-                        tmem_ld32(o_at + q * 32, v);
-                        tc::tmem_wait_ld();
-                        float x[32];
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t v[32];
+                    __syncwarp();
+                    tmem_ld32(o_at + q * 32, v);
+                    tc::tmem_wait_ld();
+                    float x[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = by == 0.0f ? 0.0f : __uint_as_float(v[j]) * by;
-                        if (!live) {
-                        } else if (begins && ends) {
+                    for (int j = 0; j < 32; ++j) x[j] = by == 0.0f ? 0.0f : __uint_as_float(v[j]) * by;
+                    if (!row.live) {
+                    } else if (begins && ends) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(out + q * 32 + j) =
-                                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
-                                               pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
-                        } else {
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(p.out + row.out + q * 32 + j) =
+                                make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
+                                           pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                    } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4*>(p.part_o + slot * D + q * 32 + j) =
-                                    make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                        }
-                    }
-                    if (live && !(begins && ends))
-                        *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, total);
-                    if (begins && !ends) {
-                        split = true;
-                        if (threadIdx.x == 0) {
-                            KvSplitItem it;
-                            it.q_row = c.seq.q0;
-                            it.row0 = row0;
-                            it.rows = rows;
-                            it.h = c.h;
-                            it.last_cta = kv_owner(range.total, range.ctas, range.begin + done + c.span.tiles - 1);
-                            it.pad = 0;
-                            p.split[blockIdx.x] = it;
-                        }
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(p.part_o + slot * D + q * 32 + j) =
+                                make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                     }
                 }
+                if (row.live && !(begins && ends))
+                    *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, total);
             }
-            kt += n;
-            done += n;
-            __syncwarp();
-            if (lane == 0) kv_next_item<kRows, kTile>(p, c);
-            __syncwarp();
+            row = next;
         }
         if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
     }

@@ -4,9 +4,11 @@
 // sequence (row r of a sequence: query token r / G, query head r % G of the
 // head's group of G); it has as many tiles as its rows see TILE-token tiles
 // of the cache, at least one, so that rows that see nothing are still
-// written.  Items are ordered by sequence, row block and head, and all tiles
-// of all items, end to end, are cut into one equal range per CTA: the work is
-// even whatever the lengths, without the host knowing them.  An item cut
+// written.  Items are ordered by sequence, row block and head; each counts as
+// its tiles plus COST more in front of them (what a CTA spends on beginning
+// and ending an item), and all items, end to end, are cut into one equal range
+// per CTA: the work is even whatever the lengths, without the host knowing
+// them.  An item cut
 // between CTAs is finished from its parts (unnormalised sums, maximum and
 // total of the softmax) by a second kernel, in the order of the CTAs, so the
 // result does not depend on timing.  Every CTA derives its range from the
@@ -120,12 +122,22 @@ struct KvCursor {
     int rb;
     int h;
     KvSpan span;
-    int tile;  // within the item
+    int tile;    // within the item
+    int64_t at;  // where the item begins, in the order of all items
 };
 
-template <int ROWS, int TILE>
+// Tiles of the cursor's item, from its tile on, that lie before `end`; 0: the
+// range is done.
+template <int COST>
+__device__ __forceinline__ int kv_take(const KvAttnParams& p, const KvCursor& c, int64_t end) {
+    if (c.b >= p.B) return 0;
+    return (int)max(min((int64_t)c.span.tiles, end - c.at - COST) - c.tile, (int64_t)0);
+}
+
+template <int ROWS, int TILE, int COST>
 __device__ __forceinline__ void kv_next_item(const KvAttnParams& p, KvCursor& c) {
     c.tile = 0;
+    c.at += c.span.tiles + COST;
     if (++c.h < p.cache.H) return;
     c.h = 0;
     if (++c.rb >= c.blocks) {
@@ -139,16 +151,16 @@ __device__ __forceinline__ void kv_next_item(const KvAttnParams& p, KvCursor& c)
     c.span = kv_span<ROWS, TILE>(p, c.seq, c.rb);
 }
 
-// Tiles of one head over all row blocks of the sequence that each lane
-// holds: a lane alone when its sequence has few blocks, the warp together
+// Tiles and costs of one head over all row blocks of the sequence that each
+// lane holds: a lane alone when its sequence has few blocks, the warp together
 // for sequences of many.
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int COST>
 __device__ __forceinline__ int64_t kv_seq_tiles(const KvAttnParams& p, const KvSeq& s, int blocks) {
     constexpr int kAlone = 4;
     const int lane = threadIdx.x & 31;
     int64_t tiles = 0;
     if (blocks <= kAlone)
-        for (int rb = 0; rb < blocks; ++rb) tiles += kv_span<ROWS, TILE>(p, s, rb).tiles;
+        for (int rb = 0; rb < blocks; ++rb) tiles += kv_span<ROWS, TILE>(p, s, rb).tiles + COST;
     unsigned many = __ballot_sync(0xffffffffu, blocks > kAlone);
     while (many) {
         const int src = __ffs(many) - 1;
@@ -159,7 +171,7 @@ __device__ __forceinline__ int64_t kv_seq_tiles(const KvAttnParams& p, const KvS
         o.len = __shfl_sync(0xffffffffu, s.len, src);
         const int n = __shfl_sync(0xffffffffu, blocks, src);
         int64_t sum = 0;
-        for (int rb = lane; rb < n; rb += 32) sum += kv_span<ROWS, TILE>(p, o, rb).tiles;
+        for (int rb = lane; rb < n; rb += 32) sum += kv_span<ROWS, TILE>(p, o, rb).tiles + COST;
 #pragma unroll
         for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         if (lane == src) tiles = sum;
@@ -171,23 +183,23 @@ __device__ __forceinline__ int64_t kv_seq_tiles(const KvAttnParams& p, const KvS
 struct KvLocate {
     int64_t warp_sum[32];
     int64_t total;
-    int64_t at;      // tiles before sequence b
+    int64_t at;      // where sequence b begins
     int64_t b;
 };
 
 struct KvRange {
-    int64_t total, begin, end;  // tiles of all items; this CTA's range
+    int64_t total, begin, end;  // tiles and costs of all items; this CTA's range
     int64_t ctas;               // CTAs that have a range (those behind have none)
 };
 
-// First tile of CTA i of n.
+// Where the range of CTA i of n begins.
 __device__ __forceinline__ int64_t kv_cut(int64_t total, int64_t i, int64_t n) {
     return (total / n) * i + (total % n) * i / n;
 }
 
 // This CTA's range and the cursor at its beginning.  Called by all THREADS
 // threads of the block (whole warps).
-template <int ROWS, int TILE, int THREADS>
+template <int ROWS, int TILE, int COST, int THREADS>
 __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm, KvCursor& c) {
     constexpr int kWarps = THREADS / 32;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -208,7 +220,7 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
                     s = kv_sequence(p, b);
                     blocks = kv_blocks<ROWS>(p, s);
                 }
-                tiles = kv_seq_tiles<ROWS, TILE>(p, s, blocks) * p.cache.H;
+                tiles = kv_seq_tiles<ROWS, TILE, COST>(p, s, blocks) * p.cache.H;
                 kept = tiles;
             }
             int64_t upto = tiles;  // inclusive sum over the warp
@@ -240,6 +252,7 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
     }
     __syncthreads();
     c = {};
+    c.b = p.B;
     if (r.begin >= r.end) return r;
     c.b = sm.b;
     c.seq = kv_sequence(p, c.b);
@@ -248,7 +261,7 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
     int64_t left = r.begin - sm.at;
     for (int rb0 = 0;; rb0 += 32) {
         const int rb = rb0 + lane;
-        const int64_t tiles = rb < c.blocks ? (int64_t)kv_span<ROWS, TILE>(p, c.seq, rb).tiles * p.cache.H : 0;
+        const int64_t tiles = rb < c.blocks ? (int64_t)(kv_span<ROWS, TILE>(p, c.seq, rb).tiles + COST) * p.cache.H : 0;
         int64_t upto = tiles;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -270,12 +283,14 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
         }
     }
     c.span = kv_span<ROWS, TILE>(p, c.seq, c.rb);
-    c.h = (int)(left / c.span.tiles);
-    c.tile = (int)(left - (int64_t)c.h * c.span.tiles);
+    c.h = (int)(left / (c.span.tiles + COST));
+    left -= (int64_t)c.h * (c.span.tiles + COST);
+    c.at = r.begin - left;
+    c.tile = (int)max(left - COST, (int64_t)0);
     return r;
 }
 
-// The CTA whose range holds tile x.
+// The CTA whose range holds place x.
 __device__ __forceinline__ int kv_owner(int64_t total, int64_t n, int64_t x) {
     int64_t i = (int64_t)((double)x * (double)n / (double)total);
     i = min(max(i, (int64_t)0), n - 1);
