@@ -77,13 +77,45 @@ struct Cfg {
     static constexpr int kSmem = kOffRawV + kRawV + 1024;  // (aligned to 1024 by hand)
 };
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
+// MMAs and commits of the lane with issue != 0.  The others run along: in a
+// branch of one lane the descriptors could not stay in uniform registers.
+template <int A_AT, int B_AT>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t issue) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 ta, tb;\n\t.reg .b64 da, db;\n\t"
+        "add.u32 ta, %1, %7;\n\t"
+        "add.u32 tb, %2, %8;\n\t"
+        "mov.b64 da, {ta, %3};\n\t"
+        "mov.b64 db, {tb, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(issue), "n"(A_AT), "n"(B_AT)
+        : "memory");
+}
+
+template <int A_AT, int B_AT>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t high, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t issue) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 ta, tb;\n\t.reg .b64 db;\n\t"
+        "add.u32 ta, %1, %7;\n\t"
+        "add.u32 tb, %2, %8;\n\t"
+        "mov.b64 db, {tb, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(issue), "n"(A_AT), "n"(B_AT)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_mma(uint64_t* bar, uint32_t issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+        "r"(issue)
         : "memory");
 }
 
@@ -428,29 +460,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         uint32_t kt = 0, items[2] = {0, 0}, steps[2] = {0, 0};
         // descriptors count in units of 16 bytes: 2 a step of 16 elements, and
         // the rest of a row's swizzle atoms behind the first 64 elements
-        const uint64_t q_base = tc::sw128_desc(smem_at + C::kOffQ), k_base = tc::sw128_desc(smem_at + C::kOffK);
-        const uint64_t v_base = tc::sw128_desc(smem_at + C::kOffV);
+        const uint32_t q_base = (uint32_t)tc::sw128_desc(smem_at + C::kOffQ);
+        const uint32_t k_base = (uint32_t)tc::sw128_desc(smem_at + C::kOffK);
+        const uint32_t v_base = (uint32_t)tc::sw128_desc(smem_at + C::kOffV);
+        const uint32_t high = (uint32_t)(tc::sw128_desc(smem_at) >> 32);
         auto qk = [&](int m, uint32_t tile) {
-            if (dead || lane != 0) return;
-            const uint64_t a = q_base + m * (128 * D * 2 / 16);
-            const uint64_t b = k_base + (tile % kKStages) * (C::kKTile / 16);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                tc::mma_f16(tmem + m * kTile, a + ((k / 4) * (128 * 128 / 16) + (k % 4) * 2),
-                            b + ((k / 4) * (kTile * 128 / 16) + (k % 4) * 2), s_desc, k != 0);
-            tc::mma_commit(&s_full[m]);
+            const uint32_t a = q_base + m * (128 * D * 2 / 16);
+            const uint32_t b = k_base + (tile % kKStages) * (C::kKTile / 16);
+            const uint32_t d = tmem + m * kTile, issue = !dead && lane == 0;
+            __syncwarp();
+            mma_ss<0, 0>(d, a, b, high, s_desc, 0, issue);
+            mma_ss<2, 2>(d, a, b, high, s_desc, 1, issue);
+            mma_ss<4, 4>(d, a, b, high, s_desc, 1, issue);
+            mma_ss<6, 6>(d, a, b, high, s_desc, 1, issue);
+            if constexpr (D == 128) {
+                constexpr int kNext = 128 * 128 / 16;  // the second 64 channels: rows of 128 tokens or queries
+                mma_ss<kNext, kNext>(d, a, b, high, s_desc, 1, issue);
+                mma_ss<kNext + 2, kNext + 2>(d, a, b, high, s_desc, 1, issue);
+                mma_ss<kNext + 4, kNext + 4>(d, a, b, high, s_desc, 1, issue);
+                mma_ss<kNext + 6, kNext + 6>(d, a, b, high, s_desc, 1, issue);
+            }
+            commit_mma(&s_full[m], issue);
         };
         auto pv = [&](int m, uint32_t tile, bool first) {
-            if (dead || lane != 0) return;
-            const uint64_t b = v_base + (tile % C::kVStages) * (C::kKTile / 16);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                mma_f16_ts(tmem + 256 + m * D, tmem + m * kTile + k * 8, b + ((k / 4) * (D * 128 / 16) + (k % 4) * 2),
-                           o_desc, !first || k != 0);
+            const uint32_t a = tmem + m * kTile;
+            const uint32_t b = v_base + (tile % C::kVStages) * (C::kKTile / 16);
+            const uint32_t d = tmem + 256 + m * D, issue = !dead && lane == 0;
+            constexpr int kNext = D * 128 / 16;  // the second 64 tokens
+            __syncwarp();
+            mma_ts<0, 0>(d, a, b, high, o_desc, !first, issue);
+            mma_ts<8, 2>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<16, 4>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<24, 6>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<32, kNext>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<40, kNext + 2>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<48, kNext + 4>(d, a, b, high, o_desc, 1, issue);
+            mma_ts<56, kNext + 6>(d, a, b, high, o_desc, 1, issue);
         };
-        auto commit = [&](uint64_t* bar) {
-            if (!dead && lane == 0) tc::mma_commit(bar);
-        };
+        auto commit = [&](uint64_t* bar) { commit_mma(bar, !dead && lane == 0); };
         while (const int n = kv_take<kCost>(p, c, found.end)) {
             const int rows = min(kRows, c.seq.nq * p.G - c.rb * kRows);
             const int tiles_m = rows > 128 ? 2 : 1;
