@@ -247,8 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     bool dead = false;
     // Waits of a whole warp; after one that gave up no work is done any more,
     // but every loop and barrier runs to its end.
+    // (The test comes before the call: a barrier that is passed already, the
+    // common case of the MMA warp, costs 40 cycles and not 170.)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead) dead = !tc::warp_wait(bar, parity, &abort_flag, p.err);
+        if (dead || __all_sync(0xffffffffu, tc::mbar_test(tc::smem_u32(bar), parity))) return;
+        dead = !tc::warp_wait(bar, parity, &abort_flag, p.err);
     };
 
     if (warp == kCopyWarp) {
@@ -510,15 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
             }
             commit(&k_empty[kt % kKStages]);
             for (int i = 0; i < n; ++i, ++kt) {
+                // (neither waits for a product that is still to be issued)
+                wait(&v_full[kt % C::kVStages], (kt / C::kVStages) & 1);
+                if (i + 1 < n) wait(&k_full[(kt + 1) % kKStages], ((kt + 1) / kKStages) & 1);
                 for (int m = 0; m < tiles_m; ++m) {
                     wait(&p_full[m], steps[m] & 1);
                     ++steps[m];
-                    if (m == 0) wait(&v_full[kt % C::kVStages], (kt / C::kVStages) & 1);
                     tc::tc_fence_after();
                     pv(m, kt, i == 0);
                     if (i + 1 < n) {
-                        if (m == 0) wait(&k_full[(kt + 1) % kKStages], ((kt + 1) / kKStages) & 1);
-                        tc::tc_fence_after();
                         qk(m, kt + 1);
                     } else {
                         commit(&o_full[m]);
