@@ -12,12 +12,13 @@
 // with the scales outside.  Centred, because sums of uncentred codes over a
 // long context would be far larger than the result that is left of them.
 //
-// Precision: logits, maxima, totals and accumulators in fp32.  fp16 holds q
-// exactly after a power of two per row has put its largest element near 2^8
-// (elements 2^32 times smaller round), and w_j s_j to 2^-11 after a power of
-// two S per warp, raised as larger scales appear, has put the largest
-// possible weight at 2^14: eight times finer than bf16, and weights down to
-// 2^-38 of the largest are kept.
+// Precision: logits, totals and accumulators in fp32.  fp16 holds q exactly
+// after a power of two per row has put its largest element near 2^8 (elements
+// 2^32 times smaller round), and w_j s_j to 2^-11 after a power of two S per
+// warp, raised as larger value scales appear, has put s_j / S below 1: eight
+// times finer than bf16.  The weights are relative to a reference that a row's
+// logits exceed by 2^5 at most (w_j s_j / S is held times 2^10, so it ends at
+// 2^15); weights down to 2^-34 of the reference are kept.
 //
 // Bound by the bytes of the cache: 136 bytes a token and head (4 bits, 128
 // channels, K and V).  Against them stands the unpacking, which is bound by
@@ -58,6 +59,8 @@ constexpr int kWarps = 4;                    // consumer warps
 constexpr int kWarpTokens = kTile / kWarps;  // tokens of a stage per warp
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kStages = 3;
+constexpr float kSlack = 5.0f;    // a logit may exceed what the weights are relative to by this (log2)
+constexpr int kValueShift = 10;   // w s / S is held times 2^this: at most 2^15 in fp16
 constexpr int kCost = 1;  // tiles that beginning and ending an item counts
 constexpr int64_t kFewRows = 32;  // query rows of a sequence's head group up to which this kernel runs
 
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = max((int)(top >> 23), 9) - 127;
-            const float f = pow2(8 - e);
+            const float f = p.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const float unit = pow2(e - 8) * p.scale_log2;
+            const float unit = pow2(e - 8) * fabsf(p.scale_log2);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int from = 4 * (2 * t + y);  // a lane that loaded row 2t + y
@@ -280,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 
         // O^T: channels g D/8 + 2i (+ 1) x rows 2t, 2t + 1 (+ 8)
         float o[kOut][HALVES][4];
-        // running maximum; this lane's share of the total and of sum w (low + z s)
+        // what the weights are relative to (a logit; at most kSlack below the row's
+        // maximum); this lane's share of the total and of sum w (low + z s)
         float m[HALVES][2], l[HALVES][2], z[HALVES][2];
-        int unit = 14;  // S = 2^(unit - 126) is above every value scale so far
+        int unit = kValueShift;  // S = 2^(unit - 126) is above every value scale so far
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) {
 #pragma unroll
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                             for (int y = 0; y < 4; ++y) o[j][x][y] *= f;
                 }
-                factors[warp][lane] = make_float4(ks, fmaf(ks, kCentre<BITS>, kv_low(pk)), vs * pow2(140 - unit),
+                factors[warp][lane] = make_float4(ks, fmaf(ks, kCentre<BITS>, kv_low(pk)), vs * pow2(kValueShift + 126 - unit),
                                                   fmaf(vs, kCentre<BITS>, kv_low(pv)));
                 __syncwarp();
             }
@@ -356,27 +360,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float& a = s[i / 2][x][2 * (i & 1) + y];
-                        a = fmaf(a, f[i].x, f[i].y * q_sum[x][y]) * q_unit[x][y];
+                        a = fmaf(a, f[i].x, f[i].y * q_sum[x][y]);
                         const int tok = token + row_g + 8 * i;
                         if (EDGE && (tok > hi[x][y] || tok < lo[x][y])) a = -INFINITY;
                         top[x][y] = fmaxf(top[x][y], a);
                     }
                 }
-            // softmax weights against the running maximum
-            bool grew = false;
+            // softmax weights; the reference is raised only when a logit exceeds
+            // it by kSlack, which spares the other steps the sums' rescaling and
+            // the exchange between the lanes of a row
+            bool above = false;
 #pragma unroll
             for (int x = 0; x < HALVES; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                    for (int k = 4; k < 32; k <<= 1) top[x][y] = fmaxf(top[x][y], __shfl_xor_sync(0xffffffffu, top[x][y], k));
-                    grew |= top[x][y] > m[x][y];
+                    top[x][y] *= q_unit[x][y];
+                    above |= top[x][y] > m[x][y] + kSlack;  // (the first time: from -infinity)
                 }
-            if (__any_sync(0xffffffffu, grew)) {
+            if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1)
+                            top[x][y] = fmaxf(top[x][y], __shfl_xor_sync(0xffffffffu, top[x][y], k));
                         const float to = fmaxf(m[x][y], top[x][y]);
                         const float by = to == -INFINITY ? 1.0f : exp2_approx(m[x][y] - to);
                         m[x][y] = to;
@@ -401,17 +409,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const float a = s[i / 2][x][2 * (i & 1) + y];
-                        const float w = exp2_approx(a - shift[y]);
-                        l[x][y] += w;
                         // a token a row does not see may hold anything: no product with it
-                        const bool skip = EDGE && a == -INFINITY;
+                        const bool skip = EDGE && (token + row_g + 8 * i > hi[x][y] || token + row_g + 8 * i < lo[x][y]);
+                        float w = exp2_approx(fmaf(a, q_unit[x][y], -shift[y]));
+                        if (skip) w = 0.0f;
+                        l[x][y] += w;
                         z[x][y] = skip ? z[x][y] : fmaf(w, f[i].w, z[x][y]);
                         wgt[y] = skip ? 0.0f : w * f[i].z;
                     }
                     pr[i][x] = transpose8(pack_f16(wgt[0], wgt[1]));
                 }
             }
-            // o += (w s 2^14 / S) (codes of V)
+            // o += (w s 2^kValueShift / S) (codes of V)
             const uint8_t* vals = st + C::kCodes + warp * kWarpTokens * C::kRowBytes + g * (kValWords * 4);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                 for (int j = 0; j < kOut; ++j)
 #pragma unroll
                     for (int k = y; k < 4; k += 2)
-                        o[j][x][k] = f == 0.0f ? 0.0f : fmaf(o[j][x][k], pow2(unit - 140), z[x][y]) * f;
+                        o[j][x][k] = f == 0.0f ? 0.0f : fmaf(o[j][x][k], pow2(unit - 126 - kValueShift), z[x][y]) * f;
             }
         // a lane holds D / 8 channels from g D / 8 on of rows 2t and 2t + 1 (+ 8)
         const int at = g * (D / 8) + 4 * (g * (D / 8) / 32);
@@ -562,78 +571,124 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
 }
 
-// Joins the parts of an item cut between CTAs, in their order: a group of
-// warps per row, the parts shared out among the group.
-constexpr int kJoinWarps = 32;
+// Joins the parts of an item cut between CTAs, always in the same order.  A
+// block takes 8 rows: of an item of few parts a warp each, of more the warps
+// share the parts (each warp all 8 rows of a part, so that 8 loads are under
+// way) and then add up.  (Blocks of 8 warps: most CTAs have an item of two or
+// three parts or none, and small blocks run side by side.)
+constexpr int kJoinWarps = 8;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnParams p) {
-    constexpr int kPer = ROWS < kJoinWarps ? kJoinWarps / ROWS : 1;  // warps per row
-    constexpr int kVec = D / 32;             // channels per lane
-    __shared__ float part[kJoinWarps][D];
+    constexpr int kVec = D / 32;  // channels per lane
+    __shared__ float sums[kJoinWarps][kJoinWarps][D];  // [warp][row]
+    __shared__ float totals[kJoinWarps][kJoinWarps];
     pdl_wait();
     const KvSplitItem it = p.split[blockIdx.x];
-    if (it.rows == 0) return;
+    const int r0 = blockIdx.y * kJoinWarps;
+    if (r0 >= it.rows) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int r = blockIdx.y * kJoinWarps + warp / kPer, sub = warp % kPer;
     const int first = blockIdx.x, count = it.last_cta - first + 1;
     // part k: the beginning (slot 1 of the first CTA), then slot 0 of the following ones
-    auto slot = [&](int k) { return ((int64_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r; };
-    float top = -INFINITY, total = 0.0f, acc[kVec] = {};
-    if (r < it.rows) {
-        for (int k = lane; k < count; k += 32) top = fmaxf(top, p.part_ml[slot(k) * 2]);
+    auto slot = [&](int k, int r) { return ((int64_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r; };
+    auto ml = [&](int k, int r) { return *reinterpret_cast<const float2*>(p.part_ml + slot(k, r) * 2); };
+    auto store = [&](int r, const float (&x)[kVec], float inv) {
+        const int i = (it.row0 + r) / p.G;
+        const int head = it.h * p.G + it.row0 + r - i * p.G;
+        uint16_t* dst = p.out + ((it.q_row + i) * ((int64_t)p.cache.H * p.G) + head) * D + lane * kVec;
+        if constexpr (kVec == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x[0] * inv, x[1] * inv);
+    };
+    auto fetch = [&](int k, int r, float (&x)[kVec]) {
+        const float* src = p.part_o + slot(k, r) * D + lane * kVec;
+        if constexpr (kVec == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[0] = v.x;
+            x[1] = v.y;
+            x[2] = v.z;
+            x[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[0] = v.x;
+            x[1] = v.y;
+        }
+    };
+    // a part's weight; 0 where it saw nothing
+    auto weigh = [](float2 x, float top) { return x.y == 0.0f ? 0.0f : exp2_approx(x.x - top); };
+    if (count <= kJoinWarps) {
+        const int r = r0 + warp;
+        if (r >= it.rows) return;
+        float2 x[kJoinWarps];
+        float top = -INFINITY, total = 0.0f, acc[kVec] = {};
 #pragma unroll
-        for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        // a part's weight; 0 where it saw nothing
-        auto weight = [&](float2 ml) { return ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - top); };
-        for (int k = lane; k < count; k += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2);
-            total += ml.y * weight(ml);
+        for (int k = 0; k < kJoinWarps; ++k) {
+            x[k] = k < count ? ml(k, r) : make_float2(-INFINITY, 0.0f);
+            top = fmaxf(top, x[k].x);
         }
 #pragma unroll
-        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-#pragma unroll 4
-        for (int k = sub; k < count; k += kPer) {
-            const float f = weight(*reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2));
-            const float* src = p.part_o + slot(k) * D + lane * kVec;
-            if constexpr (kVec == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-                acc[2] = fmaf(v.z, f, acc[2]);
-                acc[3] = fmaf(v.w, f, acc[3]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(src);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-            }
+        for (int k = 0; k < kJoinWarps; ++k) {
+            if (k >= count) break;
+            const float f = weigh(x[k], top);
+            total += x[k].y * f;
+            float v[kVec];
+            fetch(k, r, v);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[i] = fmaf(v[i], f, acc[i]);
+        }
+        store(r, acc, total == 0.0f ? 0.0f : 1.0f / total);
+        return;
+    }
+    // the rows' references: lane l looks at row r0 + l % 8, parts l / 8, l / 8 + 4, ..
+    const int my_row = r0 + lane % kJoinWarps;
+    float top = -INFINITY;
+    if (my_row < it.rows)
+        for (int k = lane / kJoinWarps; k < count; k += 4) top = fmaxf(top, ml(k, my_row).x);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    float acc[kJoinWarps][kVec] = {}, total = 0.0f;  // (the total: of row my_row)
+    for (int k = warp; k < count; k += kJoinWarps) {
+        float weight = 0.0f;  // of the part in row my_row
+        if (my_row < it.rows) {
+            const float2 x = ml(k, my_row);
+            weight = weigh(x, top);
+            total += x.y * weight;
+        }
+        float v[kJoinWarps][kVec];
+#pragma unroll
+        for (int j = 0; j < kJoinWarps; ++j) {
+            if (r0 + j < it.rows) fetch(k, r0 + j, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinWarps; ++j) {
+            const float f = __shfl_sync(0xffffffffu, weight, j);
+            if (r0 + j >= it.rows) continue;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[j][i] = fmaf(v[j][i], f, acc[j][i]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) part[warp][lane * kVec + i] = acc[i];
+    for (int j = 0; j < kJoinWarps; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sums[warp][j][lane * kVec + i] = acc[j][i];
+    if (lane < kJoinWarps) totals[warp][lane] = total;
     __syncthreads();
-    if (sub != 0 || r >= it.rows) return;
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const int i = (it.row0 + r) / p.G;
-    const int head = it.h * p.G + it.row0 + r - i * p.G;
-    uint16_t* dst = p.out + ((it.q_row + i) * ((int64_t)p.cache.H * p.G) + head) * D + lane * kVec;
-    float v[kVec];
+    const int r = r0 + warp;
+    if (r >= it.rows) return;
+    float out[kVec] = {}, all = 0.0f;
+    for (int w = 0; w < kJoinWarps; ++w) {
+        all += totals[w][warp];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        v[j] = acc[j];
-        for (int w = 1; w < kPer; ++w) v[j] += part[warp + w][lane * kVec + j];
-        v[j] *= inv;
+        for (int i = 0; i < kVec; ++i) out[i] += sums[w][warp][lane * kVec + i];
     }
-    if constexpr (kVec == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0], v[1]);
+    store(r, out, all == 0.0f ? 0.0f : 1.0f / all);
 }
 
 template <int D, int ROWS>
 cudaError_t launch_join(const KvAttnParams& p, int64_t ctas, const LaunchEnv& env) {
-    return launch_kernel(kv_join_kernel<D, ROWS>, dim3((unsigned)ctas, std::max(ROWS / kJoinWarps, 1)),
-                         dim3(kJoinWarps * 32), 0, env.stream, kNoCluster, p);
+    return launch_kernel(kv_join_kernel<D, ROWS>, dim3((unsigned)ctas, ROWS / kJoinWarps), dim3(kJoinWarps * 32), 0,
+                         env.stream, kNoCluster, p);
 }
 
 // How a call runs: the query rows of a block, the CTAs, and whether an item

@@ -13,8 +13,10 @@
 //
 // Both are bound by bytes: a token of 8 heads x 128 channels is 4 KB of bf16
 // and 1 KB of 4-bit rows.  A thread takes 8 channels (one 16-byte vector of
-// bf16), D / 8 neighbouring lanes a row; minimum and maximum go through
-// shuffles, so a row is read once and nothing is staged.
+// bf16) of several rows, D / 8 neighbouring lanes a row; minimum and maximum go
+// through shuffles, so a row is read once and nothing is staged.  The rows of a
+// thread are loaded together, and keys and values beside their slots: one row
+// at a time, behind its slot, reached a third of the bandwidth.
 
 #include <cuda_runtime.h>
 
@@ -25,49 +27,104 @@ namespace i8ql {
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr int kKvRows = 4;  // rows per thread
 
 struct KvMoveParams {
     KvCache cache;
     const int64_t* slots;
-    uint32_t rows;  // T * 2 * H
+    uint32_t rows;   // T * 2 * H < 2^31
+    uint32_t two_h;  // rows of a token
+    uint32_t inv;    // floor(2^32 / two_h)
     int64_t slot_limit;
     unsigned* err;
 };
 
-// The row this thread works on; false when it has none.  *t is its token,
-// *index its row of the cache (or -1: a token without a slot).
+// A row of keys or values that a thread works on.
+struct KvMoveRow {
+    bool there;
+    uint32_t t;  // token
+    int kv, h;   // key (0) or value (1), head
+};
+
 template <int D>
-__device__ __forceinline__ bool locate_row(const KvMoveParams& p, uint32_t* t, int* kv, int* h, int64_t* index) {
-    constexpr int kLanes = D / 8;
-    const uint32_t row = blockIdx.x * (kKvThreads / kLanes) + threadIdx.x / kLanes;
-    if (row >= p.rows) return false;
-    const uint32_t two_h = 2u * (uint32_t)p.cache.H;
-    *t = row / two_h;
-    const uint32_t in_token = row - *t * two_h;
-    *kv = in_token >= (uint32_t)p.cache.H;
-    *h = (int)in_token - (*kv ? p.cache.H : 0);
-    const int64_t slot = __ldg(p.slots + *t);
-    *index = -1;
-    if (slot >= p.slot_limit) {
-        record_fault(p.err, kErrBitBadIndex);
-    } else if (slot >= 0) {
-        const int64_t page = slot >> p.cache.page_shift;
-        *index = kv_row(p.cache, page, *kv, *h, (int)(slot - (page << p.cache.page_shift)));
+__device__ __forceinline__ KvMoveRow move_row(const KvMoveParams& p, int i) {
+    constexpr int kGroups = kKvThreads / (D / 8);  // rows side by side in a block
+    const uint32_t row = (blockIdx.x * kKvRows + i) * kGroups + threadIdx.x / (D / 8);
+    KvMoveRow r;
+    r.there = row < p.rows;
+    // row / two_h: the estimate is at most one too small (row < 2^31)
+    r.t = __umulhi(row, p.inv);
+    uint32_t in_token = row - r.t * p.two_h;
+    if (in_token >= p.two_h) {
+        ++r.t;
+        in_token -= p.two_h;
     }
-    return true;
+    r.kv = in_token >= (uint32_t)p.cache.H;
+    r.h = (int)in_token - (r.kv ? p.cache.H : 0);
+    return r;
 }
 
-// rint(fl32(t / s)) for 0 <= t <= L s: through the correctly rounded
-// reciprocal r, whose product is within 255 * 3 * 2^-24 < 2^-14 of the
-// quotient, and through the IEEE division where that lies next to a
-// half-integer (or r overflowed, s being subnormal).
-template <int BITS>
-__device__ __forceinline__ uint32_t kv_code(float t, float s, float r) {
-    constexpr float kNear = 6.103515625e-05f;  // 2^-14
-    float u = __fmul_rn(t, r);
-    const float d = __fsub_rn(u, rintf(u));
-    if (!(fabsf(d) <= 0.5f - kNear)) u = __fdiv_rn(t, s);
-    return min(__float2uint_rn(u), (1u << BITS) - 1u);
+// Its row of the cache, or -1.
+__device__ __forceinline__ int64_t cache_row(const KvMoveParams& p, const KvMoveRow& r, int64_t slot) {
+    if (!r.there || slot < 0) return -1;
+    if (slot >= p.slot_limit) {
+        record_fault(p.err, kErrBitBadIndex);
+        return -1;
+    }
+    const int64_t page = slot >> p.cache.page_shift;
+    return kv_row(p.cache, page, r.kv, r.h, (int)(slot - (page << p.cache.page_shift)));
+}
+
+// (lo, -hi) of two of them, as bf16 pairs: one minimum does both.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The codes rint(fl32(t / s)) of t = x - lo, 0 <= t <= L s, in the low byte of
+// each word.  bf16 values tie often (their differences are multiples of few
+// units), so the quotient has to be the correctly rounded one: with r the
+// correctly rounded reciprocal, q = fl(t r) is within an ulp, the remainder
+// e = t - q s is exact, and fl(q + e r) is the correctly rounded quotient
+// (Markstein's theorem, IBM J. Res. Dev. 34, 1990; the divisor's mantissa, 8
+// bits, is not all ones).  s outside 2^-90 .. 2^90, where the remainder could
+// leave the normal range, takes the division itself.  Adding 1.5 * 2^23 leaves
+// the rounded integer, ties to even, in the low mantissa bits.  Two values per
+// instruction, each with its own IEEE rounding.
+__device__ __forceinline__ void kv_codes(const uint4& w, float lo, float s, uint32_t (&b)[8]) {
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    if (s >= 0x1p-90f && s <= 0x1p90f) {
+        const float r = __frcp_rn(s);
+        uint64_t lo2, r2, ns2, magic2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(lo2) : "f"(lo));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(r2) : "f"(r));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ns2) : "f"(-s));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(magic2) : "f"(kRoundMagic));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("{\n\t.reg .b64 t, q, e;\n\t"
+                "mov.b64 t, {%2, %3};\n\t"
+                "sub.rn.f32x2 t, t, %4;\n\t"
+                "mul.rn.f32x2 q, t, %5;\n\t"
+                "fma.rn.f32x2 e, q, %6, t;\n\t"
+                "fma.rn.f32x2 q, e, %5, q;\n\t"
+                "add.rn.f32x2 q, q, %7;\n\t"
+                "mov.b64 {%0, %1}, q;\n\t}"
+                : "=r"(b[2 * i]), "=r"(b[2 * i + 1])
+                : "f"(lo_bf16(words[i])), "f"(hi_bf16(words[i])), "l"(lo2), "l"(r2), "l"(ns2), "l"(magic2));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[2 * i] = min(__float2uint_rn(__fdiv_rn(__fsub_rn(lo_bf16(words[i]), lo), s)), 255u);
+            b[2 * i + 1] = min(__float2uint_rn(__fdiv_rn(__fsub_rn(hi_bf16(words[i]), lo), s)), 255u);
+        }
+    }
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 template <int D, int BITS>
@@ -75,88 +132,116 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __
                                                               const uint16_t* __restrict__ v, int64_t k_stride,
                                                               int64_t v_stride, KvMoveParams p) {
     constexpr int kLanes = D / 8;
-    pdl_wait();
-    uint32_t t;
-    int kv, h;
-    int64_t index;
-    // rows are whole lane groups, so a group leaves together and the shuffles
-    // below only cross lanes of one row
-    const bool live = locate_row<D>(p, &t, &kv, &h, &index) && index >= 0;
     const int lane = threadIdx.x % kLanes;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) {
-        const uint16_t* src = (kv ? v + t * v_stride : k + t * k_stride) + (int64_t)h * D + lane * 8;
-        w = __ldg(reinterpret_cast<const uint4*>(src));
-    }
-    const float x[8] = {lo_bf16(w.x), hi_bf16(w.x), lo_bf16(w.y), hi_bf16(w.y),
-                        lo_bf16(w.z), hi_bf16(w.z), lo_bf16(w.w), hi_bf16(w.w)};
-    float lo = x[0], hi = x[0];
+    KvMoveRow row[kKvRows];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+    for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
+    pdl_wait();
+    uint4 w[kKvRows];
+    int64_t slot[kKvRows];
+#pragma unroll
+    for (int i = 0; i < kKvRows; ++i) {
+        const KvMoveRow& r = row[i];
+        w[i] = make_uint4(0, 0, 0, 0);
+        slot[i] = -1;
+        if (r.there) {
+            const uint16_t* src = (r.kv ? v + r.t * v_stride : k + r.t * k_stride) + (int64_t)r.h * D + lane * 8;
+            w[i] = __ldg(reinterpret_cast<const uint4*>(src));
+            slot[i] = __ldg(p.slots + r.t);
+        }
     }
 #pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    }
-    if (!live) return;
-    constexpr float kLevels = (float)((1 << BITS) - 1);
-    const float ratio = __fdiv_rn(__fsub_rn(hi, lo), kLevels);  // >= 0
-    const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
-    const float s = __uint_as_float(s_bits);
-    const float r = __frcp_rn(s);
-    uint32_t c[8];
+    for (int i = 0; i < kKvRows; ++i) {
+        // (lo, -hi): over the thread's pairs, over a pair's halves, over the row's
+        // lanes (a row is a whole group of lanes; all lanes of the warp shuffle)
+        constexpr uint32_t kSigns = 0x80008000u;
+        const uint32_t least = min_bf16x2(min_bf16x2(w[i].x, w[i].y), min_bf16x2(w[i].z, w[i].w));
+        const uint32_t most = min_bf16x2(min_bf16x2(w[i].x ^ kSigns, w[i].y ^ kSigns),
+                                         min_bf16x2(w[i].z ^ kSigns, w[i].w ^ kSigns));
+        uint32_t ends = min_bf16x2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = s > 0.0f ? kv_code<BITS>(__fsub_rn(x[i], lo), s, r) : 0u;
-    if constexpr (BITS == 4) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) word |= c[i] << (4 * i);
-        reinterpret_cast<uint32_t*>(p.cache.codes + index * (D / 2))[lane] = word;
-    } else {
-        uint2 words;
-        words.x = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-        words.y = c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24);
-        reinterpret_cast<uint2*>(p.cache.codes + index * D)[lane] = words;
+        for (int m = 1; m < kLanes; m <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+        const int64_t index = cache_row(p, row[i], slot[i]);
+        if (index < 0) continue;
+        const float lo = lo_bf16(ends), hi = -hi_bf16(ends);
+        constexpr float kLevels = (float)((1 << BITS) - 1);
+        const float ratio = __fdiv_rn(__fsub_rn(hi, lo), kLevels);  // >= 0
+        const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
+        const float s = __uint_as_float(s_bits);
+        uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (s > 0.0f) kv_codes(w[i], lo, s, c);
+        const uint32_t c0 = low_bytes(c[0], c[1], c[2], c[3]), c1 = low_bytes(c[4], c[5], c[6], c[7]);
+        if constexpr (BITS == 4) {
+            const uint32_t n0 = (c0 & 0x000f000fu) | ((c0 >> 4) & 0x00f000f0u);
+            const uint32_t n1 = (c1 & 0x000f000fu) | ((c1 >> 4) & 0x00f000f0u);
+            reinterpret_cast<uint32_t*>(p.cache.codes + index * (D / 2))[lane] = __byte_perm(n0, n1, 0x6420);
+        } else {
+            reinterpret_cast<uint2*>(p.cache.codes + index * D)[lane] = make_uint2(c0, c1);
+        }
+        if (lane == 0) p.cache.params[index] = (s_bits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
     }
-    if (lane == 0) p.cache.params[index] = (s_bits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
 template <int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                              KvMoveParams p) {
-    constexpr int kLanes = D / 8;
+    const int lane = threadIdx.x % (D / 8);
+    KvMoveRow row[kKvRows];
+#pragma unroll
+    for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
     pdl_wait();
-    uint32_t t;
-    int kv, h;
-    int64_t index;
-    if (!locate_row<D>(p, &t, &kv, &h, &index)) return;
-    const int lane = threadIdx.x % kLanes;
-    uint32_t out[4] = {0, 0, 0, 0};
-    if (index >= 0) {
-        uint32_t c[8];
-        if constexpr (BITS == 4) {
-            const uint32_t word = reinterpret_cast<const uint32_t*>(p.cache.codes + index * (D / 2))[lane];
+    int64_t index[kKvRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = (word >> (4 * i)) & 15u;
-        } else {
-            const uint2 words = reinterpret_cast<const uint2*>(p.cache.codes + index * D)[lane];
+    for (int i = 0; i < kKvRows; ++i) index[i] = row[i].there ? __ldg(p.slots + row[i].t) : -1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = ((i < 4 ? words.x : words.y) >> (8 * (i & 3))) & 255u;
-        }
-        const uint32_t param = p.cache.params[index];
-        const float s = kv_scale(param), lo = kv_low(param);
+    for (int i = 0; i < kKvRows; ++i) index[i] = cache_row(p, row[i], index[i]);
+    uint2 codes[kKvRows];
+    uint32_t param[kKvRows];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float a = __fmaf_rn(s, __uint2float_rn(c[i]), lo), b = __fmaf_rn(s, __uint2float_rn(c[i + 1]), lo);
-            out[i / 2] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) |
-                         ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
+    for (int i = 0; i < kKvRows; ++i) {
+        codes[i] = make_uint2(0, 0);
+        param[i] = 0;  // stands for 0
+        if (index[i] >= 0) {
+            if constexpr (BITS == 4)
+                codes[i].x = reinterpret_cast<const uint32_t*>(p.cache.codes + index[i] * (D / 2))[lane];
+            else
+                codes[i] = reinterpret_cast<const uint2*>(p.cache.codes + index[i] * D)[lane];
+            param[i] = p.cache.params[index[i]];
         }
     }
-    uint16_t* dst = (kv ? v : k) + ((int64_t)t * p.cache.H + h) * D + lane * 8;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+    for (int i = 0; i < kKvRows; ++i) {
+        if (!row[i].there) continue;
+        const float s = kv_scale(param[i]), lo = kv_low(param[i]);
+        uint64_t s2, lo2, base2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(lo2) : "f"(lo));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(base2) : "f"(8388608.0f));
+        uint32_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // a code in the mantissa of 2^23, less 2^23, is the code
+            uint32_t a, b;
+            if constexpr (BITS == 4) {
+                a = ((codes[i].x >> (8 * j)) & 15u) | 0x4b000000u;
+                b = ((codes[i].x >> (8 * j + 4)) & 15u) | 0x4b000000u;
+            } else {
+                const uint32_t word = j < 2 ? codes[i].x : codes[i].y;
+                a = __byte_perm(word, 0x4b000000u, 0x7540 + 2 * (j & 1));
+                b = __byte_perm(word, 0x4b000000u, 0x7541 + 2 * (j & 1));
+            }
+            asm("{\n\t.reg .b64 c;\n\t.reg .f32 x, y;\n\t"
+                "mov.b64 c, {%1, %2};\n\t"
+                "sub.rn.f32x2 c, c, %3;\n\t"
+                "fma.rn.f32x2 c, c, %4, %5;\n\t"
+                "mov.b64 {x, y}, c;\n\t"
+                "cvt.rn.bf16x2.f32 %0, y, x;\n\t}"
+                : "=r"(out[j])
+                : "r"(a), "r"(b), "l"(base2), "l"(s2), "l"(lo2));
+        }
+        uint16_t* dst = (row[i].kv ? v : k) + ((int64_t)row[i].t * p.cache.H + row[i].h) * D + lane * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
 }
 
 KvMoveParams move_params(const KvCache& cache, const int64_t* slots, int64_t T, const LaunchEnv& env) {
@@ -164,13 +249,15 @@ KvMoveParams move_params(const KvCache& cache, const int64_t* slots, int64_t T, 
     p.cache = cache;
     p.slots = slots;
     p.rows = (uint32_t)(T * 2 * cache.H);
+    p.two_h = (uint32_t)(2 * cache.H);
+    p.inv = (uint32_t)(((uint64_t)1 << 32) / p.two_h);
     p.slot_limit = cache.pages << cache.page_shift;
     p.err = env.err;
     return p;
 }
 
 dim3 move_grid(uint32_t rows, int64_t D) {
-    const int64_t per_block = kKvThreads / (D / 8);
+    const int64_t per_block = kKvThreads / (D / 8) * kKvRows;
     return dim3((unsigned)((rows + per_block - 1) / per_block));
 }
 

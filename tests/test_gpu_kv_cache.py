@@ -122,6 +122,26 @@ def test_store_and_load(bits, d, t, h, page, fused):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_codes_are_the_rounded_quotients(bits):
+    """A million rows' worth of quotients over all scales a row can have, ties and their neighbours among them."""
+    t, h, d, page = 1024, 8, 128, 64
+    rng = np.random.default_rng(bits)
+    x = rng.integers(-255, 256, (t, h, d)).astype(np.float32) * np.exp2(rng.integers(-8, 9, (t, h, 1)).astype(np.float32))
+    x *= np.exp2(rng.integers(-120, 110, (t, h, 1)).astype(np.float32))
+    x[::2] += np.abs(x[::2]).max(-1, keepdims=True) * rng.uniform(-4, 4, (t // 2, h, 1)).astype(np.float32)
+    k = torch.from_numpy(x).to(torch.bfloat16)
+    v = torch.from_numpy(rng.permutation(x.ravel()).reshape(x.shape)[..., :]).to(torch.bfloat16)
+    codes, params = _cache(t // page, h, page, d, bits)
+    capi.kv_cache_store(k.cuda(), v.cuda(), torch.arange(t, device="cuda"), codes, params)
+    got_c, got_s, got_low = _host(codes, params, d)
+    for kv, y in enumerate((k, v)):
+        c, s, low = oracle.quantize(y.float().numpy(), bits)
+        shape = lambda a: np.moveaxis(a.reshape(t // page, page, h, *a.shape[2:]), 1, 2)  # noqa: E731
+        assert np.array_equal(got_c[:, kv], shape(c))
+        assert np.array_equal(got_s[:, kv], shape(s)) and np.array_equal(got_low[:, kv], shape(low))
+
+
 def test_store_takes_non_finite_rows_without_touching_others():
     t, h, d, page = 6, 2, 128, 16
     rng = np.random.default_rng(0)
