@@ -12,9 +12,10 @@
 // (hi - lo <= L s) and every value within half a step of its code.
 //
 // Both are bound by bytes: a token of 8 heads x 128 channels is 4 KB of bf16
-// and 1 KB of 4-bit rows.  A thread takes 8 channels (one 16-byte vector of
-// bf16) of several rows, D / 8 neighbouring lanes a row; minimum and maximum go
-// through shuffles, so a row is read once and nothing is staged.  The rows of a
+// and 1 KB of 4-bit rows.  A thread takes 16 channels of several rows, D / 16
+// neighbouring lanes a row; minimum and maximum go through shuffles, so a row is
+// read once and nothing is staged.  (16 channels, not 8: what a row costs beside
+// its elements, addresses and scale, is then shared by half as many lanes.)  The rows of a
 // thread are loaded together, and keys and values beside their slots: one row
 // at a time, behind its slot, reached a third of the bandwidth.
 
@@ -27,7 +28,8 @@ namespace i8ql {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvRows = 4;  // rows per thread
+constexpr int kKvChannels = 16;  // channels per thread
+constexpr int kKvRows = 2;       // rows per thread
 
 struct KvMoveParams {
     KvCache cache;
@@ -48,8 +50,8 @@ struct KvMoveRow {
 
 template <int D>
 __device__ __forceinline__ KvMoveRow move_row(const KvMoveParams& p, int i) {
-    constexpr int kGroups = kKvThreads / (D / 8);  // rows side by side in a block
-    const uint32_t row = (blockIdx.x * kKvRows + i) * kGroups + threadIdx.x / (D / 8);
+    constexpr int kGroups = kKvThreads / (D / kKvChannels);  // rows side by side in a block
+    const uint32_t row = (blockIdx.x * kKvRows + i) * kGroups + threadIdx.x / (D / kKvChannels);
     KvMoveRow r;
     r.there = row < p.rows;
     // row / two_h: the estimate is at most one too small (row < 2^31)
@@ -131,22 +133,23 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __restrict__ k,
                                                               const uint16_t* __restrict__ v, int64_t k_stride,
                                                               int64_t v_stride, KvMoveParams p) {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / kKvChannels;
     const int lane = threadIdx.x % kLanes;
     KvMoveRow row[kKvRows];
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
     pdl_wait();
-    uint4 w[kKvRows];
+    uint4 w[kKvRows][2];
     int64_t slot[kKvRows];
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
         const KvMoveRow& r = row[i];
-        w[i] = make_uint4(0, 0, 0, 0);
+        w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
         slot[i] = -1;
         if (r.there) {
-            const uint16_t* src = (r.kv ? v + r.t * v_stride : k + r.t * k_stride) + (int64_t)r.h * D + lane * 8;
-            w[i] = __ldg(reinterpret_cast<const uint4*>(src));
+            const uint16_t* src = (r.kv ? v + r.t * v_stride : k + r.t * k_stride) + (int64_t)r.h * D + lane * kKvChannels;
+            w[i][0] = __ldg(reinterpret_cast<const uint4*>(src));
+            w[i][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
             slot[i] = __ldg(p.slots + r.t);
         }
     }
@@ -155,9 +158,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __
         // (lo, -hi): over the thread's pairs, over a pair's halves, over the row's
         // lanes (a row is a whole group of lanes; all lanes of the warp shuffle)
         constexpr uint32_t kSigns = 0x80008000u;
-        const uint32_t least = min_bf16x2(min_bf16x2(w[i].x, w[i].y), min_bf16x2(w[i].z, w[i].w));
-        const uint32_t most = min_bf16x2(min_bf16x2(w[i].x ^ kSigns, w[i].y ^ kSigns),
-                                         min_bf16x2(w[i].z ^ kSigns, w[i].w ^ kSigns));
+        auto least4 = [](const uint4& x, uint32_t flip) {
+            return min_bf16x2(min_bf16x2(x.x ^ flip, x.y ^ flip), min_bf16x2(x.z ^ flip, x.w ^ flip));
+        };
+        const uint32_t least = min_bf16x2(least4(w[i][0], 0), least4(w[i][1], 0));
+        const uint32_t most = min_bf16x2(least4(w[i][0], kSigns), least4(w[i][1], kSigns));
         uint32_t ends = min_bf16x2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
         for (int m = 1; m < kLanes; m <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
@@ -168,16 +173,26 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __
         const float ratio = __fdiv_rn(__fsub_rn(hi, lo), kLevels);  // >= 0
         const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
         const float s = __uint_as_float(s_bits);
-        uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (s > 0.0f) kv_codes(w[i], lo, s, c);
-        const uint32_t c0 = low_bytes(c[0], c[1], c[2], c[3]), c1 = low_bytes(c[4], c[5], c[6], c[7]);
-        if constexpr (BITS == 4) {
-            const uint32_t n0 = (c0 & 0x000f000fu) | ((c0 >> 4) & 0x00f000f0u);
-            const uint32_t n1 = (c1 & 0x000f000fu) | ((c1 >> 4) & 0x00f000f0u);
-            reinterpret_cast<uint32_t*>(p.cache.codes + index * (D / 2))[lane] = __byte_perm(n0, n1, 0x6420);
-        } else {
-            reinterpret_cast<uint2*>(p.cache.codes + index * D)[lane] = make_uint2(c0, c1);
+        uint32_t out[4];  // the 16 codes: 4 bits in the first half
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (s > 0.0f) kv_codes(w[i][j], lo, s, c);
+            const uint32_t c0 = low_bytes(c[0], c[1], c[2], c[3]), c1 = low_bytes(c[4], c[5], c[6], c[7]);
+            if constexpr (BITS == 4) {
+                const uint32_t n0 = (c0 & 0x000f000fu) | ((c0 >> 4) & 0x00f000f0u);
+                const uint32_t n1 = (c1 & 0x000f000fu) | ((c1 >> 4) & 0x00f000f0u);
+                out[j] = __byte_perm(n0, n1, 0x6420);
+            } else {
+                out[2 * j] = c0;
+                out[2 * j + 1] = c1;
+            }
         }
+        uint8_t* dst = p.cache.codes + index * (D * BITS / 8) + lane * (kKvChannels * BITS / 8);
+        if constexpr (BITS == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+        else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
         if (lane == 0) p.cache.params[index] = (s_bits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
     }
 }
@@ -185,7 +200,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __
 template <int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                              KvMoveParams p) {
-    const int lane = threadIdx.x % (D / 8);
+    const int lane = threadIdx.x % (D / kKvChannels);
     KvMoveRow row[kKvRows];
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
@@ -195,17 +210,27 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
     for (int i = 0; i < kKvRows; ++i) index[i] = row[i].there ? __ldg(p.slots + row[i].t) : -1;
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) index[i] = cache_row(p, row[i], index[i]);
-    uint2 codes[kKvRows];
+    constexpr int kWords = kKvChannels * BITS / 32;
+    uint32_t codes[kKvRows][kWords];
     uint32_t param[kKvRows];
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
-        codes[i] = make_uint2(0, 0);
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) codes[i][j] = 0;
         param[i] = 0;  // stands for 0
         if (index[i] >= 0) {
-            if constexpr (BITS == 4)
-                codes[i].x = reinterpret_cast<const uint32_t*>(p.cache.codes + index[i] * (D / 2))[lane];
-            else
-                codes[i] = reinterpret_cast<const uint2*>(p.cache.codes + index[i] * D)[lane];
+            const uint8_t* src = p.cache.codes + index[i] * (D * BITS / 8) + lane * (kWords * 4);
+            if constexpr (BITS == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                codes[i][0] = v.x;
+                codes[i][1] = v.y;
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                codes[i][0] = v.x;
+                codes[i][1] = v.y;
+                codes[i][2] = v.z;
+                codes[i][3] = v.w;
+            }
             param[i] = p.cache.params[index[i]];
         }
     }
@@ -217,18 +242,18 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
         asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
         asm("mov.b64 %0, {%1, %1};" : "=l"(lo2) : "f"(lo));
         asm("mov.b64 %0, {%1, %1};" : "=l"(base2) : "f"(8388608.0f));
-        uint32_t out[4];
+        uint32_t out[kKvChannels / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kKvChannels / 2; ++j) {
             // a code in the mantissa of 2^23, less 2^23, is the code
             uint32_t a, b;
             if constexpr (BITS == 4) {
-                a = ((codes[i].x >> (8 * j)) & 15u) | 0x4b000000u;
-                b = ((codes[i].x >> (8 * j + 4)) & 15u) | 0x4b000000u;
+                const uint32_t word = codes[i][j / 4] >> (8 * (j % 4));
+                a = (word & 15u) | 0x4b000000u;
+                b = ((word >> 4) & 15u) | 0x4b000000u;
             } else {
-                const uint32_t word = j < 2 ? codes[i].x : codes[i].y;
-                a = __byte_perm(word, 0x4b000000u, 0x7540 + 2 * (j & 1));
-                b = __byte_perm(word, 0x4b000000u, 0x7541 + 2 * (j & 1));
+                a = __byte_perm(codes[i][j / 2], 0x4b000000u, 0x7540 + 2 * (j % 2));
+                b = __byte_perm(codes[i][j / 2], 0x4b000000u, 0x7541 + 2 * (j % 2));
             }
             asm("{\n\t.reg .b64 c;\n\t.reg .f32 x, y;\n\t"
                 "mov.b64 c, {%1, %2};\n\t"
@@ -239,8 +264,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
                 : "=r"(out[j])
                 : "r"(a), "r"(b), "l"(base2), "l"(s2), "l"(lo2));
         }
-        uint16_t* dst = (row[i].kv ? v : k) + ((int64_t)row[i].t * p.cache.H + row[i].h) * D + lane * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+        uint4* dst = reinterpret_cast<uint4*>((row[i].kv ? v : k) + ((int64_t)row[i].t * p.cache.H + row[i].h) * D +
+                                              lane * kKvChannels);
+        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
@@ -257,7 +284,7 @@ KvMoveParams move_params(const KvCache& cache, const int64_t* slots, int64_t T, 
 }
 
 dim3 move_grid(uint32_t rows, int64_t D) {
-    const int64_t per_block = kKvThreads / (D / 8) * kKvRows;
+    const int64_t per_block = kKvThreads / (D / kKvChannels) * kKvRows;
     return dim3((unsigned)((rows + per_block - 1) / per_block));
 }
 
