@@ -40,7 +40,7 @@
 //  * a lane turns the scale and low value of one token into the four factors
 //    the warp needs, and shares them through shared memory.
 // A block is four such warps over 32 tokens of a 128-token tile each, with
-// their own running maximum, and one warp that keeps 3 tiles of bulk copies
+// their own reference, and one warp that keeps 3 tiles of bulk copies
 // in flight (about 50 KB a block, three blocks an SM).
 
 #include <cuda_runtime.h>
@@ -58,7 +58,6 @@ constexpr int kTile = 128;                   // tokens per pipeline stage
 constexpr int kWarps = 4;                    // consumer warps
 constexpr int kWarpTokens = kTile / kWarps;  // tokens of a stage per warp
 constexpr int kThreads = kWarps * 32 + 32;
-constexpr int kStages = 3;
 constexpr float kSlack = 5.0f;    // a logit may exceed what the weights are relative to by this (log2)
 constexpr int kValueShift = 10;   // w s / S is held times 2^this: at most 2^15 in fp16
 constexpr int kCost = 1;  // tiles that beginning and ending an item counts
@@ -70,10 +69,12 @@ struct Cfg {
     static constexpr int kRowBytes = D * BITS / 8;
     static constexpr int kCodes = kTile * kRowBytes;
     static constexpr int kStageBytes = 2 * kCodes + 2 * kTile * 4;
+    static constexpr int kStages = ROWS == 16 && BITS == 8 && D == 128 ? 2 : 3;  // (so that kBlocks fit an SM)
     // a merge row: D floats, 4 more after every 32 (spreads a warp's stores over the banks)
     static constexpr int kMergeRow = D + D / 8;
     static constexpr int kMergeBytes = 2 * ROWS * kMergeRow * 4;
     static constexpr int kSmem = kStages * kStageBytes + kMergeBytes;
+    static_assert(kBlocks * (kSmem + 4608) <= 228 * 1024, "shared memory of the resident blocks");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     kv_attention_kernel(const KvAttnParams p) {
     constexpr int ROWS = 8 * HALVES;
     using C = Cfg<D, BITS, ROWS>;
+    constexpr int kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ KvLocate locate;
