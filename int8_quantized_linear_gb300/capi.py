@@ -571,8 +571,6 @@ def kv_cache_load(codes, params, slots, head_dim, k=None, v=None, stream=None):
     pages, heads, page, bits = _kv_cache(codes, params, head_dim)
     t = slots.shape[0]
     _need(slots, torch.int64, (t,), "slots")
-    if k is None and v is None:  # one allocation for both
-        k, v = torch.empty((2, t, heads, head_dim), dtype=torch.bfloat16, device=codes.device).unbind(0)
     if k is None:
         k = torch.empty((t, heads, head_dim), dtype=torch.bfloat16, device=codes.device)
     if v is None:

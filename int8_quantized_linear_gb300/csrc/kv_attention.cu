@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t a[kPairs], b[kPairs];
-                    unpack_key<BITS>(kw[2 * i][k], a);
-                    unpack_key<BITS>(kw[2 * i + 1][k], b);
+                    unpack_key<BITS, true>(kw[2 * i][k], a);
+                    unpack_key<BITS, true>(kw[2 * i + 1][k], b);
 #pragma unroll
                     for (int j = 0; j < kPairs; j += 2)
 #pragma unroll
@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                 for (int k = 0; k < kValWords; ++k) {
                     uint32_t a[2 * kPairs], b[2 * kPairs];
-                    unpack_values<BITS>(v[0][k], v[1][k], a);
-                    unpack_values<BITS>(v[2][k], v[3][k], b);
+                    unpack_values<BITS, true>(v[0][k], v[1][k], a);
+                    unpack_values<BITS, true>(v[2][k], v[3][k], b);
 #pragma unroll
                     for (int j = 0; j < 2 * kPairs; j += 2)
 #pragma unroll

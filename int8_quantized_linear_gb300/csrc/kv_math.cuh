@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// What is subtracted from a code.
+// What is subtracted from a centred code.
 template <int BITS>
 constexpr float kCentre = BITS == 4 ? 8.0f : 128.0f;
 
@@ -53,39 +53,43 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return r;
 }
 
-// Eight nibbles as four pairs of fp16 (nibbles j and j + 4), less 8: exact.
+// Eight nibbles as four pairs of fp16 (nibbles j and j + 4), CENTRED less 8: exact.
+template <bool CENTRED>
 __device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&pair)[4]) {
+    constexpr uint32_t kSub = CENTRED ? 0x64086408u : 0x64006400u;  // 1032 or 1024
+    constexpr uint32_t kAdd = CENTRED ? 0xd480d480u : 0xd400d400u;  // -72 or -64
     const uint32_t u = w >> 8;
-    pair[0] = sub_f16x2(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);               // 1024 + c - 1032
-    pair[1] = fma_f16x2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // (1024 + 16 c) / 16 - 72
-    pair[2] = sub_f16x2(and_or(u, 0x000f000fu, 0x64006400u), 0x64086408u);
-    pair[3] = fma_f16x2(and_or(u, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+    pair[0] = sub_f16x2(and_or(w, 0x000f000fu, 0x64006400u), kSub);               // 1024 + c - ..
+    pair[1] = fma_f16x2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, kAdd);  // (1024 + 16 c) / 16 - ..
+    pair[2] = sub_f16x2(and_or(u, 0x000f000fu, 0x64006400u), kSub);
+    pair[3] = fma_f16x2(and_or(u, 0x00f000f0u, 0x64006400u), 0x2c002c00u, kAdd);
 }
 
-// Two bytes as a pair of fp16, less 128: exact.
+// Two bytes as a pair of fp16, CENTRED less 128: exact.
+template <bool CENTRED>
 __device__ __forceinline__ uint32_t unpack_bytes(uint32_t w, uint32_t select) {
-    return sub_f16x2(__byte_perm(w, 0x64646464u, select), 0x64806480u);  // 1024 + c - 1152
+    return sub_f16x2(__byte_perm(w, 0x64646464u, select), CENTRED ? 0x64806480u : 0x64006400u);  // 1024 + c - ..
 }
 
 // A word of a key row as pairs along the channels: (j, j + 4) of 8 codes, or
 // (2j, 2j + 1) of 4.
-template <int BITS>
+template <int BITS, bool CENTRED>
 __device__ __forceinline__ void unpack_key(uint32_t w, uint32_t (&pair)[16 / BITS]) {
     if constexpr (BITS == 4) {
-        unpack_nibbles(w, pair);
+        unpack_nibbles<CENTRED>(w, pair);
     } else {
-        pair[0] = unpack_bytes(w, 0x5150);
-        pair[1] = unpack_bytes(w, 0x5352);
+        pair[0] = unpack_bytes<CENTRED>(w, 0x5150);
+        pair[1] = unpack_bytes<CENTRED>(w, 0x5352);
     }
 }
 
 // Words of two value rows as pairs along the tokens, one per channel.
-template <int BITS>
+template <int BITS, bool CENTRED>
 __device__ __forceinline__ void unpack_values(uint32_t a, uint32_t b, uint32_t (&pair)[32 / BITS]) {
     if constexpr (BITS == 4) {
         uint32_t lo[4], hi[4];
-        unpack_nibbles(__byte_perm(a, b, 0x5410), lo);
-        unpack_nibbles(__byte_perm(a, b, 0x7632), hi);
+        unpack_nibbles<CENTRED>(__byte_perm(a, b, 0x5410), lo);
+        unpack_nibbles<CENTRED>(__byte_perm(a, b, 0x7632), hi);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             pair[j] = lo[j];
@@ -93,10 +97,10 @@ __device__ __forceinline__ void unpack_values(uint32_t a, uint32_t b, uint32_t (
         }
     } else {
         const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);  // a0 b0 a1 b1, a2 b2 a3 b3
-        pair[0] = unpack_bytes(lo, 0x5150);
-        pair[1] = unpack_bytes(lo, 0x5352);
-        pair[2] = unpack_bytes(hi, 0x5150);
-        pair[3] = unpack_bytes(hi, 0x5352);
+        pair[0] = unpack_bytes<CENTRED>(lo, 0x5150);
+        pair[1] = unpack_bytes<CENTRED>(lo, 0x5352);
+        pair[2] = unpack_bytes<CENTRED>(hi, 0x5150);
+        pair[3] = unpack_bytes<CENTRED>(hi, 0x5352);
     }
 }
 

@@ -20,9 +20,10 @@
 // chunks of 2048 tokens over 8192, 32 query heads over 8 x 128, 4 bits), and
 // inlining the waits as much again.
 //
-// K and V become fp16 including scale and low value (one rounding of 2^-11
-// relative to the element: the products then need no factors per token), Q
-// and P as in kv_attention.cu.  Ranges: a row of Q is scaled to 2^8; a tile
+// K and V become fp16 including scale and low value: fp16_rn(low + s code), one
+// rounding of 2^-11 relative to the element (scale and low value have 8 bits and
+// are exact), so the products need no factors per token.  Q and P as in
+// kv_attention.cu.  Ranges: a row of Q is scaled to 2^8; a tile
 // of K by the power of two that brings its largest element to 2^7, undone in
 // c; V by one such power for all tiles so far, O being rescaled when it
 // grows; P's maximum m is only raised when a row exceeds it by 2^8 (the sums
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     __shared__ KvRange range;
     __shared__ TileInfo infos[kInfo];
     __shared__ uint32_t exp_red[2][kUnpackWarps][2];
-    __shared__ uint32_t key_factor[kTile][2];                // scale and centre, each twice, as halves
-    __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, centres
+    __shared__ uint32_t key_factor[kTile][2];                // scale and low value, each twice, as halves
+    __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, low values
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -374,11 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     val_exp = max(val_exp, (int)(exp_red[kt & 1][w][1] >> 23));
                 }
                 const float fk = pow2(134 - key_exp), fv = pow2(134 - val_exp);
-                const float ks = kv_scale(pk) * fk, kc = fmaf(kv_scale(pk), kCentre<BITS>, kv_low(pk)) * fk;
-                const float vs = kv_scale(pv) * fv, vc = fmaf(kv_scale(pv), kCentre<BITS>, kv_low(pv)) * fv;
+                const float ks = kv_scale(pk) * fk, kl = kv_low(pk) * fk;
+                const float vs = kv_scale(pv) * fv, vl = kv_low(pv) * fv;
                 key_factor[tid][0] = pack_f16(ks, ks);
-                key_factor[tid][1] = pack_f16(kc, kc);
-                const uint32_t v2 = pack_f16(vs, vc);
+                key_factor[tid][1] = pack_f16(kl, kl);
+                const uint32_t v2 = pack_f16(vs, vl);
                 val_factor[0][tid] = (uint16_t)v2;
                 val_factor[1][tid] = (uint16_t)(v2 >> 16);
                 if (tid == 0) {
@@ -405,14 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                         for (int j = 0; j < kChunks; ++j) {
                             uint32_t h[4];
                             if constexpr (BITS == 4) {
-                                unpack_nibbles(flip ? w[j ^ 1] : w[j], h);
+                                unpack_nibbles<false>(flip ? w[j ^ 1] : w[j], h);
                             } else {
                                 const uint32_t a = flip ? w[2 * (j ^ 1)] : w[2 * j];
                                 const uint32_t b = flip ? w[2 * (j ^ 1) + 1] : w[2 * j + 1];
-                                h[0] = unpack_bytes(a, 0x5150);
-                                h[1] = unpack_bytes(a, 0x5352);
-                                h[2] = unpack_bytes(b, 0x5150);
-                                h[3] = unpack_bytes(b, 0x5352);
+                                h[0] = unpack_bytes<false>(a, 0x5150);
+                                h[1] = unpack_bytes<false>(a, 0x5352);
+                                h[2] = unpack_bytes<false>(b, 0x5150);
+                                h[3] = unpack_bytes<false>(b, 0x5352);
                             }
                             sts16(row + (((pos0 + (j ^ flip)) ^ (tok & 7)) << 4), fma_f16x2(h[0], s, o),
                                   fma_f16x2(h[1], s, o), fma_f16x2(h[2], s, o), fma_f16x2(h[3], s, o));
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
 #pragma unroll
                         for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + j * C::kRowBytes + k * 4);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) unpack_values<BITS>(w[2 * j], w[2 * j + 1], h[j]);
+                        for (int j = 0; j < 4; ++j) unpack_values<BITS, false>(w[2 * j], w[2 * j + 1], h[j]);
 #pragma unroll
                         for (int e = 0; e < kPerWord; ++e) {
                             const int ch = val_part * (D / 8) + k * kPerWord + e;
