@@ -94,7 +94,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-template <int D, int BITS, int HALVES>
+// S = 0: the work is shared out evenly (kv_schedule.cuh).  S > 0: a cluster of S
+// CTAs takes one cache head of one sequence and joins its parts through
+// distributed shared memory: one launch and no workspace, for calls of few and
+// short contexts.
+template <int D, int BITS, int HALVES, int S>
 __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     kv_attention_kernel(const KvAttnParams p) {
     constexpr int ROWS = 8 * HALVES;
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     __shared__ KvCursor cursors[kWarps];  // (kept out of the registers of the main loop)
     __shared__ KvRange range;
     __shared__ float merge_ml[kWarps][ROWS][2];
+    __shared__ __align__(16) float cta_ml[ROWS][2];  // (S > 0) this CTA's part
     __shared__ float4 factors[kWarps][kWarpTokens];  // of a token: K scale and offset, V scale and offset
     __shared__ int abort_flag;
 
@@ -123,7 +128,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     int stage = 0;
     uint32_t parity = 0;
     KvCursor start;
-    const KvRange found = kv_locate<ROWS, kTile, kCost, kThreads>(p, locate, start);  // (its barriers also publish the mbarriers)
+    KvRange found;
+    const int rank = S > 0 ? (int)tc::cluster_rank() : 0;
+    // A cursor's work: the tiles from its tile on that are this CTA's, and
+    // whether there is any item left.  (S > 0: an item's tiles are cut evenly;
+    // a CTA may have none of them.)
+    auto part_begin = [&](const KvCursor& c) { return c.span.tiles * rank / max(S, 1); };
+    auto work = [&](const KvCursor& c, int64_t end, int& n) {
+        if constexpr (S == 0) {
+            n = kv_take<kCost>(p, c, end);
+            return n > 0;
+        } else {
+            if (c.rb >= c.blocks) return false;
+            n = c.span.tiles * (rank + 1) / S - c.tile;
+            return true;
+        }
+    };
+    auto advance = [&](KvCursor& c) {
+        if constexpr (S == 0) {
+            kv_next_item<ROWS, kTile, kCost>(p, c);
+        } else if (++c.rb < c.blocks) {
+            c.span = kv_span<ROWS, kTile>(p, c.seq, c.rb);
+            c.tile = part_begin(c);
+        }
+    };
+    if constexpr (S == 0) {
+        found = kv_locate<ROWS, kTile, kCost, kThreads>(p, locate, start);  // (its barriers also publish the mbarriers)
+    } else {
+        found = {};
+        start = {};
+        const int64_t item = blockIdx.x / S;
+        start.b = item / p.cache.H;
+        start.h = (int)(item - start.b * p.cache.H);
+        start.seq = kv_sequence(p, start.b);
+        start.blocks = kv_blocks<ROWS>(p, start.seq);
+        if (start.blocks > 0) {
+            start.span = kv_span<ROWS, kTile>(p, start.seq, 0);
+            start.tile = part_begin(start);
+        }
+        __syncthreads();
+    }
 
     if (warp == kWarps) {
         KvCursor& c = start;
@@ -138,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
         const int dst = is_param ? 2 * C::kCodes + kv * kTile * 4 + at * 4 : kv * C::kCodes + at * C::kRowBytes;
         int issued = 0;
         bool ok = true;
-        while (const int n = ok ? kv_take<kCost>(p, c, found.end) : 0) {
+        int n = 0;
+        while (work(c, found.end, n) && (ok || S > 0)) {
             const int32_t* table = p.table + c.b * p.table_width;
             const int first = (c.span.first + c.tile) * kTile + at;  // this lane's token of the item's next tile
             auto needed = [&](int i) {
@@ -177,7 +222,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                     parity ^= 1;
                 }
             }
-            kv_next_item<ROWS, kTile, kCost>(p, c);
+            if constexpr (S > 0) {  // the barriers of the join
+                __syncwarp();
+                tc::cluster_sync_all();
+                tc::cluster_sync_all();
+            }
+            advance(c);
         }
         if (!ok) {
             // giving up: let the copies in flight land before the block's
@@ -210,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     if (threadIdx.x == 0) range = found;
     consumer_sync();
     bool split = false;
-    while (const int n = kv_take<kCost>(p, c, range.end)) {
+    int n = 0;
+    while (work(c, range.end, n)) {
         const int row0 = c.rb * ROWS;
         const int rows = min(ROWS, c.seq.nq * p.G - row0);
         const int base = c.seq.len - c.seq.nq;
@@ -515,44 +566,92 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             }
             consumer_sync();
         }
-        const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
         const int tid = threadIdx.x;
-        const bool store = *reinterpret_cast<volatile int*>(&abort_flag) == 0;
-        if (store) {
-            for (int k = tid; k < rows * (D / 8); k += kWarps * 32) {
-                const int r = k / (D / 8), d = (k % (D / 8)) * 8;
-                const float* src = merge + r * C::kMergeRow + d + 4 * (d / 32);
-                float v[8];
+        auto local_sum = [&](int r, int d, float (&v)[8]) {  // of the two halves of the block's warps
+            const float* src = merge + r * C::kMergeRow + d + 4 * (d / 32);
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(src + j);
-                    const float4 b = *reinterpret_cast<const float4*>(src + ROWS * C::kMergeRow + j);
-                    v[j] = a.x + b.x;
-                    v[j + 1] = a.y + b.y;
-                    v[j + 2] = a.z + b.z;
-                    v[j + 3] = a.w + b.w;
+            for (int j = 0; j < 8; j += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(src + j);
+                const float4 b = *reinterpret_cast<const float4*>(src + ROWS * C::kMergeRow + j);
+                v[j] = a.x + b.x;
+                v[j + 1] = a.y + b.y;
+                v[j + 2] = a.z + b.z;
+                v[j + 3] = a.w + b.w;
+            }
+        };
+        auto local_ml = [&](int r) {
+            float top = merge_ml[0][r][0], total = 0.0f;
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][r][0]);
+            for (int w = 0; w < kWarps; ++w)
+                total += merge_ml[w][r][1] == 0.0f ? 0.0f : merge_ml[w][r][1] * exp2_approx(merge_ml[w][r][0] - top);
+            return make_float2(top, total);
+        };
+        auto write_out = [&](int r, int d, const float (&v)[8], float total) {
+            const int i = (row0 + r) / p.G;
+            const int head = c.h * p.G + row0 + r - i * p.G;
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            *reinterpret_cast<uint4*>(p.out + ((c.seq.q0 + i) * ((int64_t)p.cache.H * p.G) + head) * D + d) =
+                make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                           pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+        };
+        const bool store = *reinterpret_cast<volatile int*>(&abort_flag) == 0;
+        if constexpr (S > 0) {
+            // this CTA's part in the first merge rows; then each CTA joins its share of the outputs
+            for (int k = tid; k < ROWS * (D / 8); k += kWarps * 32) {
+                const int r = k / (D / 8), d = (k % (D / 8)) * 8;
+                float v[8];
+                local_sum(r, d, v);
+                float4* dst = reinterpret_cast<float4*>(merge + r * C::kMergeRow + d + 4 * (d / 32));
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (d == 0) *reinterpret_cast<float2*>(cta_ml[r]) = local_ml(r);
+            }
+            __syncwarp();
+            tc::cluster_sync_all();
+            for (int k = tid * S + rank; k < rows * (D / 8) && store; k += kWarps * 32 * S) {
+                const int r = k / (D / 8), d = (k % (D / 8)) * 8;
+                const uint32_t ml_at = tc::smem_u32(cta_ml[r] - (r & 1) * 2);  // (pairs of rows: 16-byte loads)
+                const uint32_t v_at = tc::smem_u32(merge + r * C::kMergeRow + d + 4 * (d / 32));
+                float2 ml[S];
+                float top = -INFINITY, total = 0.0f, v[8] = {};
+#pragma unroll
+                for (int y = 0; y < S; ++y) {
+                    const int4 x = tc::ld_dsmem_v4(ml_at, y);
+                    ml[y] = (r & 1) ? make_float2(__int_as_float(x.z), __int_as_float(x.w))
+                                    : make_float2(__int_as_float(x.x), __int_as_float(x.y));
+                    top = fmaxf(top, ml[y].x);
                 }
-                float top = merge_ml[0][r][0];
-                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_ml[w][r][0]);
-                float total = 0.0f;
-                for (int w = 0; w < kWarps; ++w)
-                    total += merge_ml[w][r][1] == 0.0f ? 0.0f : merge_ml[w][r][1] * exp2_approx(merge_ml[w][r][0] - top);
+#pragma unroll
+                for (int y = 0; y < S; ++y) {
+                    const float f = ml[y].y == 0.0f ? 0.0f : exp2_approx(ml[y].x - top);
+                    total += ml[y].y * f;
+                    const int4 a = tc::ld_dsmem_v4(v_at, y), b = tc::ld_dsmem_v4(v_at + 16, y);
+                    const int x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = fmaf(__int_as_float(x[j]), f, v[j]);
+                }
+                write_out(r, d, v, total);
+            }
+            __syncwarp();
+            tc::cluster_sync_all();  // no CTA's rows are overwritten or gone while others read them
+        } else {
+            const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
+            for (int k = tid; k < rows * (D / 8) && store; k += kWarps * 32) {
+                const int r = k / (D / 8), d = (k % (D / 8)) * 8;
+                float v[8];
+                local_sum(r, d, v);
+                const float2 ml = local_ml(r);
                 if (begins && ends) {
-                    const int i = (row0 + r) / p.G;
-                    const int head = c.h * p.G + row0 + r - i * p.G;
-                    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                    *reinterpret_cast<uint4*>(p.out + ((c.seq.q0 + i) * ((int64_t)p.cache.H * p.G) + head) * D + d) =
-                        make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+                    write_out(r, d, v, ml.y);
                 } else {
                     const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * ROWS + r;
                     float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + d);
                     dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                     dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, total);
+                    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = ml;
                 }
             }
-            if (begins && !ends) {
+            if (begins && !ends && store) {
                 split = true;
                 if (tid == 0) {
                     KvSplitItem it;
@@ -567,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             }
         }
         __syncwarp();
-        if (lane == 0) kv_next_item<ROWS, kTile, kCost>(p, c);
+        if (lane == 0) advance(c);
         consumer_sync();  // the cursor is at the next item, and the merge rows are free again
     }
     if (threadIdx.x == 0 && p.split != nullptr && !split) p.split[blockIdx.x].rows = 0;
@@ -693,13 +792,20 @@ cudaError_t launch_join(const KvAttnParams& p, int64_t ctas, const LaunchEnv& en
                          env.stream, kNoCluster, p);
 }
 
-// How a call runs: the query rows of a block, the CTAs, and whether an item
-// may be cut between CTAs.
+// How a call runs: the query rows of a block, the CTAs, whether an item may be
+// cut between CTAs (and is joined by a second kernel), and whether it runs as
+// clusters that join by themselves.
 struct Plan {
     int rows;
     int64_t ctas;
     bool split;
+    bool cluster;
 };
+
+// Contexts of up to this many tiles (by the page table's width) run as clusters
+// when all clusters fit the device at once.
+constexpr int kClusterSize = 8;
+constexpr int64_t kClusterTiles = 64;
 
 Plan make_plan(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int64_t bits, int sms) {
     Plan pl;
@@ -711,13 +817,19 @@ Plan make_plan(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int
     const int64_t items = (T_q * G / pl.rows + B) * H;
     pl.ctas = items > sms * per_sm ? sms * per_sm : std::min<int64_t>(sms * per_sm, items * item_tiles);
     pl.split = item_tiles > 1;
+    pl.cluster = pl.rows != kKvPromptRows && item_tiles > 1 && item_tiles <= kClusterTiles &&
+                 B * H * kClusterSize <= sms * per_sm;
+    if (pl.cluster) {
+        pl.ctas = B * H * kClusterSize;
+        pl.split = false;
+    }
     return pl;
 }
 
 size_t part_bytes(int64_t ctas, int64_t rows, int64_t D) { return (size_t)(ctas * 2 * rows * (D + 2) * 4); }
 
-template <int D, int BITS, int HALVES>
-cudaError_t launch_form(const KvAttnParams& p, const Plan& pl, const LaunchEnv& env) {
+template <int D, int BITS, int HALVES, int S>
+cudaError_t launch_size(const KvAttnParams& p, const Plan& pl, const LaunchEnv& env) {
     using C = Cfg<D, BITS, 8 * HALVES>;
     static std::once_flag once[64];
     static cudaError_t set[64];
@@ -725,12 +837,18 @@ cudaError_t launch_form(const KvAttnParams& p, const Plan& pl, const LaunchEnv& 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::call_once(once[dev & 63], [&] {
-        set[dev & 63] = cudaFuncSetAttribute(kv_attention_kernel<D, BITS, HALVES>,
+        set[dev & 63] = cudaFuncSetAttribute(kv_attention_kernel<D, BITS, HALVES, S>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (set[dev & 63] != cudaSuccess) return set[dev & 63];
-    return launch_kernel(kv_attention_kernel<D, BITS, HALVES>, dim3((unsigned)pl.ctas), dim3(kThreads), C::kSmem,
-                         env.stream, kNoCluster, p);
+    return launch_kernel(kv_attention_kernel<D, BITS, HALVES, S>, dim3((unsigned)pl.ctas), dim3(kThreads), C::kSmem,
+                         env.stream, S > 0 ? dim3(S, 1, 1) : kNoCluster, p);
+}
+
+template <int D, int BITS, int HALVES>
+cudaError_t launch_form(const KvAttnParams& p, const Plan& pl, const LaunchEnv& env) {
+    return pl.cluster ? launch_size<D, BITS, HALVES, kClusterSize>(p, pl, env)
+                      : launch_size<D, BITS, HALVES, 0>(p, pl, env);
 }
 
 template <int D>

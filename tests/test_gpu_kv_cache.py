@@ -420,6 +420,12 @@ def test_strided_queries_streams_and_workspace():
     p.run(q=q, stream=st.cuda_stream, out=out.zero_())
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_workspace():
+    """Contexts long enough to be cut between CTAs: a given workspace, with anything in it, and one too small."""
+    p = Problem([300, 20000, 47], [1, 4, 2], 8, 2, 128, 4, 16, 77)
+    want = p.run()
     size = capi.i8ql_kv_attention_workspace(3, 7, 8, 2, 128, 4, 16, p.table.shape[1], 4)
     assert size > 0
     ws = torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda")  # contents do not matter
@@ -427,6 +433,35 @@ def test_strided_queries_streams_and_workspace():
     with pytest.raises(capi.I8qlError) as err:
         p.run(workspace=ws[:size - 1])
     assert err.value.status == capi.I8QL_ERR_WORKSPACE_LIMIT
+
+
+@pytest.mark.parametrize("width", [0, 80, 2000])
+def test_page_table_width_only_chooses_the_form(width):
+    """The same sequences behind a wider table: joined in clusters, by a second kernel, or not cut at all."""
+    p = Problem([700, 1, 0, 300, 17], [1, 2, 1, 0, 1], 8, 2, 128, 4, 16, 31)
+    p.table = torch.cat([p.table, torch.full((5, width), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    p.check(p.run())
+
+
+def test_keys_with_outlier_channels():
+    """Keys as models have them (a few channels many times the rest), stored and attended over: the whole output
+    within 2.5e-3 of the fp64 attention over the quantized values (its own bf16 rounding is 1.7e-3 rms)."""
+    n, h, d, page = 600, 2, 128, 64
+    for bits in (4, 8):
+        g = torch.Generator().manual_seed(bits)
+        k = torch.randn((n, h, d), generator=g)
+        k[..., [5, 77]] *= 60.0
+        k, v = k.to(torch.bfloat16), torch.randn((n, h, d), generator=g).to(torch.bfloat16)
+        codes, params = _cache(10, h, page, d, bits)
+        capi.kv_cache_store(k.cuda(), v.cuda(), torch.arange(n, device="cuda"), codes, params)
+        c, s, low = (np.stack(t) for t in zip(*(oracle.quantize(x.float().numpy(), bits) for x in (k, v))))
+        for nq in (1, 3, 50):
+            q = torch.randn((nq, 8, d), generator=g).to(torch.bfloat16)
+            y = capi.kv_cache_attention(q.cuda(), codes, params, torch.arange(10, dtype=torch.int32, device="cuda")[None],
+                                        torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                        q_offsets=torch.tensor([0, nq], dtype=torch.int32, device="cuda"), max_q=nq)
+            ref = oracle.attention(q.double().numpy(), c, s, low, nq, 0, d ** -0.5).out
+            assert np.linalg.norm(y.double().cpu().numpy() - ref) <= 2.5e-3 * np.linalg.norm(ref), (bits, nq)
 
 
 def test_graph_capture():
