@@ -472,9 +472,12 @@ i8ql_status kv_cache_load(const uint8_t* codes, const i8ql_bf16* params, const i
  * window > 0 only those with j > p - window.  With G = Hq / H query heads per
  * cache head, query head h attends over cache head h / G:
  *   a_j = softmax_scale * sum_d q[d] k_j[d];  out[d] = bf16(sum_j e^a_j v_j[d] / sum_j e^a_j)
- * (k, v: low + scale * code, not rounded to bf16 on the way with at most 32
- * query rows a head group; see the sources).  A row that sees no token
- * (p < 0: more queries than tokens) is 0.  fp32 logits, sums and softmax.
+ * with k and v = low + scale * code.  A row that sees no token (p < 0: more
+ * queries than tokens) is 0.  fp32 logits, sums and softmax; the softmax
+ * weights (times the value scale) are rounded to 11 bits for the tensor
+ * cores, and weights under about 2^-31 of a row's largest may count as 0.
+ * With max_q * G <= 32 the products run on the codes (exact); with more,
+ * keys and values are rounded to 11 bits first.
  *
  * Inputs: q bf16, token t's Hq * D values contiguous at t * q_stride (>= Hq *
  * D, a multiple of 8), 16-byte aligned; page_table int32 [B, table_width]

@@ -520,9 +520,10 @@ def kv_cache_alloc(num_pages, heads, page_size, head_dim, bits=4, device="cuda")
 
 def _kv_cache(codes: torch.Tensor, params: torch.Tensor, head_dim: int) -> tuple[int, int, int, int]:
     """(num_pages, heads, page_size, bits) of a cache for rows of head_dim channels."""
-    if codes.dim() != 5 or codes.shape[1] != 2:
+    shape = codes.shape
+    if len(shape) != 5 or shape[1] != 2:
         raise ValueError("codes must be [num_pages, 2, heads, page_size, head_dim * bits / 8]")
-    pages, _, heads, page, row = codes.shape
+    pages, _, heads, page, row = shape
     bits = 4 if 2 * row == head_dim else 8
     _need(codes, torch.uint8, (pages, 2, heads, page, head_dim * bits // 8), "codes")
     _need(params, torch.bfloat16, (pages, 2, heads, page, 2), "params")
@@ -536,12 +537,15 @@ def _need_heads(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
-        raise ValueError(f"{name} must have shape [T, {heads}, {head_dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError(f"{name} must have shape [T, {heads}, {head_dim}], got {tuple(shape)}")
+    tokens = shape[0]
     if not t.is_cuda and t.numel():
         raise ValueError(f"{name} must be a CUDA tensor")
+    if tokens <= 1 and t.is_contiguous():
+        return heads * head_dim
     step, head_step, one = t.stride()
-    tokens = t.shape[0]
     if tokens and (one != 1 or (head_step != head_dim and heads > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return step if tokens > 1 else heads * head_dim
@@ -560,8 +564,10 @@ def kv_cache_store(k, v, slots, codes, params, stream=None):
     if v.shape[0] != t:
         raise ValueError("k and v disagree on T")
     _need(slots, torch.int64, (t,), "slots")
-    _check(lib().kv_cache_store(_ptr(k), _ptr(v), k_step, v_step, _ptr(slots), _ptr(codes), _ptr(params), t, h, d,
-                                bits, page, pages, _stream(stream)), "kv_cache_store")
+    st = lib().kv_cache_store(k.data_ptr(), v.data_ptr(), k_step, v_step, slots.data_ptr(), codes.data_ptr(),
+                              params.data_ptr(), t, h, d, bits, page, pages, _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_store")
     return codes, params
 
 
@@ -571,14 +577,19 @@ def kv_cache_load(codes, params, slots, head_dim, k=None, v=None, stream=None):
     pages, heads, page, bits = _kv_cache(codes, params, head_dim)
     t = slots.shape[0]
     _need(slots, torch.int64, (t,), "slots")
+    shape = (t, heads, head_dim)
     if k is None:
-        k = torch.empty((t, heads, head_dim), dtype=torch.bfloat16, device=codes.device)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+    else:
+        _need(k, torch.bfloat16, shape, "k")
     if v is None:
-        v = torch.empty((t, heads, head_dim), dtype=torch.bfloat16, device=codes.device)
-    _need(k, torch.bfloat16, (t, heads, head_dim), "k")
-    _need(v, torch.bfloat16, (t, heads, head_dim), "v")
-    _check(lib().kv_cache_load(_ptr(codes), _ptr(params), _ptr(slots), _ptr(k), _ptr(v), t, heads, head_dim, bits,
-                               page, pages, _stream(stream)), "kv_cache_load")
+        v = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+    else:
+        _need(v, torch.bfloat16, shape, "v")
+    st = lib().kv_cache_load(codes.data_ptr(), params.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), t,
+                             heads, head_dim, bits, page, pages, _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_load")
     return k, v
 
 
@@ -625,7 +636,8 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
         max_q = 1 if q_offsets is None else max(t, 1)
     if out is None:
         out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=codes.device)
-    _need(out, torch.bfloat16, (t, hq, d), "out")
+    else:
+        _need(out, torch.bfloat16, (t, hq, d), "out")
     if workspace is None:
         size = 0
         if t and b:
@@ -640,8 +652,11 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
     else:
         _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
         size = workspace.numel()
-    _check(lib().kv_cache_attention(_ptr(q), q_step, _ptr(codes), _ptr(params), _ptr(page_table), width,
-                                    _ptr(kv_lens), _ptr(q_offsets), _ptr(out), b, t, hq, heads, d, bits, page, pages,
-                                    max_q, window, d ** -0.5 if scale is None else scale, _ptr(workspace), size,
-                                    _stream(stream)), "kv_cache_attention")
+    st = lib().kv_cache_attention(q.data_ptr(), q_step, codes.data_ptr(), params.data_ptr(), page_table.data_ptr(), width,
+                                  kv_lens.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
+                                  out.data_ptr(), b, t, hq, heads, d, bits, page, pages, max_q, window,
+                                  d ** -0.5 if scale is None else scale,
+                                  None if workspace is None else workspace.data_ptr(), size, _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_attention")
     return out

@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                     it.row0 = row0;
                     it.rows = rows;
                     it.h = c.h;
-                    it.last_cta = kv_owner(range.total, range.ctas, c.at + kCost + c.span.tiles - 1);
+                    it.last_cta = kv_owner(range, c.at + kCost + c.span.tiles - 1, blockIdx.x);
                     it.pad = 0;
                     p.split[blockIdx.x] = it;
                 }
@@ -685,6 +685,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnPa
     __shared__ float sums[kJoinWarps][kJoinWarps][D];  // [warp][row]
     __shared__ float totals[kJoinWarps][kJoinWarps];
     pdl_wait();
+    if constexpr (ROWS <= 16) pdl_launch_dependents();  // (one wave)
     const KvSplitItem it = p.split[blockIdx.x];
     const int r0 = blockIdx.y * kJoinWarps;
     if (r0 >= it.rows) return;
@@ -805,7 +806,7 @@ struct Plan {
 // Contexts of up to this many tiles (by the page table's width) run as clusters
 // when all clusters fit the device at once.
 constexpr int kClusterSize = 8;
-constexpr int64_t kClusterTiles = 64;
+constexpr int64_t kClusterTiles = 128;
 
 Plan make_plan(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int64_t bits, int sms) {
     Plan pl;

@@ -30,6 +30,7 @@ namespace {
 constexpr int kKvThreads = 256;
 constexpr int kKvChannels = 16;  // channels per thread
 constexpr int kKvRows = 2;       // rows per thread
+constexpr unsigned kKvOneWave = 512;  // blocks that surely run at once
 
 struct KvMoveParams {
     KvCache cache;
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const uint16_t* __
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
     pdl_wait();
+    if (gridDim.x <= kKvOneWave) pdl_launch_dependents();
     uint4 w[kKvRows][2];
     int64_t slot[kKvRows];
 #pragma unroll
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
     pdl_wait();
+    if (gridDim.x <= kKvOneWave) pdl_launch_dependents();
     int64_t index[kKvRows];
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) index[i] = row[i].there ? __ldg(p.slots + row[i].t) : -1;

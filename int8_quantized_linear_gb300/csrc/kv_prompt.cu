@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     it.row0 = c.rb * kRows;
                     it.rows = min(kRows, c.seq.nq * p.G - it.row0);
                     it.h = c.h;
-                    it.last_cta = kv_owner(range.total, range.ctas, c.at + kCost + c.span.tiles - 1);
+                    it.last_cta = kv_owner(range, c.at + kCost + c.span.tiles - 1, blockIdx.x);
                     it.pad = 0;
                     p.split[blockIdx.x] = it;
                 }

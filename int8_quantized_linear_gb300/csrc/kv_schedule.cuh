@@ -189,13 +189,21 @@ struct KvLocate {
 
 struct KvRange {
     int64_t total, begin, end;  // tiles and costs of all items; this CTA's range
-    int64_t ctas;               // CTAs that have a range (those behind have none)
+    uint32_t ctas;              // CTAs that have a range (those behind have none)
 };
 
-// Where the range of CTA i of n begins.
-__device__ __forceinline__ int64_t kv_cut(int64_t total, int64_t i, int64_t n) {
-    return (total / n) * i + (total % n) * i / n;
-}
+// Where the ranges of n CTAs begin: CTA i's at each * i + more * i / n (i, n and
+// more < n below 2^16: a 32-bit division).
+struct KvCuts {
+    int64_t each;
+    uint32_t more, n;
+    __device__ __forceinline__ KvCuts(int64_t total, uint32_t ctas) : n(ctas) {
+        // (the 64-bit division alone takes as long as the rest of a short call's prologue)
+        each = total < ((int64_t)1 << 32) ? (int64_t)((uint32_t)total / n) : total / n;
+        more = (uint32_t)(total - each * n);
+    }
+    __device__ __forceinline__ int64_t at(uint32_t i) const { return each * i + more * i / n; }
+};
 
 // This CTA's range and the cursor at its beginning.  Called by all THREADS
 // threads of the block (whole warps).
@@ -245,9 +253,10 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
         }
         if (pass == 0) {
             r.total = carry;
-            r.ctas = min((int64_t)gridDim.x, max(carry, (int64_t)1));
-            r.begin = kv_cut(carry, min((int64_t)blockIdx.x, r.ctas), r.ctas);
-            r.end = kv_cut(carry, min((int64_t)blockIdx.x + 1, r.ctas), r.ctas);
+            r.ctas = (uint32_t)min((int64_t)gridDim.x, max(carry, (int64_t)1));
+            const KvCuts cuts(carry, r.ctas);
+            r.begin = cuts.at(min(blockIdx.x, r.ctas));
+            r.end = cuts.at(min(blockIdx.x + 1, r.ctas));
         }
     }
     __syncthreads();
@@ -283,19 +292,22 @@ __device__ __forceinline__ KvRange kv_locate(const KvAttnParams& p, KvLocate& sm
         }
     }
     c.span = kv_span<ROWS, TILE>(p, c.seq, c.rb);
-    c.h = (int)(left / (c.span.tiles + COST));
-    left -= (int64_t)c.h * (c.span.tiles + COST);
+    const int per_head = c.span.tiles + COST;
+    c.h = left < ((int64_t)1 << 32) ? (int)((uint32_t)left / (uint32_t)per_head) : (int)(left / per_head);
+    left -= (int64_t)c.h * per_head;
     c.at = r.begin - left;
     c.tile = (int)max(left - COST, (int64_t)0);
     return r;
 }
 
-// The CTA whose range holds place x.
-__device__ __forceinline__ int kv_owner(int64_t total, int64_t n, int64_t x) {
-    int64_t i = (int64_t)((double)x * (double)n / (double)total);
-    i = min(max(i, (int64_t)0), n - 1);
-    while (i > 0 && kv_cut(total, i, n) > x) --i;
-    while (i + 1 < n && kv_cut(total, i + 1, n) <= x) ++i;
+// The CTA whose range holds place x, from CTA `from` on.
+__device__ __forceinline__ int kv_owner(const KvRange& r, int64_t x, uint32_t from) {
+    const KvCuts cuts(r.total, r.ctas);
+    // an estimate from below, then the few steps that are left
+    const float est = (float)x / (float)r.total * (float)r.ctas - 2.0f;
+    uint32_t i = max(from, (uint32_t)fmaxf(est, 0.0f));
+    while (i > from && cuts.at(i) > x) --i;
+    while (i + 1 < r.ctas && cuts.at(i + 1) <= x) ++i;
     return (int)i;
 }
 
