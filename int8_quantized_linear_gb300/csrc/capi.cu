@@ -520,7 +520,8 @@ i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8
                                void* stream) {
     I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
     I8QL_TRY(check_kv_attention(B, T_q, Hq, H, page_size, table_width, max_q));
-    if (window < 0 || !std::isfinite(softmax_scale)) return I8QL_ERR_INVALID_ARG;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (window < 0 || !std::isfinite(scale_log2)) return I8QL_ERR_INVALID_ARG;
     if (q_offsets == nullptr && T_q != B) return I8QL_ERR_INVALID_ARG;
     I8QL_TRY(check_strided(q, T_q, Hq * D, q_stride));
     I8QL_TRY(check_matrix(codes, T_q));
@@ -554,7 +555,7 @@ i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8
     p.T_q = T_q;
     p.G = (int)G;
     p.window = window;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.err = env.err;
     return from_cuda(launch_kv_attention(p, D, bits, max_q, workspace, env));
 }

@@ -46,7 +46,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "kv_math.cuh"
@@ -832,16 +831,8 @@ size_t part_bytes(int64_t ctas, int64_t rows, int64_t D) { return (size_t)(ctas 
 template <int D, int BITS, int HALVES, int S>
 cudaError_t launch_size(const KvAttnParams& p, const Plan& pl, const LaunchEnv& env) {
     using C = Cfg<D, BITS, 8 * HALVES>;
-    static std::once_flag once[64];
-    static cudaError_t set[64];
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem<kv_attention_kernel<D, BITS, HALVES, S>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    std::call_once(once[dev & 63], [&] {
-        set[dev & 63] = cudaFuncSetAttribute(kv_attention_kernel<D, BITS, HALVES, S>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    });
-    if (set[dev & 63] != cudaSuccess) return set[dev & 63];
     return launch_kernel(kv_attention_kernel<D, BITS, HALVES, S>, dim3((unsigned)pl.ctas), dim3(kThreads), C::kSmem,
                          env.stream, S > 0 ? dim3(S, 1, 1) : kNoCluster, p);
 }

@@ -2,6 +2,8 @@
 // (exact), wide shared-memory loads, bulk copies of pages.
 #pragma once
 
+#include <atomic>
+
 #include "kv_schedule.cuh"
 #include "quant_math.cuh"
 #include "tc_common.cuh"
@@ -130,6 +132,20 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                      tc::smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                  : "memory");
+}
+
+// Lets KERNEL use `bytes` of dynamic shared memory on the current device (below
+// 64, as launch_env checks); the runtime is told once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<bool> allowed[64];
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (allowed[dev & 63].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) allowed[dev & 63].store(true, std::memory_order_release);
+    return e;
 }
 
 }  // namespace

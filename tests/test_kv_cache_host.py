@@ -87,6 +87,7 @@ def test_attention_refusals(lib):
     assert f(*_with(ok, _18=-1)) == INVALID
     assert f(*_with(ok, _19=float("nan"))) == INVALID
     assert f(*_with(ok, _19=float("inf"))) == INVALID
+    assert f(*_with(ok, _19=3e38)) == INVALID              # times log2 e leaves fp32
     for i in (5, 11, 12, 17):
         assert f(*_with(ok, **{f"_{i}": 0})) == INVALID
     assert f(*_with(ok, _9=0, _7=E)) == INVALID            # query tokens of no sequence
