@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                 lo[x][y] = there && p.window > 0 ? (int)max(base + j + 1 - p.window, (int64_t)0) : 0;
             }
         }
+        const int seen_begin = c.span.begin, seen_end = c.span.end;
+        const int first_token = (c.span.first + c.tile) * kTile + warp * kWarpTokens;
         // tokens [all_lo, all_hi] are seen by every row
         const int all_hi = base + row0 / p.G;
         const int all_lo = p.window > 0 ? (int)max(base + (row0 + rows - 1) / p.G + 1 - p.window, (int64_t)0) : 0;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             {
                 const uint32_t* params = reinterpret_cast<const uint32_t*>(st + 2 * C::kCodes) + warp * kWarpTokens + lane;
                 uint32_t pk = params[0], pv = params[kTile];
-                if (EDGE && (token + lane >= c.span.end || token + lane < c.span.begin)) pk = pv = 0;  // may be anything
+                if (EDGE && (token + lane >= seen_end || token + lane < seen_begin)) pk = pv = 0;  // may be anything
                 const float ks = kv_scale(pk), vs = kv_scale(pv);
                 const uint32_t bits = __float_as_uint(vs);
                 const int e = (int)(__reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u) >> 23);
@@ -498,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
         for (int i = 0; i < n; ++i) {
             const bool ok = tc::warp_wait(&full[stage], parity, &abort_flag, p.err);
             const uint8_t* st = smem + stage * C::kStageBytes;
-            const int token = (c.span.first + c.tile + i) * kTile + warp * kWarpTokens;
-            if (ok) {
+            const int token = first_token + i * kTile;
+            // (a warp whose tokens no row sees has nothing to do)
+            if (ok && token < seen_end && token + kWarpTokens > seen_begin) {
                 if (token + kWarpTokens - 1 > all_hi || token < all_lo)
                     step(st, token, std::true_type{});
                 else

@@ -371,11 +371,19 @@ def test_single_token_form_equals_offsets():
     assert torch.equal(p.run(single=True), p.run(single=False))
 
 
-@pytest.mark.parametrize("batch", [159, 161, 400])
-def test_many_sequences(batch):
+@pytest.mark.parametrize("batch,most", [(159, 300), (161, 300), (400, 300), (641, 200), (1500, 150)])
+def test_many_sequences(batch, most):
     rng = np.random.default_rng(batch)
     nqs = rng.integers(0, 3, batch).tolist()
-    p = Problem(rng.integers(0, 300, batch).tolist(), nqs, 4, 2, 64, 4, 16, batch)
+    p = Problem(rng.integers(0, most, batch).tolist(), nqs, 4, 2, 64, 4, 16, batch)
+    p.check(p.run())
+
+
+def test_many_prompts():
+    """More prompts than one round of the work sharing looks at, most of them empty."""
+    rng = np.random.default_rng(0)
+    nqs = [int(n) if rng.random() < 0.03 else 0 for n in rng.integers(1, 90, 2100)]
+    p = Problem([n + int(rng.integers(0, 60)) for n in nqs], nqs, 4, 2, 64, 4, 16, 2100)
     p.check(p.run())
 
 
