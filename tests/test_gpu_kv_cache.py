@@ -122,6 +122,24 @@ def test_store_and_load(bits, d, t, h, page, fused):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("ahead", [8, 16, 24])
+def test_load_into_any_16_byte_boundary(bits, d, ahead):
+    t, h, page = 77, 3, 16
+    rng = np.random.default_rng(ahead)
+    codes, params = _cache(6, h, page, d, bits)
+    x = _rows(rng, t, h, d).cuda()
+    slots = torch.from_numpy(rng.permutation(6 * page)[:t].astype(np.int64)).cuda()
+    capi.kv_cache_store(x, -x, slots, codes, params)
+    want = capi.kv_cache_load(codes, params, slots, d)
+    room = torch.full((2, t * h * d + 48), 7.0, dtype=torch.bfloat16, device="cuda")
+    kb, vb = (r[n:n + t * h * d].view(t, h, d) for r, n in zip(room, (ahead, 16)))
+    capi.kv_cache_load(codes, params, slots, d, k=kb, v=vb)
+    assert torch.equal(kb, want[0]) and torch.equal(vb, want[1])
+    for r, n in zip(room, (ahead, 16)):
+        assert (r[:n] == 7).all() and (r[n + t * h * d:] == 7).all()
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_codes_are_the_rounded_quotients(bits):
     """A million rows' worth of quotients over all scales a row can have, ties and their neighbours among them."""
