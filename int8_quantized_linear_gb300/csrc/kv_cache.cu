@@ -14,10 +14,13 @@
 // Both are bound by bytes: a token of 8 heads x 128 channels is 4 KB of bf16
 // and 1 KB of 4-bit rows.  A thread takes 16 channels of several rows, D / 16
 // neighbouring lanes a row; minimum and maximum go through shuffles, so a row is
-// read once and nothing is staged.  (16 channels, not 8: what a row costs beside
-// its elements, addresses and scale, is then shared by half as many lanes.)  The rows of a
-// thread are loaded together, and keys and values beside their slots: one row
-// at a time, behind its slot, reached a third of the bandwidth.
+// read once and nothing is staged.  (16 channels, not 8:
+// what a row costs beside its elements, addresses and scale, is then shared by half
+// as many lanes.)  A thread's two rows are the key and the value of one token and head,
+// loaded together and beside their slot, so that their place is worked out once:
+// 127.6 us against 139.9 with two unrelated rows (131072 tokens of 8 heads x 128
+// channels, 4 bits).  One row at a time, behind its slot, reached a third of the
+// bandwidth.
 
 #include <cuda_runtime.h>
 
@@ -31,46 +34,46 @@ namespace {
 // (4 bits), 33.4 with 256 threads.
 constexpr int kKvThreads = 128;
 constexpr int kKvChannels = 16;  // channels per thread
-constexpr int kKvRows = 2;       // rows per thread
+constexpr int kKvRows = 2;       // rows per thread: a token's key and value of a head
 constexpr unsigned kKvOneWave = 1024;  // blocks that surely run at once
 
 struct KvMoveParams {
     KvCache cache;
     const int64_t* slots;
-    uint32_t rows;   // T * 2 * H < 2^31
-    uint32_t two_h;  // rows of a token
-    uint32_t inv;    // floor(2^32 / two_h)
+    uint32_t rows;  // T * H < 2^31
+    uint32_t inv;   // floor(2^32 / H), or 2^32 - 1
     int64_t slot_limit;
     bool wide;  // load: keys and values lie on 32-byte boundaries
     unsigned* err;
 };
 
-// A row of keys or values that a thread works on.
+// The token and head whose key and value a thread works on.
 struct KvMoveRow {
     bool there;
     uint32_t t;  // token
-    int kv, h;   // key (0) or value (1), head
+    uint32_t h;  // head
 };
 
 template <int D>
-__device__ __forceinline__ KvMoveRow move_row(const KvMoveParams& p, int i) {
+__device__ __forceinline__ KvMoveRow move_row(const KvMoveParams& p) {
     constexpr int kGroups = kKvThreads / (D / kKvChannels);  // rows side by side in a block
-    const uint32_t row = (blockIdx.x * kKvRows + i) * kGroups + threadIdx.x / (D / kKvChannels);
+    const uint32_t row = blockIdx.x * kGroups + threadIdx.x / (D / kKvChannels), heads = (uint32_t)p.cache.H;
     KvMoveRow r;
     r.there = row < p.rows;
-    // row / two_h: the estimate is at most one too small (row < 2^31)
+    // row / heads: the estimate is at most one too small (row < 2^31)
     r.t = __umulhi(row, p.inv);
-    uint32_t in_token = row - r.t * p.two_h;
-    if (in_token >= p.two_h) {
+    r.h = row - r.t * heads;
+    if (r.h >= heads) {
         ++r.t;
-        in_token -= p.two_h;
+        r.h -= heads;
     }
-    r.kv = in_token >= (uint32_t)p.cache.H;
-    r.h = (int)in_token - (r.kv ? p.cache.H : 0);
     return r;
 }
 
-// Its row of the cache, or -1.
+// Cache rows from a key to its value.
+__device__ __forceinline__ int64_t value_rows(const KvCache& c) { return (int64_t)c.H << c.page_shift; }
+
+// The key's row of the cache, or -1; the value's is value_rows on.
 __device__ __forceinline__ int64_t cache_row(const KvMoveParams& p, const KvMoveRow& r, int64_t slot) {
     if (!r.there || slot < 0) return -1;
     if (slot >= p.slot_limit) {
@@ -78,7 +81,7 @@ __device__ __forceinline__ int64_t cache_row(const KvMoveParams& p, const KvMove
         return -1;
     }
     const int64_t page = slot >> p.cache.page_shift;
-    return kv_row(p.cache, page, r.kv, r.h, (int)(slot - (page << p.cache.page_shift)));
+    return kv_row(p.cache, page, 0, (int)r.h, (int)(slot - (page << p.cache.page_shift)));
 }
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
@@ -148,36 +151,32 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// 32768 tokens of 8 heads x 128 channels, 4 bits: 41.6 us, 4080 GB/s (60 % of a
-// copy).  Bound by instruction issue (two thirds of the cycles issue, and warps
-// wait for the arithmetic pipes): what the codes take an element, and what a
-// row's addresses and scale take.  10 blocks an SM: with the registers that the
-// compiler takes unasked, fewer warps run, and it takes 2 us more.
+// 32768 tokens of 8 heads x 128 channels, 4 bits: 39.6 us, 4300 GB/s (63 % of a
+// copy; 131072 tokens: 128 us, 5320 GB/s).  Bound by instruction issue: what the
+// codes take an element, and what a row's scale takes.  10 blocks an SM: with the
+// registers that the compiler takes unasked, fewer warps run, and it takes 2 us more.
 template <int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads, 10) kv_store_kernel(const uint16_t* __restrict__ k,
                                                                   const uint16_t* __restrict__ v, int64_t k_stride,
                                                                   int64_t v_stride, KvMoveParams p) {
     constexpr int kLanes = D / kKvChannels;
     const int lane = threadIdx.x % kLanes;
-    KvMoveRow row[kKvRows];
-#pragma unroll
-    for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
+    const KvMoveRow row = move_row<D>(p);
     pdl_wait();
     if (gridDim.x <= kKvOneWave) pdl_launch_dependents();
     uint4 w[kKvRows][2];
-    int64_t slot[kKvRows];
+    int64_t slot = -1;
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
-        const KvMoveRow& r = row[i];
         w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-        slot[i] = -1;
-        if (r.there) {
-            const uint16_t* src = (r.kv ? v + r.t * v_stride : k + r.t * k_stride) + (int64_t)r.h * D + lane * kKvChannels;
+        if (row.there) {
+            const uint16_t* src = (i ? v + row.t * v_stride : k + row.t * k_stride) + (int64_t)row.h * D + lane * kKvChannels;
             w[i][0] = __ldg(reinterpret_cast<const uint4*>(src));
             w[i][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-            slot[i] = __ldg(p.slots + r.t);
         }
     }
+    if (row.there) slot = __ldg(p.slots + row.t);
+    const int64_t key = cache_row(p, row, slot);
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
         // Over the thread's pairs; then as a pair (lo, -hi), of which one minimum does
@@ -190,8 +189,8 @@ __global__ void __launch_bounds__(kKvThreads, 10) kv_store_kernel(const uint16_t
         uint32_t ends = min_bf16x2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
         for (int m = 1; m < kLanes; m <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
-        const int64_t index = cache_row(p, row[i], slot[i]);
-        if (index < 0) continue;
+        if (key < 0) continue;
+        const int64_t index = i ? key + value_rows(p.cache) : key;
         const float lo = lo_bf16(ends), hi = -hi_bf16(ends);
         const float ratio = divided_by<(1 << BITS) - 1>(__fsub_rn(hi, lo));  // >= 0
         const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
@@ -225,16 +224,11 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                              KvMoveParams p) {
     const int lane = threadIdx.x % (D / kKvChannels);
-    KvMoveRow row[kKvRows];
-#pragma unroll
-    for (int i = 0; i < kKvRows; ++i) row[i] = move_row<D>(p, i);
+    const KvMoveRow row = move_row<D>(p);
     pdl_wait();
     if (gridDim.x <= kKvOneWave) pdl_launch_dependents();
-    int64_t index[kKvRows];
-#pragma unroll
-    for (int i = 0; i < kKvRows; ++i) index[i] = row[i].there ? __ldg(p.slots + row[i].t) : -1;
-#pragma unroll
-    for (int i = 0; i < kKvRows; ++i) index[i] = cache_row(p, row[i], index[i]);
+    const int64_t key = cache_row(p, row, row.there ? __ldg(p.slots + row.t) : -1);
+    if (!row.there) return;
     constexpr int kWords = kKvChannels * BITS / 32;
     uint32_t codes[kKvRows][kWords];
     uint32_t param[kKvRows];
@@ -243,8 +237,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
 #pragma unroll
         for (int j = 0; j < kWords; ++j) codes[i][j] = 0;
         param[i] = 0;  // stands for 0
-        if (index[i] >= 0) {
-            const uint8_t* src = p.cache.codes + index[i] * (D * BITS / 8) + lane * (kWords * 4);
+        if (key >= 0) {
+            const int64_t index = i ? key + value_rows(p.cache) : key;
+            const uint8_t* src = p.cache.codes + index * (D * BITS / 8) + lane * (kWords * 4);
             if constexpr (BITS == 4) {
                 const uint2 v = *reinterpret_cast<const uint2*>(src);
                 codes[i][0] = v.x;
@@ -256,12 +251,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
                 codes[i][2] = v.z;
                 codes[i][3] = v.w;
             }
-            param[i] = p.cache.params[index[i]];
+            param[i] = p.cache.params[index];
         }
     }
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
-        if (!row[i].there) continue;
         const float s = kv_scale(param[i]), lo = kv_low(param[i]);
         uint64_t s2, lo2, base2;
         asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
@@ -289,7 +283,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(uint16_t* __restric
                 : "=r"(out[j])
                 : "r"(a), "r"(b), "l"(base2), "l"(s2), "l"(lo2));
         }
-        uint4* dst = reinterpret_cast<uint4*>((row[i].kv ? v : k) + ((int64_t)row[i].t * p.cache.H + row[i].h) * D +
+        uint4* dst = reinterpret_cast<uint4*>((i ? v : k) + ((int64_t)row.t * p.cache.H + row.h) * D +
                                               lane * kKvChannels);
         // (two 16-byte stores each fill half of every sector: 35.5 against 33.4 us
         // for 32768 tokens of 8 heads x 128 channels, 4 bits)
@@ -308,9 +302,8 @@ KvMoveParams move_params(const KvCache& cache, const int64_t* slots, int64_t T, 
     KvMoveParams p;
     p.cache = cache;
     p.slots = slots;
-    p.rows = (uint32_t)(T * 2 * cache.H);
-    p.two_h = (uint32_t)(2 * cache.H);
-    p.inv = (uint32_t)(((uint64_t)1 << 32) / p.two_h);
+    p.rows = (uint32_t)(T * cache.H);
+    p.inv = cache.H == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / (uint64_t)cache.H);
     p.slot_limit = cache.pages << cache.page_shift;
     p.wide = false;
     p.err = env.err;
@@ -318,7 +311,7 @@ KvMoveParams move_params(const KvCache& cache, const int64_t* slots, int64_t T, 
 }
 
 dim3 move_grid(uint32_t rows, int64_t D) {
-    const int64_t per_block = kKvThreads / (D / kKvChannels) * kKvRows;
+    const int64_t per_block = kKvThreads / (D / kKvChannels);
     return dim3((unsigned)((rows + per_block - 1) / per_block));
 }
 
