@@ -44,7 +44,7 @@
 // in flight (61 KB a block at 4 bits and 128 channels, three blocks an SM).
 //
 // Measured, 32 query heads over 8 x 128, one token a sequence: 128 sequences of
-// 16384 tokens in 436 us at 4 bits (5.2 TB/s, 77 % of a copy; warps wait on
+// 16384 tokens in 437 us at 4 bits (5.2 TB/s, 77 % of a copy; warps wait on
 // the chain unpack, product, softmax and for each other's issue slots), 64 of
 // 4096 in 51 us with the join; at 8 bits, which unpack with fewer instructions
 // a byte, 64 of 16384 in 340 us (6.5 TB/s, 96 %).  Pages of 16 tokens: 3.8 TB/s

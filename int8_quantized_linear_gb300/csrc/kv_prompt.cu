@@ -37,7 +37,7 @@
 // rows are copied eight tokens at a time to a stride 16 bytes longer, which
 // keeps the transposing reads off each other's banks.
 //
-// Measured: those two chunks now 482 us with the join (998 TFLOP/s, 52 % of a
+// Measured: those two chunks now 481 us with the join (1000 TFLOP/s, 52 % of a
 // large bf16 product; the tensor pipe is busy 44 % of the time, the issue slots
 // 53 %), one prompt of 8192 tokens 586 us (938 TFLOP/s).
 
