@@ -625,8 +625,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 for (int i = 0; i < n; ++i, ++steps) {
                     const int token = first + i * kTile;
                     const uint32_t k = kt + i;
-                    wait(&info_full[k % kInfo], (k / kInfo) & 1);
+                    // S first: an M tile that sat out an item may be two rounds of
+                    // info_full behind, whose parity then passes at once; after this
+                    // tile's S its exponents are there (they were written before K),
+                    // and no later ones can be (those wait for this tile's P)
                     wait(&s_full[m], steps & 1);
+                    wait(&info_full[k % kInfo], (k / kInfo) & 1);
                     tc::tc_fence_after();
                     if (!dead) {
                         const TileInfo info = infos[k % kInfo];

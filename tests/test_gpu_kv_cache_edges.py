@@ -1,0 +1,53 @@
+"""GPU tests of attention over the quantized cache where its parts meet: row
+blocks of different heights in one block's range, values that must not reach
+other rows, magnitudes far apart.  Bounds: tests/kv_reference.py."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from int8_quantized_linear_gb300 import capi
+from tests.kv_reference import check
+from tests.test_gpu_kv_cache import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library(cuda_device):
+    from int8_quantized_linear_gb300 import build
+    build.build()
+    capi.lib()
+    assert capi.i8ql_get_device_error() == capi.I8QL_OK
+    yield
+    assert capi.i8ql_get_device_error() == capi.I8QL_OK
+
+
+def rescale(p, factor):
+    """Multiplies keys and values of every sequence by powers of two: factor(b, kv, tokens) -> exponents."""
+    for b, (c, s, low) in enumerate(p.seqs):
+        n = p.lens[b]
+        if not n:
+            continue
+        f = np.stack([np.exp2(factor(b, kv, np.arange(n))) for kv in (0, 1)]).astype(np.float32)[:, :, None]
+        p.seqs[b] = (c, s * f, low * f)
+        pages = -(-n // p.page)
+        full = torch.ones((2, pages * p.page))
+        full[:, :n] = torch.from_numpy(f[..., 0])
+        at = p.table[b, :pages].long()
+        p.params[at] = (p.params[at].float() * full.view(2, pages, 1, p.page, 1).transpose(0, 1).cuda()).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+def test_low_row_blocks_between_high_ones(bits, d):
+    """Blocks of at most 128 rows leave the second M tile out, blocks of more take it back in; both walk many tiles, of
+    exponents that differ from tile to tile."""
+    lens = [1500, 1300] * 40
+    p = Problem(lens, [50, 9] * 40, 8, 2, d, bits, 16, 7 + bits, spread=0.5)
+    rescale(p, lambda b, kv, j: (j // 128 * (3 + b + kv)) % 5 - 2)
+    y = p.run()
+    check(p, y)
+    for _ in range(5):
+        assert torch.equal(p.run(), y)
