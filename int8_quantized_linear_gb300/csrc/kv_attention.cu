@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                 }
                 const unsigned copies = __popc(__ballot_sync(0xffffffffu, need)) / 4;
                 ok = tc::warp_wait(&empty[stage], parity ^ 1, &abort_flag, p.err);
+                // a consumer that gave up says so before it frees a stage that it
+                // did not wait for, whose copies may still be on their way
+                ok = ok && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&abort_flag));
                 if (!ok) break;
                 if (lane == 0) tc::mbar_expect_tx(&full[stage], copies * piece * (2 * C::kRowBytes + 8));
                 __syncwarp();
@@ -240,17 +243,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             }
             advance(c);
         }
-        if (!ok) {
-            // giving up: let the copies in flight land before the block's
-            // shared memory can go to another
-            for (int i = 0; i < min(issued, kStages); ++i) {
-                int none = 0;
-                if (--stage < 0) {
-                    stage = kStages - 1;
-                    parity ^= 1;
-                }
-                tc::mbar_wait(&full[stage], parity, &none, p.err);
+        // the last copies land before the block's shared memory can go to
+        // another (the consumers may have given up on them)
+        for (int i = 0; i < min(issued, kStages); ++i) {
+            int none = 0;
+            if (--stage < 0) {
+                stage = kStages - 1;
+                parity ^= 1;
             }
+            tc::mbar_wait(&full[stage], parity, &none, p.err);
         }
         return;
     }

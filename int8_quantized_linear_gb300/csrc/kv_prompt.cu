@@ -268,6 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         const int at = (lane >> 2) * piece;
         const int at_v = lane * 8;  // V codes: eight tokens
         uint32_t kt = 0;            // tiles so far
+        uint32_t keys_issued = 0, values_issued = 0;
+        // An unpacking warp that gave up says so before it frees raw tiles that it
+        // did not wait for, whose copies may still be on their way.
+        auto wait_free = [&](uint64_t* bar, uint32_t parity) {
+            wait(bar, parity);
+            dead = dead || __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&abort_flag));
+        };
         while (const int n = dead ? 0 : kv_take<kCost>(p, c, found.end)) {
             const int32_t* table = p.table + c.b * p.table_width;
             const int first = (c.span.first + c.tile) * kTile;
@@ -293,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 const uint32_t slot = kt % kRawKeys;
                 const unsigned keys = __popc(__ballot_sync(0xffffffffu, nk && kind == 0));
                 const unsigned groups = __popc(__ballot_sync(0xffffffffu, nv));
-                wait(&raw_k_empty[slot], ((kt / kRawKeys) & 1) ^ 1);
+                wait_free(&raw_k_empty[slot], ((kt / kRawKeys) & 1) ^ 1);
                 if (!dead) {
+                    ++keys_issued;
                     if (lane == 0) tc::mbar_expect_tx(&raw_k_full[slot], keys * piece * (C::kRowBytes + 8));
                     __syncwarp();
                     if (nk) {
@@ -309,8 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                                       p.cache.params + row, piece * 4, &raw_k_full[slot]);
                     }
                 }
-                wait(&raw_v_empty, (kt & 1) ^ 1);
+                wait_free(&raw_v_empty, (kt & 1) ^ 1);
                 if (!dead) {
+                    ++values_issued;
                     if (lane == 0) tc::mbar_expect_tx(&raw_v_full, groups * 8 * C::kRowBytes);
                     __syncwarp();
                     if (nv) {
@@ -323,17 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
             }
             if (!dead) kv_next_item<kRows, kTile, kCost>(p, c);
         }
-        if (dead) {
-            // giving up: let the copies in flight land before the block's
-            // shared memory can go to another (a wait for one that was never
-            // issued runs out)
-            for (uint32_t k = kt > kRawKeys ? kt - kRawKeys : 0; k <= kt; ++k) {
-                int none = 0;
-                tc::mbar_wait(&raw_k_full[k % kRawKeys], (k / kRawKeys) & 1, &none, p.err);
-            }
-            int none = 0;
-            if (kt > 0) tc::mbar_wait(&raw_v_full, (kt - 1) & 1, &none, p.err);
-        }
+        // the last copies land before the block's shared memory can go to
+        // another (the unpacking warps may have given up on them)
+        int none = 0;
+        for (uint32_t k = keys_issued > kRawKeys ? keys_issued - kRawKeys : 0; k < keys_issued; ++k)
+            tc::mbar_wait(&raw_k_full[k % kRawKeys], (k / kRawKeys) & 1, &none, p.err);
+        if (values_issued > 0) tc::mbar_wait(&raw_v_full, (values_issued - 1) & 1, &none, p.err);
     } else if (warp >= kSoftmaxWarps && warp < kCopyWarp) {
         // ------------------------------------------------------------ unpacking
         KvCursor c = start;

@@ -8,6 +8,12 @@ takes part in.  An M tile that sits out an item does not wait for that item's
 tiles, so when it comes back the parity of ``info_full`` may pass for a round
 that is not there yet, and then it has not acquired what the unpacking warps
 wrote.  Waiting for the tile's S first makes the second wait exact.
+
+Both kernels: a warp fills stages by bulk copies that consumer warps wait for.
+Every wait is bounded; a consumer whose wait ran out sets a flag and goes on
+without waiting, so it frees stages whose copies may not have landed.  The
+copying warp looks at the flag before it fills a stage, and waits for its last
+copies before it ends.
 """
 
 from __future__ import annotations
@@ -149,3 +155,84 @@ def test_the_other_order_passes_early():
         for seed in range(600):
             rng = random.Random(seed)
             prompt(items_of(rng), 2, False, rng)
+
+
+# ------------------------------------------------------------ rings of bulk copies
+
+class InFlight(Exception):
+    pass
+
+
+def ring(tiles, stages, consumers, looks, drains, rng):
+    """One ring of stages that a producer fills by copies and consumer warps empty, any of which may give up any wait
+    that does not pass at once (a bounded wait that ran out), and then goes on without waiting.  `looks`: the producer
+    reads the flag of a warp that gave up before it fills a stage; `drains`: at its end it waits for its last copies.
+    Raises InFlight when a stage is filled again, or the block ends, while copies into it are on their way."""
+    full, empty = [Barrier(1) for _ in range(stages)], [Barrier(consumers) for _ in range(stages)]
+    flying = [0] * stages  # copies on their way, by stage
+    state = {"abort": False, "done": 0}
+    patience = rng.choice([0.0, 0.02, 0.3])
+
+    def wait(bar, parity, result):
+        def ready():
+            result["ok"] = bar.passes(parity & 1)
+            if not result["ok"] and (state["abort"] or rng.random() < patience):
+                state["abort"] = True
+                return True
+            return result["ok"]
+        return ready
+
+    def producer():
+        r, issued = {}, 0
+        for k in range(tiles):
+            s = k % stages
+            yield wait(empty[s], (k // stages & 1) ^ 1, r)
+            if not r["ok"] or (looks and state["abort"]):
+                break
+            if full[s].left != 1 or flying[s]:
+                raise InFlight(f"stage {s} filled again")
+            full[s].tx += 1
+            flying[s] += 1
+            full[s].arrive()
+            issued += 1
+            yield lambda: True
+        if drains:
+            for k in range(max(issued - stages, 0), issued):
+                yield lambda k=k: full[k % stages].passes(k // stages & 1)
+        state["done"] += 1
+
+    def consumer():
+        r = {}
+        for k in range(tiles):
+            s = k % stages
+            yield wait(full[s], k // stages, r)
+            yield lambda: True
+            empty[s].arrive()
+        state["done"] += 1
+
+    def memory():
+        while state["done"] < consumers + 1 or any(flying):
+            if state["done"] == consumers + 1:
+                raise InFlight("the block ended")
+            s = rng.randrange(stages)
+            if flying[s]:
+                flying[s] -= 1
+                full[s].land(1)
+            yield lambda: True
+
+    run({"producer": producer(), "memory": memory(), **{f"consumer {i}": consumer() for i in range(consumers)}}, rng)
+
+
+@pytest.mark.parametrize("stages,consumers", [(1, 4), (2, 4), (3, 4)])
+def test_copies_land_in_the_block_that_waits_for_them(stages, consumers):
+    for seed in range(400):
+        rng = random.Random(seed)
+        ring(rng.randint(0, 9), stages, consumers, True, True, rng)
+
+
+@pytest.mark.parametrize("looks,drains", [(False, True), (True, False)])
+def test_either_omission_shows(looks, drains):
+    with pytest.raises(InFlight):
+        for seed in range(400):
+            rng = random.Random(seed)
+            ring(rng.randint(0, 9), 3, 4, looks, drains, rng)
