@@ -197,6 +197,30 @@ struct TileInfo {
     int val_exp;  // V is held times 2^(134 - val_exp), from this tile on
 };
 
+// The bits of a row's largest magnitude (a row is low .. low + scale * kTop); not
+// below infinity's when some element is not finite.
+template <int BITS>
+__device__ __forceinline__ uint32_t row_bits(uint32_t param) {
+    constexpr float kTop = BITS == 4 ? 15.0f : 255.0f;
+    const float lo = kv_low(param);
+    return max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(fmaf(kv_scale(param), kTop, lo)) & 0x7fffffffu);
+}
+
+// Whether the value rows of one of the sequence's tokens lo .. hi are not finite
+// (rare: only asked once a block has met such a row).
+template <int BITS>
+__device__ __noinline__ bool sees_not_finite(const KvAttnParams& p, const KvCursor& c, int lo, int hi) {
+    bool sees = false;
+#pragma unroll 1
+    for (int t = lo; t <= hi; ++t) {
+        int64_t page = p.table[c.b * p.table_width + (t >> p.cache.page_shift)];
+        if (page < 0 || page >= p.cache.pages) page = 0;  // (as copied)
+        const int off = t & ((1 << p.cache.page_shift) - 1);
+        sees = sees || row_bits<BITS>(p.cache.params[kv_row(p.cache, page, 1, c.h, off)]) >= 0x7f800000u;
+    }
+    return sees;
+}
+
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnParams p) {
     using C = Cfg<D, BITS>;
@@ -213,12 +237,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, low values
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
+    __shared__ int met_not_finite;  // some value row so far was not finite
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_at = tc::smem_u32(smem);
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        met_not_finite = 0;
         for (int i = 0; i < kRawKeys; ++i) {
             tc::mbar_init(&raw_k_full[i], 1);
             tc::mbar_init(&raw_k_empty[i], kUnpackWarps);
@@ -344,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         const int tid = threadIdx.x - kSoftmaxWarps * 32;  // 0 .. 127
         const int w4 = warp - kSoftmaxWarps;
         uint32_t kt = 0;
-        constexpr float kTop = BITS == 4 ? 15.0f : 255.0f;
         constexpr int kLanesPerKey = C::kRowBytes / 16;
         constexpr int kChunks = BITS == 4 ? 4 : 2;  // operand chunks (8 channels) per 16 raw bytes
         constexpr int kValWords = D * BITS / 256;   // raw words of D / 8 channels
@@ -365,13 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     pk = params[0];
                     pv = params[kTile];
                 }
-                auto magnitude = [](uint32_t param) {
-                    const float lo = kv_low(param);
-                    const uint32_t b = __float_as_uint(fmaxf(fabsf(lo), fabsf(fmaf(kv_scale(param), kTop, lo))));
-                    return b < 0x7f800000u ? b : 0u;
-                };
-                const uint32_t top_k = __reduce_max_sync(0xffffffffu, magnitude(pk));
-                const uint32_t top_v = __reduce_max_sync(0xffffffffu, magnitude(pv));
+                const uint32_t bits_k = row_bits<BITS>(pk);
+                uint32_t bits_v = row_bits<BITS>(pv);
+                if (bits_v >= 0x7f800000u) {
+                    // not finite: it must not meet the weight 0 of a row that does not
+                    // see it, so it counts as 0, and the rows that do see it look for it
+                    bits_v = pv = 0;
+                    met_not_finite = 1;
+                }
+                const uint32_t top_k = __reduce_max_sync(0xffffffffu, bits_k < 0x7f800000u ? bits_k : 0u);
+                const uint32_t top_v = __reduce_max_sync(0xffffffffu, bits_v);
                 if (lane == 0) {
                     exp_red[kt & 1][w4][0] = top_k;
                     exp_red[kt & 1][w4][1] = top_v;
@@ -725,6 +753,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     tc::tc_fence_before();
                     tc::mbar_arrive(&p_full[m]);
                 }
+                // (set, if at all, before the exponents of the tile that were waited for)
+                if (*reinterpret_cast<volatile int*>(&met_not_finite) && row.live &&
+                    sees_not_finite<BITS>(p, c, max(lo, first), min(hi, first + n * kTile - 1)))
+                    total = NAN;
             }
             if (begins && !ends) {
                 split = true;

@@ -51,3 +51,37 @@ def test_low_row_blocks_between_high_ones(bits, d):
     check(p, y)
     for _ in range(5):
         assert torch.equal(p.run(), y)
+
+
+NON_FINITE = [("scale", float("nan")), ("low", float("nan")), ("scale", float("inf")), ("low", float("-inf"))]
+
+
+@pytest.mark.parametrize("which,value", NON_FINITE)
+@pytest.mark.parametrize("lens,nqs,window", [([500, 70], [3, 1], 0), ([500, 70], [60, 1], 0), ([700, 130], [200, 90], 40),
+                                             ([5003, 900], [40, 70], 0)])
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 128), (4, 64), (8, 64)])
+def test_non_finite_rows_reach_only_rows_that_see_them(bits, d, lens, nqs, window, which, value):
+    """A token whose params are not finite, among the query tokens: rows that do not see it give the bits they give
+    when its params are zero, in few rows as in many; rows that see such a value are not a number."""
+    p = Problem(lens, nqs, 8, 2, d, bits, 16, 40 + bits)
+    first = lens[0] - nqs[0]
+    bad = [first + 1, first + nqs[0] // 2, lens[0] - 1]
+    at = [(int(p.table[0, t // 16]), t % 16) for t in bad]
+    sees = torch.zeros(p.q.shape[0], dtype=torch.bool)
+    for i in range(nqs[0]):
+        sees[i] = any(t <= first + i and (not window or t > first + i - window) for t in bad)
+    assert sees.any() and not sees.all()
+    for kv in (0, 1):
+        keep = p.params.clone()
+        for page, off in at:
+            p.params[page, kv, 1, off] = 0.0
+        want = p.run(window=window)
+        for page, off in at:
+            p.params[page, kv, 1, off, 0 if which == "scale" else 1] = value
+        y = p.run(window=window)
+        p.params = keep
+        assert torch.equal(y[:, :4], want[:, :4])          # the other cache head
+        assert torch.equal(y[~sees, 4:], want[~sees, 4:])  # rows that see none of them
+        if kv == 1:
+            assert torch.isnan(y[sees, 4:]).any(-1).all() or value in (float("inf"), float("-inf"))
+            assert not torch.isfinite(y[sees, 4:]).all(-1).any()
