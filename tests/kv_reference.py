@@ -1,8 +1,8 @@
 """Attention over a quantized cache in 64 bits, with element-wise error bounds of the kernels' arithmetic.
 
 Notation: o = sum_j p_j v_j over the tokens a row sees, v_j and k_j = low_j +
-s_j c_j, size = sum_j p_j |v_j|.  An output is rounded to bf16 (2^-9 of it);
-what stands before that rounding is off by at most
+s_j c_j, size = sum_j p_j |v_j|.  An output is rounded to bf16, 8 significant
+bits (2^-8 of it: 1 + 2^-8 becomes 1); what stands before that rounding is off by at most
 
 few query rows (max_q * G <= 32):
     2^-11 sum_j p_j s_j |c_j - z|   each weight p_j s_j rounded to fp16 before it meets the centred code (z: 8, 128)
@@ -70,7 +70,7 @@ def attended(q, codes, scale, low, n_q, window, softmax_scale, wide, centre):
         err = err + (torch.einsum("igj,jd->igd", r, v.abs()) + r.sum(-1)[..., None] * o.abs()) * lost
         err = err + 2.0 ** -14 * size
         out[:, h * g:(h + 1) * g] = o
-        bound[:, h * g:(h + 1) * g] += 2.0 ** -9 * o.abs() + 1.01 * err
+        bound[:, h * g:(h + 1) * g] += 2.0 ** -8 * o.abs() + 1.01 * err
     return out, bound
 
 
