@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
     __shared__ KvCursor cursors[kWarps];  // (kept out of the registers of the main loop)
     __shared__ KvRange range;
     __shared__ float merge_ml[kWarps][ROWS][2];
+    __shared__ float shrunk[kWarps][ROWS];  // by how much a row's unit and reference have been shrunk, where any has
     __shared__ __align__(16) float cta_ml[ROWS][2];  // (S > 0) this CTA's part
     __shared__ float4 factors[kWarps][kWarpTokens];  // of a token: K scale and offset, V scale and offset
     __shared__ int abort_flag;
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
         // what the weights are relative to (a logit; at most kSlack below the row's
         // maximum); this lane's share of the total and of sum w (low + z s)
         float m[HALVES][2], l[HALVES][2], z[HALVES][2];
+        bool any_shrunk = false;
         int unit = kValueShift;  // S = 2^(unit - 126) is above every value scale so far
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) {
@@ -445,6 +447,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
                     above |= top[x][y] > m[x][y] + kSlack;  // (the first time: from -infinity)
                 }
             if (__any_sync(0xffffffffu, above)) {
+                bool large = false;
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) large |= fabsf(top[x][y]) >= 0x1p23f && top[x][y] != -INFINITY;
+                large = __any_sync(0xffffffffu, large);
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
@@ -452,6 +460,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 #pragma unroll
                         for (int k = 4; k < 32; k <<= 1)
                             top[x][y] = fmaxf(top[x][y], __shfl_xor_sync(0xffffffffu, top[x][y], k));
+                    }
+                if (__builtin_expect(large, 0)) {  // (rare)
+#pragma unroll
+                    for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float shrink = shrink_reference(fmaxf(m[x][y], top[x][y]));
+                            m[x][y] *= shrink;
+                            top[x][y] *= shrink;
+                            q_unit[x][y] *= shrink;
+                            float& all = shrunk[warp][8 * x + 2 * t + y];
+                            if (g == 0) all = any_shrunk ? all * shrink : shrink;
+                        }
+                    any_shrunk = true;
+                }
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
                         const float to = fmaxf(m[x][y], top[x][y]);
                         const float by = to == -INFINITY ? 1.0f : exp2_approx(m[x][y] - to);
                         m[x][y] = to;
@@ -529,6 +556,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
             }
         }
 
+        if (__builtin_expect(any_shrunk, 0))
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) m[x][y] /= shrunk[warp][8 * x + 2 * t + y];
         // join the four warps: totals over the lanes of a row, then one common maximum
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)

@@ -44,6 +44,15 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// What brings a softmax reference (log2 units) below 2^23; 1 where it is.  A weight's
+// exponent is c a - m in one step, so it misses logit less reference by the rounding
+// of m, which has to stay small: c and m are shrunk together.  Logits of that size are
+// known to 2^-24 of their magnitude at best, which is more than shrinking blurs.
+__device__ __forceinline__ float shrink_reference(float m) {
+    const int e = (int)(__float_as_uint(m) >> 23 & 255) - 127;
+    return e < 23 || e == 128 ? 1.0f : pow2(22 - e);
+}
+
 // What is subtracted from a centred code.
 template <int BITS>
 constexpr float kCentre = BITS == 4 ? 8.0f : 128.0f;

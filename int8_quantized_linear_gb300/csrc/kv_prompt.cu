@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     __shared__ KvCursor cursors[kSoftmaxWarps];  // (kept out of the registers of the softmax)
     __shared__ KvRange range;
     __shared__ TileInfo infos[kInfo];
+    __shared__ float shrunk[kRows];  // by how much a row's unit and maximum have been shrunk
     __shared__ uint32_t exp_red[2][kUnpackWarps][2];
     __shared__ uint32_t key_factor[kTile][2];                // scale and low value, each twice, as halves
     __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, low values
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
             int val_exp = 8;
             if (row.active) {
                 const int hi = row.hi, lo = row.lo;
-                const float unit = row.unit;
+                float unit = row.unit;
+                shrunk[r] = 1.0f;
                 const int first = (c.span.first + c.tile) * kTile;
                 for (int i = 0; i < n; ++i, ++steps) {
                     const int token = first + i * kTile;
@@ -696,9 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                         if (__any_sync(0xffffffffu, raise) || info.val_exp != val_exp) {
                             float f = 1.0f;
                             if (raise) {
-                                f = exp2_approx(top - a);
+                                const float shrink = shrink_reference(a);
+                                f = exp2_approx((top - a) * shrink);
                                 top = a;
                                 total *= f;
+                                if (shrink != 1.0f) {
+                                    unit *= shrink;
+                                    top *= shrink;
+                                    shrunk[r] *= shrink;
+                                }
                             }
                             if (i > 0) {
                                 f *= info.val_exp - val_exp > 126 ? 0.0f : pow2(val_exp - info.val_exp);
@@ -714,7 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                             }
                             val_exp = info.val_exp;
                         }
-                        const uint64_t cst2 = pair_f32(cst, cst);
+                        const float cst_now = unit * pow2(info.key_exp - 134);  // (the maximum may just have been shrunk)
+                        const uint64_t cst2 = pair_f32(cst_now, cst_now);
                         const float shift = top == -INFINITY ? 0.0f : kPShift - top;
                         const uint64_t shift2 = pair_f32(shift, shift);
                         auto weights = [&](auto edge_tag) {
@@ -812,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     }
                 }
                 if (row.live && !(begins && ends))
-                    *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, total);
+                    *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top / shrunk[r], total);
             }
             row = next;
         }

@@ -85,3 +85,15 @@ def test_non_finite_rows_reach_only_rows_that_see_them(bits, d, lens, nqs, windo
         if kv == 1:
             assert torch.isnan(y[sees, 4:]).any(-1).all() or value in (float("inf"), float("-inf"))
             assert not torch.isfinite(y[sees, 4:]).all(-1).any()
+
+
+@pytest.mark.parametrize("nq", [1, 4, 60, 200])
+@pytest.mark.parametrize("far", [16, 20, 22, 25, 28, 31, 40])
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+def test_logits_of_any_size(bits, d, far, nq):
+    """Keys 2^far times the queries' size: logits whose fp32 spacing passes the softmax's own units."""
+    p = Problem([700, 130], [nq, 1], 8, 2, d, bits, 16, 60 + far)
+    rescale(p, lambda b, kv, j: np.where(kv == 0, far, 0) + 0 * j)
+    y = p.run()
+    # (a row is pinned where its largest logits lie further apart than they may be off: nearly all)
+    assert check(p, y) > 0.9
