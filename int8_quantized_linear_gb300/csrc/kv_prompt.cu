@@ -21,14 +21,19 @@
 // inlining the waits as much again.
 //
 // K and V become fp16 including scale and low value: fp16_rn(low + s code), one
-// rounding of 2^-11 relative to the element (scale and low value have 8 bits and
-// are exact), so the products need no factors per token.  Q and P as in
-// kv_attention.cu.  Ranges: a row of Q is scaled to 2^8; a tile
-// of K by the power of two that brings its largest element to 2^7, undone in
-// c; V by one such power for all tiles so far, O being rescaled when it
-// grows; P's maximum m is only raised when a row exceeds it by 2^8 (the sums
-// are rescaled then), so P reaches at most 2^15 and keeps weights down to
-// 2^-31 of the largest.
+// rounding of 2^-11 relative to the element (scale and low value have 8 bits), so
+// the products need no factors per token.  Q and P as in kv_attention.cu.  Ranges:
+// a row of Q is scaled to 2^8; a tile of K by the power of two that brings its
+// largest element to 2^7, undone in c; V by one such power for all tiles so far, O
+// being rescaled when it grows.  A token whose largest element is more than 2^12
+// below that is held at an exponent of its own (least_exp), which S and P then make
+// up for (uneven_tile), so that what fp16 keeps of a token's keys does not depend on
+// its neighbours; of its values, with weights that reach 2^-14 at that distance, down
+// to 2^-33 of the largest.  P's maximum m is only raised when a row exceeds it by 2^8
+// (the sums are rescaled then), so P reaches at most 2^15 and keeps weights down to
+// 2^-31 of the largest.  Value rows that are not finite count as 0 and turn the total
+// of the rows that see them into no number (sees_not_finite): a product with the
+// weight 0 would carry them to the other rows.
 //
 // Operand layout: K-major, 128-byte swizzle.  The order of the channels is
 // free as long as Q and K agree, so key words are stored in the order in
@@ -42,8 +47,6 @@
 // 53 %), one prompt of 8192 tokens 586 us (938 TFLOP/s).
 
 #include <cuda_runtime.h>
-
-#include <type_traits>
 
 #include "kv_math.cuh"
 
@@ -196,6 +199,170 @@ struct TileInfo {
     int key_exp;  // K is held times 2^(134 - key_exp)
     int val_exp;  // V is held times 2^(134 - val_exp), from this tile on
 };
+// Added to val_exp where some tokens are so much smaller than others that they are
+// held at exponents of their own (least_exp), keys or values.
+constexpr int kUneven = 1 << 16;
+
+// The least exponent a row (its largest magnitude, as bits) may be held at: 12 above
+// its own, so that its elements stay clear of the subnormal numbers of fp16: they
+// keep 11 bits down to 2^-9 of the largest, and a scale that is subnormal itself
+// loses less than 2^-12 of the largest over all codes.
+__device__ __forceinline__ uint32_t least_exp(uint32_t bits) {
+    return bits - 1 < 0x7f7fffffu ? (bits >> 23) + 12 : 255;
+}
+
+// The maximum of a tile's S over the tokens the row sees.  EDGE: some row does not
+// see some of them.
+template <bool EDGE>
+__device__ __forceinline__ float tile_maximum(uint32_t s_at, int token, int lo, int hi) {
+    uint32_t x[32];
+    float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float y = __uint_as_float(x[j]), z = __uint_as_float(x[j + 1]);
+            if (EDGE) {
+                const int tok = token + q * 32 + j;
+                y = tok <= hi && tok >= lo ? y : -INFINITY;
+                z = tok + 1 <= hi && tok + 1 >= lo ? z : -INFINITY;
+            }
+            high[(j / 2) & 3] = max3(high[(j / 2) & 3], y, z);
+        }
+    }
+    return max3(fmaxf(high[0], high[1]), high[2], high[3]);
+}
+
+// What a row's sums stand at.
+struct RowSums {
+    float unit;   // what a scaled logit counts (times 2^(key_exp - 134)), in log2 units
+    float top;    // the maximum, in the same units
+    float total;
+    int val_exp;  // of O
+};
+
+// The tile's maximum `high` in the row's units, and whether it exceeds what the sums
+// stand at by more than the slack (the first time: from -infinity).
+__device__ __forceinline__ float in_units(const RowSums& row, float high, const TileInfo& info) {
+    return high == -INFINITY ? -INFINITY : high * (row.unit * pow2(info.key_exp - 134));
+}
+__device__ __forceinline__ bool exceeds(const RowSums& row, float a) { return a > row.top + kSlack; }
+
+// Whether some row of the warp does, or the exponent changes.
+__device__ __forceinline__ bool sums_change(const RowSums& row, float high, const TileInfo& info) {
+    return __any_sync(0xffffffffu, exceeds(row, in_units(row, high, info))) || info.val_exp != row.val_exp;
+}
+
+// Raises the maximum where it is exceeded, and brings O and the total to it and to the
+// tile's exponent.
+template <int D>
+__device__ __forceinline__ void change_sums(RowSums& row, float high, const TileInfo& info, uint32_t o_at, bool first,
+                                            float& shrunk) {
+    const float a = in_units(row, high, info);
+    const bool raise = exceeds(row, a);
+    float f = 1.0f;
+    if (raise) {
+        const float shrink = shrink_reference(a);
+        f = exp2_approx((row.top - a) * shrink);
+        row.top = a;
+        row.total *= f;
+        if (shrink != 1.0f) {
+            row.unit *= shrink;
+            row.top *= shrink;
+            shrunk *= shrink;
+        }
+    }
+    if (!first) {
+        f *= info.val_exp - row.val_exp > 126 ? 0.0f : pow2(row.val_exp - info.val_exp);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(o_at + q * 32, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            tmem_st32(o_at + q * 32, v);
+        }
+    }
+    row.val_exp = info.val_exp;
+}
+
+// P over the columns of S; returns the sum of the row's weights.
+template <bool EDGE>
+__device__ __forceinline__ float tile_weights(const RowSums& row, int key_exp, uint32_t s_at, int token, int lo, int hi) {
+    const float cst = row.unit * pow2(key_exp - 134);
+    const uint64_t cst2 = pair_f32(cst, cst);
+    const float shift = row.top == -INFINITY ? 0.0f : kPShift - row.top;
+    const uint64_t shift2 = pair_f32(shift, shift);
+    uint32_t x[32];
+    uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+        uint32_t h[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float y, z;
+            split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), cst2, shift2), y, z);
+            y = exp2_approx(y);
+            z = exp2_approx(z);
+            if (EDGE) {
+                const int tok = token + q * 32 + j;
+                y = tok <= hi && tok >= lo ? y : 0.0f;
+                z = tok + 1 <= hi && tok + 1 >= lo ? z : 0.0f;
+            }
+            sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(y, z));
+            h[j / 2] = pack_f16(y, z);
+        }
+        // (columns of S that have been read: chunk q of P lies in chunk q / 2)
+        tmem_st16(s_at + q * 16, h);
+    }
+    float y, z;
+    split_f32(add_f32x2(sum[0], sum[1]), y, z);
+    return y + z;
+}
+
+// A tile some of whose tokens are held at exponents `down` below the tile's: the same,
+// with S brought to the tile's before, and P (which the sum of the weights does not
+// see) after.  (Rare: a function, so that the loop over the tiles stays small.)
+template <int D>
+__device__ __noinline__ RowSums uneven_tile(RowSums row, TileInfo info, const uint32_t* down, uint32_t s_at,
+                                            uint32_t o_at, bool first, float* shrunk, int token, int lo, int hi) {
+    info.val_exp -= kUneven;
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        uint32_t x[32];
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int by = down[q * 32 + j] & 0xffff;
+            x[j] = by > 126 ? 0u : __float_as_uint(__uint_as_float(x[j]) * pow2(-by));
+        }
+        tmem_st32(s_at + q * 32, x);
+    }
+    tmem_wait_st();
+    const float high = tile_maximum<true>(s_at, token, lo, hi);
+    if (sums_change(row, high, info)) change_sums<D>(row, high, info, o_at, first, *shrunk);
+    row.total += tile_weights<true>(row, info.key_exp, s_at, token, lo, hi);
+    tmem_wait_st();
+#pragma unroll 1
+    for (int q = 0; q < kTile / 64; ++q) {
+        uint32_t x[32];
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int a = down[q * 64 + 2 * j] >> 16, b = down[q * 64 + 2 * j + 1] >> 16;
+            x[j] = fma_f16x2(x[j], pack_f16(a > 24 ? 0.0f : pow2(-a), b > 24 ? 0.0f : pow2(-b)), 0u);
+        }
+        tmem_st32(s_at + q * 32, x);
+    }
+    return row;
+}
 
 // The bits of a row's largest magnitude (a row is low .. low + scale * kTop); not
 // below infinity's when some element is not finite.
@@ -232,8 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
     __shared__ KvCursor cursors[kSoftmaxWarps];  // (kept out of the registers of the softmax)
     __shared__ KvRange range;
     __shared__ TileInfo infos[kInfo];
+    __shared__ uint32_t down[kInfo][kTile];  // how much a token's exponents are below the tile's: keys, and values << 16
     __shared__ float shrunk[kRows];  // by how much a row's unit and maximum have been shrunk
-    __shared__ uint32_t exp_red[2][kUnpackWarps][2];
+    __shared__ __align__(16) uint32_t exp_red[2][kUnpackWarps];  // largest exponents: keys, and values << 16
+    static_assert(kUnpackWarps == 4);
     __shared__ uint32_t key_factor[kTile][2];                // scale and low value, each twice, as halves
     __shared__ __align__(16) uint16_t val_factor[2][kTile];  // scales, low values
     __shared__ uint32_t tmem_base;
@@ -264,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
             tc::mbar_init(&p_full[i], 128);
             tc::mbar_init(&o_full[i], 1);
         }
-        for (int i = 0; i < kInfo; ++i) tc::mbar_init(&info_full[i], 1);
+        for (int i = 0; i < kInfo; ++i) tc::mbar_init(&info_full[i], kUnpackWarps);
         tc::mbar_init(&drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -378,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         const int key_lane = tid % kLanesPerKey;
         const int val_group = tid & 15, val_part = tid >> 4;  // eight tokens, D / 8 channels
         while (const int n = kv_take<kCost>(p, c, found.end)) {
-            int val_exp = 8;
+            uint32_t tile_exp = 8u << 16;  // of the tile's keys, and of the values so far << 16
             for (int i = 0; i < n; ++i, ++kt) {
                 const int token = (c.span.first + c.tile + i) * kTile;
                 const uint32_t slot = kt % kRawKeys, stage = kt % kKStages;
@@ -401,17 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 }
                 const uint32_t top_k = __reduce_max_sync(0xffffffffu, bits_k < 0x7f800000u ? bits_k : 0u);
                 const uint32_t top_v = __reduce_max_sync(0xffffffffu, bits_v);
-                if (lane == 0) {
-                    exp_red[kt & 1][w4][0] = top_k;
-                    exp_red[kt & 1][w4][1] = top_v;
-                }
+                const uint32_t least = least_exp(bits_k) | least_exp(bits_v) << 16;
+                if (lane == 0) exp_red[kt & 1][w4] = top_k >> 23 | top_v >> 23 << 16;
                 unpack_sync();
-                int key_exp = 8;
-                for (int w = 0; w < kUnpackWarps; ++w) {
-                    key_exp = max(key_exp, (int)(exp_red[kt & 1][w][0] >> 23));
-                    val_exp = max(val_exp, (int)(exp_red[kt & 1][w][1] >> 23));
-                }
-                const float fk = pow2(134 - key_exp), fv = pow2(134 - val_exp);
+                const uint4 tops = *reinterpret_cast<const uint4*>(exp_red[kt & 1]);
+                tile_exp = __vmaxu2(__vmaxu2(__vmaxu2(tops.x, tops.y), __vmaxu2(tops.z, tops.w)), (tile_exp & 0xffff0000u) | 8);
+                const uint32_t exps = __vminu2(tile_exp, least), below = tile_exp - exps;
+                const float fk = __uint_as_float((261u << 23) - (exps << 23));  // 2^(134 - exponent)
+                const float fv = __uint_as_float((261u << 23) - (exps >> 16 << 23));
                 const float ks = kv_scale(pk) * fk, kl = kv_low(pk) * fk;
                 const float vs = kv_scale(pv) * fv, vl = kv_low(pv) * fv;
                 key_factor[tid][0] = pack_f16(ks, ks);
@@ -419,12 +585,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 const uint32_t v2 = pack_f16(vs, vl);
                 val_factor[0][tid] = (uint16_t)v2;
                 val_factor[1][tid] = (uint16_t)(v2 >> 16);
+                down[kt % kInfo][tid] = below;
                 if (tid == 0) {
-                    infos[kt % kInfo].key_exp = key_exp;
-                    infos[kt % kInfo].val_exp = val_exp;
-                    tc::mbar_arrive(&info_full[kt % kInfo]);
+                    infos[kt % kInfo].key_exp = tile_exp & 0xffff;
+                    infos[kt % kInfo].val_exp = tile_exp >> 16;
                 }
                 unpack_sync();
+                if (below) atomicOr(&infos[kt % kInfo].val_exp, kUneven);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&info_full[kt % kInfo]);
                 // K: 16 raw bytes of a token at a time
                 wait(&k_empty[stage], ((kt / kKStages) & 1) ^ 1);
                 if (!dead) {
@@ -648,12 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
         if (n > 0) take_up(row);
         while (n > 0) {
             const bool begins = c.tile == 0, ends = c.tile + n == c.span.tiles;
-            float top = -INFINITY;  // the maximum the sums stand at, in log2 units
-            float total = 0.0f;
-            int val_exp = 8;
+            RowSums sums = {row.unit, -INFINITY, 0.0f, 8};
             if (row.active) {
                 const int hi = row.hi, lo = row.lo;
-                float unit = row.unit;
                 shrunk[r] = 1.0f;
                 const int first = (c.span.first + c.tile) * kTile;
                 for (int i = 0; i < n; ++i, ++steps) {
@@ -668,95 +834,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     tc::tc_fence_after();
                     if (!dead) {
                         const TileInfo info = infos[k % kInfo];
-                        const float cst = unit * pow2(info.key_exp - 134);
                         const bool edge = token + kTile - 1 > row.all_hi || token < row.all_lo;
-                        // the tile's maximum
-                        auto maximum = [&](auto edge_tag) {
-                            constexpr bool EDGE = decltype(edge_tag)::value;
-                            uint32_t x[32];
-                            float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                            for (int q = 0; q < kTile / 32; ++q) {
-                                tmem_ld32(s_at + q * 32, x);
-                                tc::tmem_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float y = __uint_as_float(x[j]), z = __uint_as_float(x[j + 1]);
-                                    if (EDGE) {
-                                        const int tok = token + q * 32 + j;
-                                        y = tok <= hi && tok >= lo ? y : -INFINITY;
-                                        z = tok + 1 <= hi && tok + 1 >= lo ? z : -INFINITY;
-                                    }
-                                    high[(j / 2) & 3] = max3(high[(j / 2) & 3], y, z);
-                                }
+                        const float high = edge ? tile_maximum<true>(s_at, token, lo, hi)
+                                                : tile_maximum<false>(s_at, token, lo, hi);
+                        if (sums_change(sums, high, info)) {
+                            if (info.val_exp >= kUneven) {
+                                sums = uneven_tile<D>(sums, info, down[k % kInfo], s_at, o_at, i == 0, &shrunk[r], token, lo,
+                                                      hi);
+                                tmem_wait_st();
+                                tc::tc_fence_before();
+                                tc::mbar_arrive(&p_full[m]);
+                                continue;
                             }
-                            return max3(fmaxf(high[0], high[1]), high[2], high[3]);
-                        };
-                        const float high = edge ? maximum(std::true_type{}) : maximum(std::false_type{});
-                        const float a = high == -INFINITY ? -INFINITY : high * cst;
-                        const bool raise = a > top + kSlack;  // (the first time: from -infinity)
-                        if (__any_sync(0xffffffffu, raise) || info.val_exp != val_exp) {
-                            float f = 1.0f;
-                            if (raise) {
-                                const float shrink = shrink_reference(a);
-                                f = exp2_approx((top - a) * shrink);
-                                top = a;
-                                total *= f;
-                                if (shrink != 1.0f) {
-                                    unit *= shrink;
-                                    top *= shrink;
-                                    shrunk[r] *= shrink;
-                                }
-                            }
-                            if (i > 0) {
-                                f *= info.val_exp - val_exp > 126 ? 0.0f : pow2(val_exp - info.val_exp);
-#pragma unroll 1
-                                for (int q = 0; q < D / 32; ++q) {
-                                    uint32_t v[32];
-                                    tmem_ld32(o_at + q * 32, v);
-                                    tc::tmem_wait_ld();
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                                    tmem_st32(o_at + q * 32, v);
-                                }
-                            }
-                            val_exp = info.val_exp;
+                            change_sums<D>(sums, high, info, o_at, i == 0, shrunk[r]);
                         }
-                        const float cst_now = unit * pow2(info.key_exp - 134);  // (the maximum may just have been shrunk)
-                        const uint64_t cst2 = pair_f32(cst_now, cst_now);
-                        const float shift = top == -INFINITY ? 0.0f : kPShift - top;
-                        const uint64_t shift2 = pair_f32(shift, shift);
-                        auto weights = [&](auto edge_tag) {
-                            constexpr bool EDGE = decltype(edge_tag)::value;
-                            uint32_t x[32];
-                            uint64_t sum[2] = {0, 0};
-#pragma unroll 1
-                            for (int q = 0; q < kTile / 32; ++q) {
-                                tmem_ld32(s_at + q * 32, x);
-                                tc::tmem_wait_ld();
-                                uint32_t h[16];
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float y, z;
-                                    split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), cst2, shift2), y, z);
-                                    y = exp2_approx(y);
-                                    z = exp2_approx(z);
-                                    if (EDGE) {
-                                        const int tok = token + q * 32 + j;
-                                        y = tok <= hi && tok >= lo ? y : 0.0f;
-                                        z = tok + 1 <= hi && tok + 1 >= lo ? z : 0.0f;
-                                    }
-                                    sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(y, z));
-                                    h[j / 2] = pack_f16(y, z);
-                                }
-                                // (columns of S that have been read: chunk q of P lies in chunk q / 2)
-                                tmem_st16(s_at + q * 16, h);
-                            }
-                            float y, z;
-                            split_f32(add_f32x2(sum[0], sum[1]), y, z);
-                            return y + z;
-                        };
-                        total += edge ? weights(std::true_type{}) : weights(std::false_type{});
+                        sums.total += edge ? tile_weights<true>(sums, info.key_exp, s_at, token, lo, hi)
+                                           : tile_weights<false>(sums, info.key_exp, s_at, token, lo, hi);
                         tmem_wait_st();
                     }
                     tc::tc_fence_before();
@@ -765,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 // (set, if at all, before the exponents of the tile that were waited for)
                 if (*reinterpret_cast<volatile int*>(&met_not_finite) && row.live &&
                     sees_not_finite<BITS>(p, c, max(lo, first), min(hi, first + n * kTile - 1)))
-                    total = NAN;
+                    sums.total = NAN;
             }
             if (begins && !ends) {
                 split = true;
@@ -794,8 +887,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 tc::tc_fence_after();
             }
             if (row.active && !dead) {
-                const float back = pow2(val_exp - 134);
-                const float by = begins && ends ? (total == 0.0f ? 0.0f : back / total) : back;
+                const float back = pow2(sums.val_exp - 134);
+                const float by = begins && ends ? (sums.total == 0.0f ? 0.0f : back / sums.total) : back;
                 const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows + r;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
@@ -821,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     }
                 }
                 if (row.live && !(begins && ends))
-                    *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top / shrunk[r], total);
+                    *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(sums.top / shrunk[r], sums.total);
             }
             row = next;
         }
@@ -836,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
 template <int D, int BITS>
 cudaError_t launch_form(const KvAttnParams& p, int64_t ctas, const LaunchEnv& env) {
     using C = Cfg<D, BITS>;
-    static_assert(C::kSmem <= 227 * 1024 - 4096, "shared memory of a block");
+    static_assert(C::kSmem <= 227 * 1024 - 6144, "shared memory of a block");
     const cudaError_t e = allow_smem<kv_prompt_kernel<D, BITS>>(C::kSmem);
     if (e != cudaSuccess) return e;
     return launch_kernel(kv_prompt_kernel<D, BITS>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, env.stream,

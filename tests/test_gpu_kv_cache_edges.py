@@ -97,3 +97,27 @@ def test_logits_of_any_size(bits, d, far, nq):
     y = p.run()
     # (a row is pinned where its largest logits lie further apart than they may be off: nearly all)
     assert check(p, y) > 0.9
+
+
+FAR = [(nq, 0, far) for nq in (3, 150) for far in (12, 16, 20, 24, 30)] + [(3, 1, 8), (3, 1, 12)] + [
+    (150, 1, far) for far in (8, 12, 16, 20, 24, 30)]
+
+
+@pytest.mark.parametrize("nq,kv,far", FAR)
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 128), (4, 64), (8, 64)])
+def test_a_token_far_larger_than_its_neighbours(bits, d, nq, kv, far):
+    """A key (or value) 2^far times the rest of its tile, hidden from most rows or outweighed by its strongly negative
+    logit: the small tokens decide those outputs.  (Few rows hold value scales in fp16 relative to the largest: less
+    far.)"""
+    p = Problem([700], [nq], 8, 2, d, bits, 16, far + bits)
+    big = [600, 640, 698]
+    if kv == 0:  # key channels of the big tokens all of one sign, against the queries' sign: far below every other logit
+        p.q = p.q.abs()
+        c, s, low = p.seqs[0]
+        for t in big:
+            low[0, t] = -np.abs(low[0, t]) - s[0, t] * 2 ** bits
+            page, off = int(p.table[0, t // 16]), t % 16
+            p.params[page, 0, :, off, 1] = torch.from_numpy(low[0, t]).to(torch.bfloat16).cuda()
+            low[0, t] = p.params[page, 0, :, off, 1].float().cpu().numpy()
+    rescale(p, lambda b, x, j: np.where(np.isin(j, big) & (x == kv), far, 0))
+    assert check(p, p.run()) > 0.9
