@@ -116,6 +116,19 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _empty(shape: tuple, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """torch.empty with the call's stream current, so that the allocator knows
+    which stream uses the memory (and does not hand out a block that the
+    current stream has freed but may still be reading)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (0 is the default stream's handle; ExternalStream makes a new stream of it)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -642,13 +655,8 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
         size = 0
         if t and b:
             size = _workspace_size(torch.cuda.current_device(), b, t, hq, heads, d, bits, page, width, max_q)
-        if size and stream is not None:
-            # allocated with the call's stream current, so that the allocator knows which stream uses it
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                   else torch.cuda.ExternalStream(int(stream))):
-                workspace = torch.empty((size,), dtype=torch.uint8, device=codes.device)
-        elif size:
-            workspace = torch.empty((size,), dtype=torch.uint8, device=codes.device)
+        if size:
+            workspace = _empty((size,), torch.uint8, codes.device, stream)
     else:
         _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
         size = workspace.numel()
