@@ -6,6 +6,10 @@ pass (torch is only the device-memory and stream provider), and calls the C
 ABI with raw device pointers and the current CUDA stream.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback.  If the
 library is missing, loading fails with an error that says how to build it.
+
+Calls run on torch's current stream, or on `stream` (a torch stream or a raw
+handle); what a call allocates itself belongs to that stream, as if the stream
+had been current.
 """
 
 from __future__ import annotations
@@ -154,9 +158,9 @@ def _quant(fn_name: str, src: torch.Tensor, q, scale, stream):
     rows, k = src.shape
     _need(src, torch.bfloat16, (rows, k), "input")
     if q is None:
-        q = torch.empty((rows, k), dtype=torch.int8, device=src.device)
+        q = _empty((rows, k), torch.int8, src.device, stream)
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=src.device)
+        scale = _empty((rows,), torch.float32, src.device, stream)
     _need(q, torch.int8, (rows, k), "q")
     _need(scale, torch.float32, (rows,), "scale")
     st = getattr(lib(), fn_name)(_ptr(src), rows, k, _ptr(q), _ptr(scale), _stream(stream))
@@ -187,7 +191,7 @@ def w8a8_linear(x, qw, sw, bias=None, y=None, qx=None, sx=None, acc_debug=None, 
     if bias is not None:
         _need(bias, torch.bfloat16, (n,), "bias")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((m, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     if qx is not None:
         _need(qx, torch.int8, (m, k), "qx")
@@ -213,7 +217,7 @@ def w8a8_gemm(qx, sx, qw, sw, bias=None, y=None, acc_debug=None, stream=None):
     if bias is not None:
         _need(bias, torch.bfloat16, (n,), "bias")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((m, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     if acc_debug is not None:
         _need(acc_debug, torch.int32, (m, n), "acc_debug")
@@ -257,7 +261,7 @@ def w8a16_gemm(x, qw, sw, y=None, stream=None):
     _need(qw, torch.int8, (n, k), "qw")
     _need(sw, torch.float32, (n,), "sw")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((m, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     st = lib().w8a16_gemm(_ptr(x), _ptr(qw), _ptr(sw), _ptr(y), m, n, k, _stream(stream))
     _check(st, "w8a16_gemm")
@@ -275,7 +279,7 @@ def grouped_w8a16_gemm(x, offsets, qw, sw, y=None, stream=None):
     _need(qw, torch.int8, (e, n, k), "qw")
     _need(sw, torch.float32, (e, n), "sw")
     if y is None:
-        y = torch.empty((t, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((t, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (t, n), "y")
     st = lib().grouped_w8a16_gemm(_ptr(x), _ptr(offsets), e, _ptr(qw), _ptr(sw), _ptr(y), t, n, k,
                                   _stream(stream))
@@ -351,9 +355,9 @@ def _quant_fp8(fn_name: str, src: torch.Tensor, q, scale, stream):
     rows, k = src.shape
     _need(src, torch.bfloat16, (rows, k), "input")
     if q is None:
-        q = torch.empty((rows, k), dtype=torch.uint8, device=src.device)
+        q = _empty((rows, k), torch.uint8, src.device, stream)
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=src.device)
+        scale = _empty((rows,), torch.float32, src.device, stream)
     _need(q, torch.uint8, (rows, k), "q")
     _need(scale, torch.float32, (rows,), "scale")
     _check(getattr(lib(), fn_name)(_ptr(src), rows, k, _ptr(q), _ptr(scale), _stream(stream)), fn_name)
@@ -381,7 +385,7 @@ def w8a8_fp8_gemm(qx, sx, qw, sw, bias=None, y=None, stream=None):
     if bias is not None:
         _need(bias, torch.bfloat16, (n,), "bias")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((m, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     _check(lib().w8a8_fp8_gemm(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(bias), _ptr(y), m, n, k,
                                _stream(stream)), "w8a8_fp8_gemm")
@@ -398,7 +402,7 @@ def w8a8_fp8_linear(x, qw, sw, bias=None, y=None, qx=None, sx=None, stream=None)
     if bias is not None:
         _need(bias, torch.bfloat16, (n,), "bias")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=qw.device)
+        y = _empty((m, n), torch.bfloat16, qw.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     if qx is not None:
         _need(qx, torch.uint8, (m, k), "qx")
@@ -416,9 +420,9 @@ def quantize_weight_w4_g128(w: torch.Tensor, q=None, scale=None, stream=None):
     n, k = w.shape
     _need(w, torch.bfloat16, (n, k), "w")
     if q is None:
-        q = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+        q = _empty((n, k // 2), torch.uint8, w.device, stream)
     if scale is None:
-        scale = torch.empty((n, k // 128), dtype=torch.bfloat16, device=w.device)
+        scale = _empty((n, k // 128), torch.bfloat16, w.device, stream)
     _need(q, torch.uint8, (n, k // 2), "q")
     _need(scale, torch.bfloat16, (n, k // 128), "scale")
     _check(lib().quantize_weight_w4_g128(_ptr(w), n, k, _ptr(q), _ptr(scale), _stream(stream)),
@@ -434,7 +438,7 @@ def w4a16_gemm(x, q, scale, y=None, stream=None):
     _need(q, torch.uint8, (n, k // 2), "q")
     _need(scale, torch.bfloat16, (n, k // 128), "scale")
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16, device=q.device)
+        y = _empty((m, n), torch.bfloat16, q.device, stream)
     _need(y, torch.bfloat16, (m, n), "y")
     _check(lib().w4a16_gemm(_ptr(x), _ptr(q), _ptr(scale), _ptr(y), m, n, k, _stream(stream)), "w4a16_gemm")
     return y
@@ -449,10 +453,10 @@ def moe_route_topk(logits, top_k, n_shared, stream=None):
     _need(logits, torch.float32, (t, e), "logits")
     s = top_k + n_shared
     dev = logits.device
-    offsets = torch.empty((e + n_shared + 1,), dtype=torch.int32, device=dev)
-    row_token = torch.empty((t * s,), dtype=torch.int32, device=dev)
-    token_row = torch.empty((t, s), dtype=torch.int32, device=dev)
-    slot_weight = torch.empty((t, s), dtype=torch.float32, device=dev)
+    offsets = _empty((e + n_shared + 1,), torch.int32, dev, stream)
+    row_token = _empty((t * s,), torch.int32, dev, stream)
+    token_row = _empty((t, s), torch.int32, dev, stream)
+    slot_weight = _empty((t, s), torch.float32, dev, stream)
     _check(lib().moe_route_topk(_ptr(logits), t, e, top_k, n_shared, _ptr(offsets), _ptr(row_token),
                                 _ptr(token_row), _ptr(slot_weight), _stream(stream)), "moe_route_topk")
     return offsets, row_token, token_row, slot_weight
@@ -471,7 +475,7 @@ def grouped_w8a16_silu_mul(x, row_token, offsets, qw, sw, h=None, rows=None, str
         _need(row_token, torch.int32, (rows,), "row_token")
     _need(sw, torch.float32, (e, two_i), "sw")
     if h is None:
-        h = torch.empty((rows, inter), dtype=torch.bfloat16, device=qw.device)
+        h = _empty((rows, inter), torch.bfloat16, qw.device, stream)
     _need(h, torch.bfloat16, (rows, inter), "h")
     _check(lib().grouped_w8a16_silu_mul(_ptr(x), _ptr(row_token), _ptr(offsets), e, _ptr(qw), _ptr(sw), _ptr(h),
                                         rows, inter, k, _stream(stream)), "grouped_w8a16_silu_mul")
@@ -486,7 +490,7 @@ def moe_combine(yd, token_row, slot_weight, out=None, stream=None):
     _need(slot_weight, torch.float32, (t, s), "slot_weight")
     _need(yd, torch.bfloat16, (yd.shape[0], h), "yd")
     if out is None:
-        out = torch.empty((t, h), dtype=torch.bfloat16, device=yd.device)
+        out = _empty((t, h), torch.bfloat16, yd.device, stream)
     _need(out, torch.bfloat16, (t, h), "out")
     _check(lib().moe_combine(_ptr(yd), _ptr(token_row), _ptr(slot_weight), _ptr(out), t, s, h, _stream(stream)),
            "moe_combine")
@@ -510,7 +514,7 @@ def moe_expert_mlp_w8a16(x, logits, top_k, n_shared, qw_gate_up, sw_gate_up, qw_
     _need(qw_down, torch.int8, (e, hid, inter), "qw_down")
     _need(sw_down, torch.float32, (e, hid), "sw_down")
     if out is None:
-        out = torch.empty((t, hid), dtype=torch.bfloat16, device=x.device)
+        out = _empty((t, hid), torch.bfloat16, x.device, stream)
     _need(out, torch.bfloat16, (t, hid), "out")
     _check(lib().moe_expert_mlp_w8a16(_ptr(x), _ptr(logits), e_r, top_k, n_shared, _ptr(qw_gate_up),
                                       _ptr(sw_gate_up), _ptr(qw_down), _ptr(sw_down), _ptr(out), t, hid, inter,
@@ -592,11 +596,11 @@ def kv_cache_load(codes, params, slots, head_dim, k=None, v=None, stream=None):
     _need(slots, torch.int64, (t,), "slots")
     shape = (t, heads, head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+        k = _empty(shape, torch.bfloat16, codes.device, stream)
     else:
         _need(k, torch.bfloat16, shape, "k")
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+        v = _empty(shape, torch.bfloat16, codes.device, stream)
     else:
         _need(v, torch.bfloat16, shape, "v")
     st = lib().kv_cache_load(codes.data_ptr(), params.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), t,
@@ -648,7 +652,7 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
     if max_q is None:
         max_q = 1 if q_offsets is None else max(t, 1)
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=codes.device)
+        out = _empty((t, hq, d), torch.bfloat16, codes.device, stream)
     else:
         _need(out, torch.bfloat16, (t, hq, d), "out")
     if workspace is None:
