@@ -137,8 +137,10 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _need(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> None:
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _need(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: int | None = None) -> None:
+    """Checks a dense CUDA tensor; with `device`, that it is on that one (its index)."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and (
+            t.is_cuda if device is None else t.get_device() == device) and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -148,6 +150,8 @@ def _need(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.numel() and not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.numel() and device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the cache's device (cuda:{device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -535,21 +539,26 @@ def kv_cache_alloc(num_pages, heads, page_size, head_dim, bits=4, device="cuda")
     return codes, params
 
 
-def _kv_cache(codes: torch.Tensor, params: torch.Tensor, head_dim: int) -> tuple[int, int, int, int]:
-    """(num_pages, heads, page_size, bits) of a cache for rows of head_dim channels."""
+def _kv_cache(codes: torch.Tensor, params: torch.Tensor, head_dim: int) -> tuple[int, int, int, int, int | None]:
+    """(num_pages, heads, page_size, bits, device index) of a cache for rows of
+    head_dim channels, which has to be on the current device."""
     shape = codes.shape
     if len(shape) != 5 or shape[1] != 2:
         raise ValueError("codes must be [num_pages, 2, heads, page_size, head_dim * bits / 8]")
     pages, _, heads, page, row = shape
     bits = 4 if 2 * row == head_dim else 8
     _need(codes, torch.uint8, (pages, 2, heads, page, head_dim * bits // 8), "codes")
-    _need(params, torch.bfloat16, (pages, 2, heads, page, 2), "params")
-    return pages, heads, page, bits
+    device = codes.get_device() if codes.is_cuda else None
+    if device is not None and device != torch._C._cuda_getDevice():
+        raise ValueError(f"codes is on {codes.device}, not on the current device (cuda:{torch.cuda.current_device()})")
+    _need(params, torch.bfloat16, (pages, 2, heads, page, 2), "params", device)
+    return pages, heads, page, bits, device
 
 
-def _need_heads(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
+def _need_heads(t: torch.Tensor, heads: int, head_dim: int, name: str, device: int | None) -> int:
     """Checks bf16 [T, heads, head_dim] whose tokens are dense (tokens may lie
-    apart: a slice of a fused projection's rows); returns their distance."""
+    apart: a slice of a fused projection's rows), on the cache's device;
+    returns their distance."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != torch.bfloat16:
@@ -558,8 +567,10 @@ def _need_heads(t: torch.Tensor, heads: int, head_dim: int, name: str) -> int:
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError(f"{name} must have shape [T, {heads}, {head_dim}], got {tuple(shape)}")
     tokens = shape[0]
-    if not t.is_cuda and t.numel():
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device and t.numel():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, not on the cache's device (cuda:{device})")
     if tokens <= 1 and t.is_contiguous():
         return heads * head_dim
     step, head_step, one = t.stride()
@@ -575,12 +586,12 @@ def kv_cache_store(k, v, slots, codes, params, stream=None):
     if k.dim() != 3:
         raise ValueError("k must be [T, heads, head_dim]")
     t, h, d = k.shape
-    pages, heads, page, bits = _kv_cache(codes, params, d)
-    k_step = _need_heads(k, heads, d, "k")
-    v_step = _need_heads(v, heads, d, "v")
+    pages, heads, page, bits, device = _kv_cache(codes, params, d)
+    k_step = _need_heads(k, heads, d, "k", device)
+    v_step = _need_heads(v, heads, d, "v", device)
     if v.shape[0] != t:
         raise ValueError("k and v disagree on T")
-    _need(slots, torch.int64, (t,), "slots")
+    _need(slots, torch.int64, (t,), "slots", device)
     st = lib().kv_cache_store(k.data_ptr(), v.data_ptr(), k_step, v_step, slots.data_ptr(), codes.data_ptr(),
                               params.data_ptr(), t, h, d, bits, page, pages, _stream(stream))
     if st != I8QL_OK:
@@ -591,18 +602,18 @@ def kv_cache_store(k, v, slots, codes, params, stream=None):
 def kv_cache_load(codes, params, slots, head_dim, k=None, v=None, stream=None):
     """(k, v) bf16 [T, heads, head_dim]: the cache rows at slots, bf16(low +
     scale * code); zeros where the slot is negative."""
-    pages, heads, page, bits = _kv_cache(codes, params, head_dim)
+    pages, heads, page, bits, device = _kv_cache(codes, params, head_dim)
     t = slots.shape[0]
-    _need(slots, torch.int64, (t,), "slots")
+    _need(slots, torch.int64, (t,), "slots", device)
     shape = (t, heads, head_dim)
     if k is None:
         k = _empty(shape, torch.bfloat16, codes.device, stream)
     else:
-        _need(k, torch.bfloat16, shape, "k")
+        _need(k, torch.bfloat16, shape, "k", device)
     if v is None:
         v = _empty(shape, torch.bfloat16, codes.device, stream)
     else:
-        _need(v, torch.bfloat16, shape, "v")
+        _need(v, torch.bfloat16, shape, "v", device)
     st = lib().kv_cache_load(codes.data_ptr(), params.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), t,
                              heads, head_dim, bits, page, pages, _stream(stream))
     if st != I8QL_OK:
@@ -640,21 +651,21 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, head_dim]")
     t, hq, d = q.shape
-    pages, heads, page, bits = _kv_cache(codes, params, d)
-    q_step = _need_heads(q, hq, d, "q")
+    pages, heads, page, bits, device = _kv_cache(codes, params, d)
+    q_step = _need_heads(q, hq, d, "q", device)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, width]")
     b, width = page_table.shape
-    _need(page_table, torch.int32, (b, width), "page_table")
-    _need(kv_lens, torch.int32, (b,), "kv_lens")
+    _need(page_table, torch.int32, (b, width), "page_table", device)
+    _need(kv_lens, torch.int32, (b,), "kv_lens", device)
     if q_offsets is not None:
-        _need(q_offsets, torch.int32, (b + 1,), "q_offsets")
+        _need(q_offsets, torch.int32, (b + 1,), "q_offsets", device)
     if max_q is None:
         max_q = 1 if q_offsets is None else max(t, 1)
     if out is None:
         out = _empty((t, hq, d), torch.bfloat16, codes.device, stream)
     else:
-        _need(out, torch.bfloat16, (t, hq, d), "out")
+        _need(out, torch.bfloat16, (t, hq, d), "out", device)
     if workspace is None:
         size = 0
         if t and b:
@@ -662,7 +673,7 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
         if size:
             workspace = _empty((size,), torch.uint8, codes.device, stream)
     else:
-        _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
+        _need(workspace, torch.uint8, (workspace.numel(),), "workspace", device)
         size = workspace.numel()
     st = lib().kv_cache_attention(q.data_ptr(), q_step, codes.data_ptr(), params.data_ptr(), page_table.data_ptr(), width,
                                   kv_lens.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),

@@ -121,3 +121,46 @@ def test_a_token_far_larger_than_its_neighbours(bits, d, nq, kv, far):
             low[0, t] = p.params[page, 0, :, off, 1].float().cpu().numpy()
     rescale(p, lambda b, x, j: np.where(np.isin(j, big) & (x == kv), far, 0))
     assert check(p, p.run()) > 0.9
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another device (its memory is never touched there)."""
+
+    def get_device(self):
+        return 1
+
+    @property
+    def device(self):
+        return torch.device("cuda:1")
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Pointers of one device handed to a kernel on another would fault where the two do not share memory."""
+    p = Problem([50, 20], [2, 1], 4, 2, 64, 4, 16, 3)
+    k, slots, q = torch.zeros((5, 2, 64), dtype=torch.bfloat16, device="cuda"), torch.arange(5, device="cuda"), p.q.cuda()
+    calls = {
+        "store": (lambda **a: capi.kv_cache_store(a["k"], a["v"], a["slots"], a["codes"], a["params"]),
+                  dict(k=k, v=k.clone(), slots=slots, codes=p.codes, params=p.params)),
+        "load": (lambda **a: capi.kv_cache_load(a["codes"], a["params"], a["slots"], 64, k=a["k"], v=a["v"]),
+                 dict(k=k.clone(), v=k.clone(), slots=slots, codes=p.codes, params=p.params)),
+        "attention": (lambda **a: capi.kv_cache_attention(a["q"], a["codes"], a["params"], a["page_table"], a["kv_lens"],
+                                                          q_offsets=a["q_offsets"], out=a["out"], workspace=a["workspace"]),
+                      dict(q=q, codes=p.codes, params=p.params, page_table=p.table, kv_lens=p.kv_lens, q_offsets=p.offsets,
+                           out=torch.zeros_like(q), workspace=torch.zeros(1 << 20, dtype=torch.uint8, device="cuda"))),
+    }
+
+    class Fake:  # of the library: nothing may reach it
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+
+    for call, args in calls.values():
+        call(**args)
+        torch.cuda.synchronize()
+        with monkeypatch.context() as m:
+            m.setattr(capi, "lib", Fake)
+            for name in args:
+                with pytest.raises(ValueError, match=f"{name} .*device"):
+                    call(**{**args, name: args[name].as_subclass(Elsewhere)})
+            m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+            with pytest.raises(ValueError, match="codes .*device"):
+                call(**args)
