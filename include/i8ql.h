@@ -434,8 +434,10 @@ i8ql_status moe_expert_mlp_w8a16(const i8ql_bf16* x, const float* logits, int64_
  *   scale = the smallest bf16 >= r, low = lo (a bf16 value),
  *   code[d] = rint(fl32(fl32(x[d] - lo) / scale)) (IEEE fp32 divisions, ties
  *   to even), or 0 when scale = 0.
- * Rounding the scale up keeps every code inside 0 .. L: the value read back
- * is within scale / 2 of x[d], and the row's lowest value exact.
+ * Rounding the scale up keeps every code inside 0 .. L: low + scale * code is
+ * within scale / 2 of x[d] (and 2^-14 of the scale, for the fp32 roundings),
+ * the value read back, which is that rounded to bf16, within twice as much,
+ * and the row's lowest value exact.
  *
  * k and v: bf16 [T, H, D], the H * D values of a token contiguous, tokens
  * k_stride and v_stride elements apart (>= H * D, multiples of 8; so slices
@@ -452,8 +454,9 @@ i8ql_status kv_cache_store(const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_str
 
 /*
  * Reads keys and values back: k and v bf16 [T, H, D] (dense) receive
- * bf16_rne(low + scale * code) of the rows at slots[t], zeros where the slot
- * is negative (or, recording I8QL_ERR_BAD_INDEX, past the cache).
+ * low + scale * code (rounded to fp32, then to bf16, both to nearest, ties to
+ * even) of the rows at slots[t], zeros where the slot is negative (or,
+ * recording I8QL_ERR_BAD_INDEX, past the cache).
  *
  * No counterpart on the pages.  Arguments as kv_cache_store.
  */

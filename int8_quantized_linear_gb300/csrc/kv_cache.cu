@@ -4,12 +4,13 @@
 //     lo = min x, hi = max x, r = fl32(fl32(hi - lo) / L), L = 2^bits - 1,
 //     s = the smallest bf16 >= r,
 //     c[d] = rint(fl32(fl32(x[d] - lo) / s))  (ties to even; 0 when s = 0)
-//   load: x[d] = bf16_rne(lo + s * c[d])  (s * c is exact in fp32)
+//   load: x[d] = bf16_rne(fl32(lo + s * c[d]))  (s * c is exact in fp32)
 //
 // lo is an input value, so it is exact in bf16.  The scale is held in 16 bits
 // to keep a 4-bit row of 128 channels at 68 bytes; it is rounded up, not to
 // nearest, so that the largest value stays inside the code range
-// (hi - lo <= L s) and every value within half a step of its code.
+// (hi - lo <= L s) and every value within half a step of lo + s c.  Rounding that to
+// bf16 at most doubles it: x is a bf16 value too, no nearer than the nearest.
 //
 // Both are bound by bytes: a token of 8 heads x 128 channels is 4 KB of bf16
 // and 1 KB of 4-bit rows.  A thread takes 16 channels of several rows, D / 16
