@@ -452,7 +452,8 @@ KvCache make_kv_cache(const uint8_t* codes, const i8ql_bf16* params, int64_t H, 
 
 i8ql_status check_kv_attention(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t page_size, int64_t table_width,
                                int64_t max_q) {
-    if (B < 0 || T_q < 0 || Hq <= 0 || Hq % H != 0 || table_width <= 0 || max_q <= 0) return I8QL_ERR_INVALID_ARG;
+    if (B < 0 || T_q < 0 || Hq <= 0 || Hq % H != 0 || table_width <= 0 || max_q < 0 || (max_q == 0 && T_q > 0))
+        return I8QL_ERR_INVALID_ARG;
     if (B >= kMaxRows || Hq > 65535 || T_q >= ((int64_t)1 << 30) || T_q * (Hq / H) >= ((int64_t)1 << 30) ||
         table_width > (kMaxRows - 65536) / page_size)
         return I8QL_ERR_UNSUPPORTED;

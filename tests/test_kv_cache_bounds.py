@@ -1,5 +1,6 @@
-"""How far a value read back from the quantized cache lies from the value
-written, on the CPU from the oracle (the kernels are equal to it bit for bit).
+"""Host checks of the quantized cache at its edges: how far a value read back
+lies from the value written, from the oracle (the kernels are equal to it bit
+for bit), and sizes of nothing.
 
 low + scale * code is within half a scale of x, up to the fp32 roundings of
 x - low and of the quotient.  The value read back is that rounded to bf16, and
@@ -8,10 +9,14 @@ code than x is: at most the same again, a whole scale."""
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
+from int8_quantized_linear_gb300 import build as lib_build
+from int8_quantized_linear_gb300 import capi
 from oracle import kv_cache as oracle
 
 
@@ -36,3 +41,19 @@ def test_values_are_within_half_a_scale_and_read_back_within_one(bits, kind):
     assert np.array_equal(back.min(-1), x.min(-1))
     if bits == 8 and kind == "normal":  # half a scale would not hold
         assert (np.abs(back - x) > half).any()
+
+
+def test_a_batch_without_query_tokens():
+    """An upper bound of 0 query tokens is one, where there are none."""
+    lib_build.build()
+    #     q q_stride codes params table width lens offsets out B T Hq H D bits page pages max_q window scale ws bytes stream
+    args = [0x10000, 4096, 0x20000, 0x30000, 0x40000, 16, 0x50000, 0x60000, 0x70000, 4, 0, 32, 8, 128, 4, 64, 100, 0, 0, 0.1,
+            None, 0, None]
+    assert capi.lib().kv_cache_attention(*args) == capi.I8QL_OK
+    n = ctypes.c_int64(-1)
+    assert capi.lib().i8ql_kv_attention_workspace(4, 0, 32, 8, 128, 4, 64, 16, 0, ctypes.byref(n)) == capi.I8QL_OK
+    assert n.value == 0
+    args[10] = 3
+    assert capi.lib().kv_cache_attention(*args) == capi.I8QL_ERR_INVALID_ARG
+    args[17] = -1
+    assert capi.lib().kv_cache_attention(*args) == capi.I8QL_ERR_INVALID_ARG
