@@ -26,7 +26,7 @@
 // a row of Q is scaled to 2^8; a tile of K by the power of two that brings its
 // largest element to 2^7, undone in c; V by one such power for all tiles so far, O
 // being rescaled when it grows.  A token whose largest element is more than 2^12
-// below that is held at an exponent of its own (least_exp), which S and P then make
+// below that is held at an exponent of its own (least_exps), which S and P then make
 // up for (uneven_tile), so that what fp16 keeps of a token's keys does not depend on
 // its neighbours; of its values, with weights that reach 2^-14 at that distance, down
 // to 2^-33 of the largest.  P's maximum m is only raised when a row exceeds it by 2^8
@@ -200,15 +200,17 @@ struct TileInfo {
     int val_exp;  // V is held times 2^(134 - val_exp), from this tile on
 };
 // Added to val_exp where some tokens are so much smaller than others that they are
-// held at exponents of their own (least_exp), keys or values.
+// held at exponents of their own (least_exps), keys or values.
 constexpr int kUneven = 1 << 16;
 
-// The least exponent a row (its largest magnitude, as bits) may be held at: 12 above
-// its own, so that its elements stay clear of the subnormal numbers of fp16: they
-// keep 11 bits down to 2^-9 of the largest, and a scale that is subnormal itself
-// loses less than 2^-12 of the largest over all codes.
-__device__ __forceinline__ uint32_t least_exp(uint32_t bits) {
-    return bits - 1 < 0x7f7fffffu ? (bits >> 23) + 12 : 255;
+// The least exponents a token's key and value row (their largest magnitudes, as
+// bits) may be held at, the value's << 16: 12 above their own, so that elements stay
+// clear of the subnormal numbers of fp16: they keep 11 bits down to 2^-9 of the
+// largest, and a scale that is subnormal itself loses less than 2^-12 of the largest
+// over all codes.  (Rows of zeros, and keys that are not finite, come out above any
+// tile's exponent.)
+__device__ __forceinline__ uint32_t least_exps(uint32_t bits_k, uint32_t bits_v) {
+    return ((bits_k - 1) >> 23 | ((bits_v - 1) >> 23 << 16)) + (12u | 12u << 16);
 }
 
 // The maximum of a tile's S over the tokens the row sees.  EDGE: some row does not
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                 }
                 const uint32_t top_k = __reduce_max_sync(0xffffffffu, bits_k < 0x7f800000u ? bits_k : 0u);
                 const uint32_t top_v = __reduce_max_sync(0xffffffffu, bits_v);
-                const uint32_t least = least_exp(bits_k) | least_exp(bits_v) << 16;
+                const uint32_t least = least_exps(bits_k, bits_v);
                 if (lane == 0) exp_red[kt & 1][w4] = top_k >> 23 | top_v >> 23 << 16;
                 unpack_sync();
                 const uint4 tops = *reinterpret_cast<const uint4*>(exp_red[kt & 1]);
@@ -828,11 +830,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttnPara
                     // S first: an M tile that sat out an item may be two rounds of
                     // info_full behind, whose parity then passes at once; after this
                     // tile's S its exponents are there (they were written before K),
-                    // and no later ones can be (those wait for this tile's P)
+                    // and no later ones can be (those wait for this tile's P), so one
+                    // test of the barrier passes, and acquires them
                     wait(&s_full[m], steps & 1);
-                    wait(&info_full[k % kInfo], (k / kInfo) & 1);
+                    const bool there = tc::mbar_test(tc::smem_u32(&info_full[k % kInfo]), (k / kInfo) & 1);
                     tc::tc_fence_after();
-                    if (!dead) {
+                    if (!dead && __all_sync(0xffffffffu, there)) {
                         const TileInfo info = infos[k % kInfo];
                         const bool edge = token + kTile - 1 > row.all_hi || token < row.all_lo;
                         const float high = edge ? tile_maximum<true>(s_at, token, lo, hi)
