@@ -476,28 +476,39 @@ i8ql_status kv_cache_load(const uint8_t* codes, const i8ql_bf16* params, const i
  * cache head, query head h attends over cache head h / G:
  *   a_j = softmax_scale * sum_d q[d] k_j[d];  out[d] = bf16(sum_j e^a_j v_j[d] / sum_j e^a_j)
  * with k and v = low + scale * code.  A row that sees no token (p < 0: more
- * queries than tokens) is 0.  fp32 logits, sums and softmax; the softmax
- * weights (times the value scale) are rounded to 11 bits for the tensor
- * cores, and weights under about 2^-31 of a row's largest may count as 0.
- * With max_q * G <= 32 the products run on the codes (exact); with more,
- * keys and values are rounded to 11 bits first.
+ * queries than tokens) is 0.  A key or value row that is not finite gives
+ * unspecified rows where it is seen, and changes no others.
+ *
+ * Precision: fp32 logits, sums and softmax; the softmax weights (times the
+ * value scale) are rounded to 11 bits for the tensor cores.
+ *  - max_q * G <= 32: the products run on the codes (exact).  Weights under
+ *    2^-31 of a row's largest may count as 0; where a value row's scale is
+ *    2^-k of the largest that the rows computed together have met, weights
+ *    keep 11 bits down to 2^(k - 24).  Keys stay below 2^110.
+ *  - more: keys and values are rounded to 11 bits first (elements under 2^-9
+ *    of their row's largest to a fixed step).  Weights as above, but with 11
+ *    bits down to 2^-21, or to 2^(k - 21) where a value row's largest element
+ *    is 2^-(12 + k) of the largest so far.
  *
  * Inputs: q bf16, token t's Hq * D values contiguous at t * q_stride (>= Hq *
  * D, a multiple of 8), 16-byte aligned; page_table int32 [B, table_width]
  * (entries that no visible token needs are not read as pages: any value);
  * kv_lens int32 [B]; q_offsets int32 [B+1] from 0 to T_q, non-decreasing, or
  * NULL for one query token per sequence (T_q = B).  max_q: an upper bound of
- * the query tokens of one sequence; it only chooses the kernel.  Output: out
- * bf16 [T_q, Hq, D] (dense).  What the cache holds behind a sequence's end
- * is never used.  Lengths, offsets or pages out of range record
- * I8QL_ERR_BAD_INDEX and leave unspecified rows.
+ * the query tokens of one sequence; it only chooses the kernel (with the
+ * precision above).  table_width only chooses the form: a few sequences whose
+ * table is up to 16384 tokens wide run in one launch without a workspace, so a
+ * table no wider than the contexts need is quicker.  Output: out bf16 [T_q,
+ * Hq, D] (dense).  What the cache holds behind a sequence's end is never
+ * used.  Lengths, offsets or pages out of range record I8QL_ERR_BAD_INDEX and
+ * leave unspecified rows (page 0 is read in place of a page out of range).
  *
  * workspace: I8QL_ERR_WORKSPACE_LIMIT when smaller than
  * i8ql_kv_attention_workspace reports for these sizes; 16-byte aligned; it
  * need not be cleared, and belongs to the call until its work is done.
- * Limits: B, num_pages < 2^31, T_q * G < 2^30, table_width * page_size <=
- * 2^31 - 65536.  The result does not depend on timing: the same inputs give
- * the same bits on the same device.
+ * Limits: B, num_pages < 2^31, H, Hq <= 65535, T_q * G < 2^30, table_width *
+ * page_size <= 2^31 - 65536.  The result does not depend on timing: the same
+ * inputs give the same bits on the same device.
  */
 i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8_t* codes, const i8ql_bf16* params,
                                const int32_t* page_table, int64_t table_width, const int32_t* kv_lens,

@@ -18,7 +18,10 @@
 // warp, raised as larger value scales appear, has put s_j / S below 1: eight
 // times finer than bf16.  The weights are relative to a reference that a row's
 // logits exceed by 2^5 at most (w_j s_j / S is held times 2^10, so it ends at
-// 2^15); weights down to 2^-34 of the reference are kept.
+// 2^15); weights down to 2^-34 of the reference are kept, and to 2^-24 at 11
+// bits, either times S / s_j less: S also counts the scales of tokens that only
+// other rows of the block see.  References are held below 2^23 (shrink_reference).
+// Keys of 2^110 and more can take the sums of the products past fp32.
 //
 // Bound by the bytes of the cache: 136 bytes a token and head (4 bits, 128
 // channels, K and V).  Against them stands the unpacking, which is bound by
@@ -44,12 +47,12 @@
 // in flight (61 KB a block at 4 bits and 128 channels, three blocks an SM).
 //
 // Measured, 32 query heads over 8 x 128, one token a sequence: 128 sequences of
-// 16384 tokens in 437 us at 4 bits (5.2 TB/s, 77 % of a copy; warps wait on
+// 16384 tokens in 440 us at 4 bits (5.2 TB/s, 77 % of a copy; warps wait on
 // the chain unpack, product, softmax and for each other's issue slots), 64 of
-// 4096 in 51 us with the join; at 8 bits, which unpack with fewer instructions
-// a byte, 64 of 16384 in 340 us (6.5 TB/s, 96 %).  Pages of 16 tokens: 3.8 TB/s
-// (32 copies a tile and more).  With keys and values as the 8-column operand, half
-// of the rows of every product were empty: 654 us for the first of these against 461 then.
+// up to 4096 in 51 us with the join; at 8 bits, which unpack with fewer instructions
+// a byte, 64 of 16384 in 345 us (6.4 TB/s, 94 %).  With pages of 16 tokens, whose
+// tiles take 32 copies, these are 621 us (3.7 TB/s) and 427; short contexts do not
+// mind (24 of up to 2047, 16 own heads, 8 bits: 31.3 us in pages of 16, 32.7 of 64).
 
 #include <cuda_runtime.h>
 
@@ -69,9 +72,10 @@ constexpr float kSlack = 5.0f;    // a logit may exceed what the weights are rel
 constexpr int kValueShift = 10;   // w s / S is held times 2^this: at most 2^15 in fp16
 // Tiles that beginning and ending an item counts (0 to 3 measure alike).
 constexpr int kCost = 1;
-// Query rows of a sequence's head group up to which this kernel runs: 32 rows over
-// 16 sequences of 4096 tokens take it 74 us, the kernel for many rows 80; beyond, it
-// reads the cache a third time.
+// Query rows of a sequence's head group up to which this kernel runs.  Over 16
+// sequences of 4096 tokens and 8 heads, 32 rows take it 64 us and the kernel for many
+// rows 75 (4 bits, 128 channels; 75 and 94 at 8 bits, 40 and 67 with 64 channels); each
+// 16 rows more read and unpack the cache once more here, about 22 us, and nothing there.
 constexpr int64_t kFewRows = 32;
 
 template <int D, int BITS, int ROWS>
@@ -724,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, BITS, 8 * HALVES>::kBlocks)
 // share the parts (each warp all 8 rows of a part, so that 8 loads are under
 // way) and then add up.  (Blocks of 8 warps: most CTAs have an item of two or
 // three parts or none, and small blocks run side by side.)  Bound by the latency
-// of its chain of loads: with cold caches 6.5 us for 64 sequences of 4096 tokens, 11 for 2
-// of 131072, 28 for two prompt chunks of 2048, whose parts are 35 MB.
+// of its chain of loads: with cold caches 5 us for 64 sequences of 4096 tokens, 9.5 for 2
+// of 131072, 27 for two prompt chunks of 2048, whose parts are 35 MB.
 constexpr int kJoinWarps = 8;
 
 template <int D, int ROWS>
@@ -852,8 +856,9 @@ struct Plan {
     bool cluster;
 };
 
-// Contexts of up to this many tiles (by the page table's width) run as clusters
-// when all clusters fit the device at once: one sequence of 517 tokens takes 10.9
+// Contexts of up to this many tiles run as clusters when all clusters fit the device
+// at once.  (By the page table's width, since only the device knows the lengths: short
+// contexts behind a wide table run in the other form.)  One sequence of 517 tokens takes 10.9
 // us so, 14.9 in two launches (events around the call; 5.3 us on the device), one
 // of 16000 23.2 against 25.2, one of 32000 39.6 against 29.3.
 constexpr int kClusterSize = 8;

@@ -64,6 +64,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return r;
 }
 
+// Small integers become fp16 as is widely done: put into the mantissa of 1024, whose
+// last place counts 1, and less 1024.
+
 // Eight nibbles as four pairs of fp16 (nibbles j and j + 4), CENTRED less 8: exact.
 template <bool CENTRED>
 __device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&pair)[4]) {

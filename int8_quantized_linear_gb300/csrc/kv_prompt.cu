@@ -16,9 +16,9 @@
 // copies pages, warp 13 issues the MMAs.  While one tile's softmax runs, the
 // tensor cores work on the other's products.  Four kinds of warp share one
 // instruction cache, so the loops are kept rolled: unrolling the softmax over
-// the row and the unpacking over the tile cost 20 % (650 against 541 us for two
-// chunks of 2048 tokens over 8192, 32 query heads over 8 x 128, 4 bits), and
-// inlining the waits as much again.
+// the row and the unpacking over the tile cost 20 % (650 against 541 us, when that
+// was done, for two chunks of 2048 tokens over 8192, 32 query heads over 8 x 128, 4
+// bits), inlining the waits as much again, and what is rare stands in functions.
 //
 // K and V become fp16 including scale and low value: fp16_rn(low + s code), one
 // rounding of 2^-11 relative to the element (scale and low value have 8 bits), so
@@ -42,9 +42,12 @@
 // rows are copied eight tokens at a time to a stride 16 bytes longer, which
 // keeps the transposing reads off each other's banks.
 //
-// Measured: those two chunks now 481 us with the join (1000 TFLOP/s, 52 % of a
+// Measured: those two chunks now 490 us with the join (982 TFLOP/s, 51 % of a
 // large bf16 product; the tensor pipe is busy 44 % of the time, the issue slots
-// 53 %), one prompt of 8192 tokens 586 us (938 TFLOP/s).
+// 53 %), 680 at 8 bits (707 TFLOP/s: one V stage, so that V's unpacking and P V
+// take turns), 407 with 64 channels (590); one prompt of 8192 tokens 600 us (916
+// TFLOP/s).  Parts of items cut between blocks go through memory: the join is 27 of
+// those 490 with cold caches.
 
 #include <cuda_runtime.h>
 
@@ -63,7 +66,7 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kKStages = 2;      // unpacked K tiles
 constexpr int kRawKeys = 2;      // raw K tiles (with the params of K and V)
 // Tiles that beginning and ending an item counts (one prompt of 8192 tokens, whose
-// items have 1 to 64 tiles: 789 us at 2, 586 at 4, 588 at 6).
+// items have 1 to 64 tiles: 789 us at 2, 586 at 4, 588 at 6, when it was chosen).
 constexpr int kCost = 4;
 constexpr int kInfo = 4;         // tiles whose exponents are kept
 constexpr float kPShift = 7.0f;  // P = 2^(logit - m + kPShift)
