@@ -155,7 +155,7 @@ def work(case):
             pairs += q * first + q * (q + 1) // 2
             seen += n
     return {"bytes": seen * h * _row_bytes(case) + 2 * sum(qs) * case["qheads"] * case["dim"] +
-            4 * sum(lens) * h * (2 if case["sum"] else 1) + 4 * seen // case["page"],
+            4 * seen * h * (2 if case["sum"] else 1) + 4 * seen // case["page"],
             "flops": (2 * case["dim"] + 2) * pairs * case["qheads"]}
 
 
@@ -390,10 +390,11 @@ def _weigh(s):
     if case["sum"]:
         older = j < (lens - nq)[:, None]
         x = x + torch.where(older[:, None], flat(s["previous"][at, :, :, None])[..., 0], torch.zeros_like(x))
-    # the visible pages' live tokens
+    # the tokens that some query sees
+    seen = see.any(1)
     slot = at[..., None] * page + torch.arange(page, device=DEV)  # [batch, pages, page]
-    slot = slot.flatten(1)[live]
-    s["weights"][slot // page, :, slot % page] = x.transpose(1, 2)[live]
+    slot = slot.flatten(1)[seen]
+    s["weights"][slot // page, :, slot % page] = x.transpose(1, 2)[seen]
     return s["weights"]
 
 
@@ -561,6 +562,7 @@ def exact(case, seed):
                 total += torch.softmax(a.masked_fill(hidden, float("-inf")), -1).sum(0)
             if case["sum"]:
                 total[: n - nq] += s["previous"][at, h].reshape(-1)[: n - nq].double()
-            out[at[j // page], h, j % page] = total
+            some = j[max(0, n - nq + 1 - w) if w else 0:]
+            out[at[some // page], h, some % page] = total[some]
         first += nq
     return out
