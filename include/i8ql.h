@@ -48,9 +48,10 @@ enum {
     I8QL_ERR_BAD_OFFSETS = 5,  /* grouped offsets not 0 .. T_total, non-decreasing     */
     I8QL_ERR_NO_DEVICE = 6,    /* no CUDA device, or not an sm_103 device              */
     I8QL_ERR_WORKSPACE_LIMIT = 7,/* w8a8_gemm_noalloc: problem exceeds its fixed array;
-                                    kv_cache_attention: workspace too small            */
-    I8QL_ERR_BAD_INDEX = 8       /* a cache slot, page, length or query offset is out of
-                                    range (sticky word)                                */
+                                    kv_cache_attention, kv_cache_weights: workspace
+                                    too small                                          */
+    I8QL_ERR_BAD_INDEX = 8       /* a cache slot, page, length, query offset or position
+                                    is out of range (sticky word)                      */
 };
 
 /* Largest K whose worst-case int8 dot product fits int32:
@@ -525,6 +526,136 @@ i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8
  */
 i8ql_status i8ql_kv_attention_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
                                         int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes);
+
+/*
+ * Rotary positions: the table of angles.
+ *
+ * No counterpart on the pages.  Row r of the table stands for a position p
+ * (positions[r], or r itself when positions is NULL):
+ *   table[r, i] = amplitude * cos(p * freqs[i]),  table[r, F + i] = amplitude * sin(p * freqs[i])
+ * Inputs: freqs fp64 [F], radians a position (finite; scaling for long contexts
+ * is in them), 8-byte aligned; positions int64 [P] (any sign) or NULL.
+ * Output: table fp32 [P, 2F], 16-byte aligned.  The angle's fraction of a turn
+ * is exact to |p| 2^-64, so cosine and sine are within 2^-23 of their value
+ * (before the amplitude's rounding) for |p| < 2^31.  F <= I8QL_ROTARY_MAX_D / 2.
+ */
+#define I8QL_ROTARY_MAX_D 512
+i8ql_status rotary_table(const double* freqs, const int64_t* positions, float* table, int64_t P, int64_t F,
+                         float amplitude, void* stream);
+
+/*
+ * Rotary positions: rows turned by the angles of their tokens.
+ *
+ * No counterpart on the pages.  Of every head's D channels the first rot are
+ * turned in pairs (a, b): channels (i, i + rot / 2), or with interleaved = 1
+ * (2i, 2i + 1), by row positions[t] of the table (cosines c, sines s):
+ *   a' = bf16(fl32(fl32(a c) - fl32(b s))),  b' = bf16(fl32(fl32(b c) + fl32(a s)))
+ * With backward = 1 by the negative angle (s -> -s): the gradient of the
+ * forward call with the same table, given the gradient of its output.  The
+ * channels from rot on are copied.  A token whose position is negative is
+ * copied as it is (padding); so is one past the table, which also records
+ * I8QL_ERR_BAD_INDEX.
+ *
+ * x and out: bf16 [T, heads, D], a token's heads * D values contiguous, tokens
+ * x_stride and out_stride elements apart (>= heads * D, multiples of 8; so
+ * slices of a fused projection need no copy), 16-byte aligned.  out may be x
+ * (the same pointer and stride) and share rows with it (other heads), but not
+ * overlap it otherwise.  table fp32 [table_rows, rot], 16-byte aligned;
+ * positions int64 [T], or NULL: token t takes row t (table_rows >= T).
+ * D a multiple of 8 up to I8QL_ROTARY_MAX_D, rot a multiple of 8 up to D,
+ * T * heads < 2^30.
+ */
+i8ql_status rotary_apply(const i8ql_bf16* x, int64_t x_stride, const float* table, int64_t table_rows,
+                         const int64_t* positions, i8ql_bf16* out, int64_t out_stride, int64_t T, int64_t heads,
+                         int64_t D, int64_t rot, int32_t interleaved, int32_t backward, void* stream);
+
+/*
+ * Queries and keys turned by their positions, keys and values quantized into
+ * the cache, in one launch: what rotary_apply on q and k and kv_cache_store on
+ * the turned keys and v do, bit for bit.
+ *
+ * No counterpart on the pages.  q and q_out bf16 [T, Hq, D] (strides and
+ * aliasing as rotary_apply's x and out; Hq = 0: no queries, both ignored); k,
+ * v, slots and the cache as kv_cache_store; table, positions and interleaved
+ * as rotary_apply, rot a multiple of 16.  A negative slot stores nothing and
+ * its query is turned all the same.  T * (Hq + H) < 2^30.
+ */
+i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf16* q_out, int64_t q_out_stride,
+                                  const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_stride, int64_t v_stride,
+                                  const float* table, int64_t table_rows, const int64_t* positions,
+                                  const int64_t* slots, uint8_t* codes, i8ql_bf16* params, int64_t T, int64_t Hq,
+                                  int64_t H, int64_t D, int64_t bits, int64_t page_size, int64_t num_pages, int64_t rot,
+                                  int32_t interleaved, void* stream);
+
+/*
+ * How much attention each cached token gets: softmax weights summed over query
+ * rows, for kv_cache_evict.
+ *
+ * No counterpart on the pages.  Sequences, queries, positions, window and page
+ * table as kv_cache_attention.  For cache head h and token j of a sequence of n
+ * query tokens, summed over the rows of h's query heads that see j,
+ *   weights[page, h, place] = before_j + sum_rows softmax(softmax_scale * q . k)_j
+ * where before_j is previous[page, h, place] for the tokens that were cached
+ * before this call's queries (j < kv_lens[b] - n), and 0 for the queries' own
+ * tokens (and for all with previous = NULL).  So one buffer, passed as both,
+ * keeps the sums of a sequence from prompt to last token, with no clearing of
+ * reused pages.  Tokens that no row of the call sees are left as they are.
+ *
+ * previous and weights: fp32 [num_pages, H, page_size], 16-byte aligned; the
+ * same buffer, or two that do not overlap.  All in fp32 (products on the
+ * codes, exact); rows that see no token add nothing.  A key row that is not
+ * finite gives unspecified weights of its sequence and head where it is seen.
+ * max_q: the most query tokens of one sequence (more record
+ * I8QL_ERR_BAD_INDEX); pages out of range record it too and are not written.
+ * workspace as kv_cache_attention, i8ql_kv_weights_workspace bytes.  The
+ * result does not depend on timing.  Sequences must not share a page that is
+ * seen: its weights would be written by each.
+ */
+i8ql_status kv_cache_weights(const i8ql_bf16* q, int64_t q_stride, const uint8_t* codes, const i8ql_bf16* params,
+                             const int32_t* page_table, int64_t table_width, const int32_t* kv_lens,
+                             const int32_t* q_offsets, const float* previous, float* weights, int64_t B, int64_t T_q,
+                             int64_t Hq, int64_t H, int64_t D, int64_t bits, int64_t page_size, int64_t num_pages,
+                             int64_t max_q, int64_t window, float softmax_scale, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/*
+ * Workspace of a kv_cache_weights call of these sizes on the current device,
+ * in bytes (*bytes is a HOST pointer; 0: none is needed).  No counterpart on
+ * the pages.  Depends on sizes only.
+ */
+i8ql_status i8ql_kv_weights_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
+                                      int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes);
+
+/*
+ * Cuts sequences of the cache down to a budget of tokens: per cache head, those
+ * that got most attention stay.
+ *
+ * No counterpart on the pages.  A sequence of n = kv_lens[b] > budget tokens
+ * keeps, of each head, its first `first` and last `last` tokens, and of those
+ * between the budget - first - last with the largest weights (equal ones: the
+ * lower index; not a number is the least).  Kept tokens keep their order; the
+ * s-th moves to place s of the sequence, with its codes, params and weight.
+ * Heads keep different tokens, all the same number.  A sequence of n <= budget
+ * tokens keeps all.  Positions are the caller's: keys are stored turned
+ * (kv_cache_store_rotary), and the next token's position goes on from n, its
+ * slot from new_lens[b].
+ *
+ * new_table int32 [B, new_width]: the pages that the kept tokens move to, none
+ * of which any sequence of the call occupies (so pages shared between
+ * sequences can be cut); NULL (or page_table itself): in place, the front
+ * pages of each sequence, which no other sequence may share; what lies behind
+ * is left as it was.  weights fp32 [num_pages, H, page_size], 16-byte aligned.
+ * Outputs: new_lens int32 [B], min(n, budget) (not overlapping kv_lens); kept
+ * int32 [B, H, budget], the kept tokens' indices in order, -1 behind new_lens[b].
+ * first + last <= budget.  Lengths and pages out of range, and a new_width too
+ * small for the kept tokens, record I8QL_ERR_BAD_INDEX; no row is then read or
+ * written outside the cache.  B * H * budget / 16 < 2^31.
+ */
+i8ql_status kv_cache_evict(uint8_t* codes, i8ql_bf16* params, float* weights, const int32_t* page_table,
+                           int64_t table_width, const int32_t* kv_lens, const int32_t* new_table, int64_t new_width,
+                           int32_t* new_lens, int32_t* kept, int64_t B, int64_t H, int64_t D, int64_t bits,
+                           int64_t page_size, int64_t num_pages, int64_t budget, int64_t first, int64_t last,
+                           void* stream);
 
 /*
  * W8A8 GEMM that allocates nothing.

@@ -13,6 +13,7 @@ from .capi import (  # noqa: F401
     i8ql_fp8_plan,
     i8ql_get_device_error,
     i8ql_kv_attention_workspace,
+    i8ql_kv_weights_workspace,
     i8ql_set_early_weight_loads,
     i8ql_version,
     i8ql_w8a8_linear_launches,
@@ -20,8 +21,11 @@ from .capi import (  # noqa: F401
     i8ql_w8a8_plan,
     kv_cache_alloc,
     kv_cache_attention,
+    kv_cache_evict,
     kv_cache_load,
     kv_cache_store,
+    kv_cache_store_rotary,
+    kv_cache_weights,
     moe_combine,
     moe_expert_mlp_w8a16,
     moe_route_topk,
@@ -30,6 +34,9 @@ from .capi import (  # noqa: F401
     quantize_weight_per_channel_fp8,
     quantize_weight_per_channel_int8,
     quantize_weight_w4_g128,
+    rotary_apply,
+    rotary_frequencies,
+    rotary_table,
     w4a16_gemm,
     w8a8_fp8_gemm,
     w8a8_fp8_linear,

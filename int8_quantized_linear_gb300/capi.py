@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -36,6 +37,7 @@ I8QL_MAX_K = 133144
 I8QL_NOALLOC_MAX_ELEMENTS = 16 * 1024 * 1024
 I8QL_KV_MIN_PAGE = 16
 I8QL_KV_MAX_PAGE = 256
+I8QL_ROTARY_MAX_D = 512
 I8QL_W8A8_DECODE_MAX_M = 32  # w8a8_gemm runs the decode kernel up to this M
 
 # Every symbol the C header declares, with its ctypes signature.
@@ -72,6 +74,12 @@ SIGNATURES = {
     "kv_cache_load": (_S, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P]),
     "kv_cache_attention": (_S, [_P, _I64, _P, _P, _P, _I64, _P, _P, _P, *[_I64] * 10, _F, _P, _I64, _P]),
     "i8ql_kv_attention_workspace": (_S, [*[_I64] * 9, _P]),
+    "rotary_table": (_S, [_P, _P, _P, _I64, _I64, _F, _P]),
+    "rotary_apply": (_S, [_P, _I64, _P, _I64, _P, _P, *[_I64] * 5, _S, _S, _P]),
+    "kv_cache_store_rotary": (_S, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, *[_I64] * 8, _S, _P]),
+    "kv_cache_weights": (_S, [_P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, *[_I64] * 10, _F, _P, _I64, _P]),
+    "i8ql_kv_weights_workspace": (_S, [*[_I64] * 9, _P]),
+    "kv_cache_evict": (_S, [_P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, *[_I64] * 9, _P]),
     "moe_expert_mlp_w8a16": (_S, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
 }
 
@@ -683,3 +691,262 @@ def kv_cache_attention(q, codes, params, page_table, kv_lens, q_offsets=None, ma
     if st != I8QL_OK:
         _check(st, "kv_cache_attention")
     return out
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, low=1.0, high=4.0, device="cuda"):
+    """fp64 [rot / 2]: radians a position of rotary channel pairs,
+    base ** (-2 i / rot), scaled for contexts `factor` times as long:
+
+    None      as they are
+    "linear"  all divided by factor (positions are interpolated)
+    "base"    a larger base, that divides the slowest by factor and leaves the
+              fastest
+    "turns"   by how often pair i turns over `original` positions,
+              n = original f / 2 pi: divided by factor up to n = low, as they
+              are from n = high on, between them blended linearly in n
+    "index"   the same, blended linearly in i between the (whole) indices that
+              turn `high` and `low` times
+    """
+    if rot <= 0 or rot % 2 or base <= 1.0 or factor < 1.0:
+        raise ValueError("rot must be positive and even, base above 1, factor at least 1")
+    if scaling in ("turns", "index") and not (original > 0 and 0 < low < high):
+        raise ValueError("scaling by turns needs original > 0 and 0 < low < high")
+    n = rot // 2
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("a single frequency has no base to scale")
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2.0 * i / rot) for i in range(n)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "turns":
+        keep = [min(max((original * x / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for x in f]
+        f = [x * ((1 - k) / factor + k) for x, k in zip(f, keep)]
+    elif scaling == "index":
+        at = lambda turns: n * math.log(original / (2 * math.pi * turns)) / math.log(base)  # noqa: E731
+        begin, end = max(math.floor(at(high)), 0), min(math.ceil(at(low)), n - 1)
+        keep = [1 - min(max((i - begin) / max(end - begin, 1e-3), 0.0), 1.0) for i in range(n)]
+        f = [x * ((1 - k) / factor + k) for x, k in zip(f, keep)]
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(f, dtype=torch.float64, device=device)
+
+
+def _current(t: torch.Tensor, name: str) -> int | None:
+    """The tensor's device index (None: not a CUDA tensor), which has to be the current device's."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        return None
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, not on the current device (cuda:{torch.cuda.current_device()})")
+    return device
+
+
+def rotary_table(freqs, positions, amplitude=1.0, table=None, stream=None):
+    """fp32 [P, 2F]: amplitude times the cosines, then the sines, of p *
+    freqs (fp64 [F], see rotary_frequencies) for the positions 0 .. P-1 (an
+    int) or those of an int64 tensor [P]."""
+    device = _current(freqs, "freqs")
+    f = freqs.shape[0] if freqs.dim() == 1 else -1
+    _need(freqs, torch.float64, (f,), "freqs", device)
+    if isinstance(positions, torch.Tensor):
+        p = positions.shape[0] if positions.dim() == 1 else -1
+        _need(positions, torch.int64, (p,), "positions", device)
+        at = positions.data_ptr()
+    else:
+        p, at = int(positions), None
+        if p < 0:
+            raise ValueError("positions must not be negative")
+    if table is None:
+        table = _empty((p, 2 * f), torch.float32, freqs.device, stream)
+    else:
+        _need(table, torch.float32, (p, 2 * f), "table", device)
+    _check(lib().rotary_table(freqs.data_ptr(), at, table.data_ptr(), p, f, amplitude, _stream(stream)), "rotary_table")
+    return table
+
+
+def _rotary(table, positions, tokens: int, device) -> tuple[int, int, int | None]:
+    """(rows, channels turned, positions' address) of a table for so many tokens."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [rows, rot]")
+    _need(table, torch.float32, tuple(table.shape), "table", device)
+    if positions is None:
+        return table.shape[0], table.shape[1], None
+    _need(positions, torch.int64, (tokens,), "positions", device)
+    return table.shape[0], table.shape[1], positions.data_ptr()
+
+
+def rotary_apply(x, table, positions=None, interleaved=False, backward=False, out=None, stream=None):
+    """bf16 [T, heads, D]: the first rot channels of every head of x (whose
+    tokens may lie apart: a slice of a fused projection) turned by the rows
+    positions (int64 [T]; None: row t for token t) of table (fp32 [rows, rot],
+    see rotary_table).  Pairs are channels i and i + rot / 2, or neighbours
+    with interleaved.  backward: by the negative angles, the gradient.  Tokens
+    with a negative position are copied.  out may be x."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be [T, heads, D]")
+    device = _current(x, "x")
+    t, heads, d = x.shape
+    x_step = _need_heads(x, heads, d, "x", device)
+    rows, rot, at = _rotary(table, positions, t, device)
+    if out is None:
+        out, out_step = _empty((t, heads, d), torch.bfloat16, x.device, stream), heads * d
+    else:
+        out_step = _need_heads(out, heads, d, "out", device)
+        if out.shape[0] != t:
+            raise ValueError("x and out disagree on T")
+    st = lib().rotary_apply(x.data_ptr(), x_step, table.data_ptr(), rows, at, out.data_ptr(), out_step, t, heads, d, rot,
+                            bool(interleaved), bool(backward), _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "rotary_apply")
+    return out
+
+
+def kv_cache_store_rotary(q, k, v, table, slots, codes, params, positions=None, interleaved=False, q_out=None,
+                          stream=None):
+    """rotary_apply on q and k and kv_cache_store of the turned keys and v in one
+    launch.  Returns the turned queries, bf16 [T, q_heads, head_dim] (q_out may
+    be q; None with q = None, which stores alone)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T, heads, head_dim]")
+    t, _, d = k.shape
+    pages, heads, page, bits, device = _kv_cache(codes, params, d)
+    k_step = _need_heads(k, heads, d, "k", device)
+    v_step = _need_heads(v, heads, d, "v", device)
+    if v.shape[0] != t:
+        raise ValueError("k and v disagree on T")
+    _need(slots, torch.int64, (t,), "slots", device)
+    rows, rot, at = _rotary(table, positions, t, device)
+    hq = q_step = q_out_step = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [T, q_heads, head_dim]")
+        hq = q.shape[1]
+        q_step = _need_heads(q, hq, d, "q", device)
+        if q.shape[0] != t:
+            raise ValueError("q and k disagree on T")
+        if q_out is None:
+            q_out, q_out_step = _empty((t, hq, d), torch.bfloat16, codes.device, stream), hq * d
+        else:
+            q_out_step = _need_heads(q_out, hq, d, "q_out", device)
+            if q_out.shape[0] != t:
+                raise ValueError("q and q_out disagree on T")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = lib().kv_cache_store_rotary(_ptr(q), q_step, _ptr(q_out), q_out_step, k.data_ptr(), v.data_ptr(), k_step, v_step,
+                                     table.data_ptr(), rows, at, slots.data_ptr(), codes.data_ptr(), params.data_ptr(),
+                                     t, hq, heads, d, bits, page, pages, rot, bool(interleaved), _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_store_rotary")
+    return q_out
+
+
+# ---------------------------------------------------------------- eviction from the key/value cache
+
+def i8ql_kv_weights_workspace(batch, tokens, q_heads, heads, head_dim, bits, page_size, table_width, max_q=1) -> int:
+    """Bytes of workspace a kv_cache_weights call of these sizes takes on the
+    current device."""
+    n = ctypes.c_int64(0)
+    _check(lib().i8ql_kv_weights_workspace(batch, tokens, q_heads, heads, head_dim, bits, page_size, table_width, max_q,
+                                           ctypes.byref(n)), "i8ql_kv_weights_workspace")
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _weights_workspace_size(device: int, *sizes) -> int:
+    """The same, asked once per device and sizes (a function of those alone)."""
+    return i8ql_kv_weights_workspace(*sizes)
+
+
+def kv_cache_weights(q, codes, params, page_table, kv_lens, weights, q_offsets=None, max_q=None, window=0, scale=None,
+                     previous=None, workspace=None, stream=None):
+    """Attention weights summed per cached token and head: weights (fp32
+    [num_pages, heads, page_size]) = previous (the same; may be weights; None:
+    nothing yet) of the tokens cached before this call's queries, plus the
+    softmax weights of the query rows that see a token.  The other arguments as
+    kv_cache_attention's, max_q being the most query rows a sequence has.
+    Tokens that no query sees keep their weights.  Returns weights."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, head_dim]")
+    t, hq, d = q.shape
+    pages, heads, page, bits, device = _kv_cache(codes, params, d)
+    q_step = _need_heads(q, hq, d, "q", device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width]")
+    b, width = page_table.shape
+    _need(page_table, torch.int32, (b, width), "page_table", device)
+    _need(kv_lens, torch.int32, (b,), "kv_lens", device)
+    _need(weights, torch.float32, (pages, heads, page), "weights", device)
+    if previous is not None:
+        _need(previous, torch.float32, (pages, heads, page), "previous", device)
+    if q_offsets is not None:
+        _need(q_offsets, torch.int32, (b + 1,), "q_offsets", device)
+    if max_q is None:
+        max_q = 1 if q_offsets is None else t
+    max_q = min(max_q, t)
+    if workspace is None:
+        size = 0
+        if t and b:
+            size = _weights_workspace_size(torch.cuda.current_device(), b, t, hq, heads, d, bits, page, width, max_q)
+        if size:
+            workspace = _empty((size,), torch.uint8, codes.device, stream)
+    else:
+        _need(workspace, torch.uint8, (workspace.numel(),), "workspace", device)
+        size = workspace.numel()
+    st = lib().kv_cache_weights(q.data_ptr(), q_step, codes.data_ptr(), params.data_ptr(), page_table.data_ptr(), width,
+                                kv_lens.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
+                                None if previous is None else previous.data_ptr(), weights.data_ptr(), b, t, hq, heads,
+                                d, bits, page, pages, max_q, window, d ** -0.5 if scale is None else scale,
+                                None if workspace is None else workspace.data_ptr(), size, _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_weights")
+    return weights
+
+
+def kv_cache_evict(codes, params, weights, page_table, kv_lens, budget, first=0, last=0, new_table=None, new_lens=None,
+                   kept=None, stream=None):
+    """Cuts every sequence to at most `budget` tokens: per head its first
+    `first` and last `last` tokens stay, and those between with the largest
+    weights (fp32 [num_pages, heads, page_size], see kv_cache_weights); codes,
+    params and weights move to the front of the sequence's pages, or to those
+    of new_table (int32 [B, width], pages that no sequence of the call
+    occupies).  Returns (new_lens int32 [B], kept int32 [B, heads, budget]: the
+    kept tokens' indices, -1 behind the last)."""
+    if codes.dim() != 5:
+        raise ValueError("codes must be [num_pages, 2, heads, page_size, head_dim * bits / 8]")
+    row = codes.shape[4]  # (only the bytes of a row count here)
+    d, bits = {32: (64, 4), 64: (128, 4), 128: (128, 8)}.get(row, (row, 8))
+    pages, heads, page, bits, device = _kv_cache(codes, params, d)
+    _need(weights, torch.float32, (pages, heads, page), "weights", device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width]")
+    b, width = page_table.shape
+    _need(page_table, torch.int32, (b, width), "page_table", device)
+    _need(kv_lens, torch.int32, (b,), "kv_lens", device)
+    new_width = width
+    if new_table is not None:
+        if new_table.dim() != 2:
+            raise ValueError("new_table must be [B, width]")
+        new_width = new_table.shape[1]
+        _need(new_table, torch.int32, (b, new_width), "new_table", device)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    if new_lens is None:
+        new_lens = _empty((b,), torch.int32, codes.device, stream)
+    else:
+        _need(new_lens, torch.int32, (b,), "new_lens", device)
+    if kept is None:
+        kept = _empty((b, heads, budget), torch.int32, codes.device, stream)
+    else:
+        _need(kept, torch.int32, (b, heads, budget), "kept", device)
+    st = lib().kv_cache_evict(codes.data_ptr(), params.data_ptr(), weights.data_ptr(), page_table.data_ptr(), width,
+                              kv_lens.data_ptr(), None if new_table is None else new_table.data_ptr(), new_width,
+                              new_lens.data_ptr(), kept.data_ptr(), b, heads, d, bits, page, pages, budget, first, last,
+                              _stream(stream))
+    if st != I8QL_OK:
+        _check(st, "kv_cache_evict")
+    return new_lens, kept

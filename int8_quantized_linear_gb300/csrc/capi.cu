@@ -13,6 +13,8 @@
 
 #include "common.cuh"
 #include "kv_schedule.cuh"
+#include "kv_weights.cuh"
+#include "rotary.cuh"
 
 namespace i8ql {
 
@@ -561,6 +563,222 @@ i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8
     return from_cuda(launch_kv_attention(p, D, bits, max_q, workspace, env));
 }
 
+namespace {
+
+// Whether token rows of n values at `a` and `b` (`rows` of them, their strides apart)
+// share memory without being the same rows.
+bool tangled(const i8ql_bf16* a, int64_t a_stride, const i8ql_bf16* b, int64_t b_stride, int64_t rows, int64_t n) {
+    if (a == b) return a_stride != b_stride && rows > 1;
+    const i8ql_bf16 *lo = a < b ? a : b, *hi = a < b ? b : a;
+    const int64_t lo_stride = a < b ? a_stride : b_stride;
+    const int64_t apart = hi - lo;
+    if (apart >= (rows - 1) * lo_stride + n) return false;
+    if (a_stride != b_stride) return true;
+    // (neighbours in rows of the same width do not meet)
+    return apart % a_stride < n || apart % a_stride > a_stride - n;
+}
+
+// A table of angles for T tokens' rows of D channels.
+i8ql_status check_rotary(const float* table, int64_t table_rows, const int64_t* positions, int64_t T, int64_t D,
+                         int64_t rot, int64_t multiple, int32_t interleaved) {
+    if (rot <= 0 || table_rows < 0 || (interleaved != 0 && interleaved != 1)) return I8QL_ERR_INVALID_ARG;
+    if (rot > D || rot % multiple != 0 || table_rows >= kMaxRows) return I8QL_ERR_UNSUPPORTED;
+    if (T == 0) return I8QL_OK;
+    if (positions == nullptr && table_rows < T) return I8QL_ERR_INVALID_ARG;
+    if (positions != nullptr && !aligned(positions, 8)) return I8QL_ERR_INVALID_ARG;
+    return check_matrix(table, table_rows);
+}
+
+RotaryTable make_rotary(const float* table, int64_t table_rows, const int64_t* positions, int64_t rot) {
+    RotaryTable t;
+    t.rows = table;
+    t.count = table_rows;
+    t.positions = positions;
+    t.rot = (int)rot;
+    return t;
+}
+
+}  // namespace
+
+i8ql_status rotary_table(const double* freqs, const int64_t* positions, float* table, int64_t P, int64_t F,
+                         float amplitude, void* stream) {
+    I8QL_TRY(check_rows(P));
+    if (F <= 0 || !std::isfinite(amplitude)) return I8QL_ERR_INVALID_ARG;
+    if (F > I8QL_ROTARY_MAX_D / 2) return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_vec(freqs, P, 8));
+    if (positions != nullptr && !aligned(positions, 8)) return I8QL_ERR_INVALID_ARG;
+    I8QL_TRY(check_matrix(table, P));
+    if (P == 0) return I8QL_OK;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    return from_cuda(launch_rotary_table(freqs, positions, table, P, F, amplitude, env));
+}
+
+i8ql_status rotary_apply(const i8ql_bf16* x, int64_t x_stride, const float* table, int64_t table_rows,
+                         const int64_t* positions, i8ql_bf16* out, int64_t out_stride, int64_t T, int64_t heads,
+                         int64_t D, int64_t rot, int32_t interleaved, int32_t backward, void* stream) {
+    I8QL_TRY(check_rows(T));
+    if (heads <= 0 || D <= 0 || (backward != 0 && backward != 1)) return I8QL_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > I8QL_ROTARY_MAX_D || heads > 65535 || T * heads >= ((int64_t)1 << 30))
+        return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_rotary(table, table_rows, positions, T, D, rot, 8, interleaved));
+    I8QL_TRY(check_strided(x, T, heads * D, x_stride));
+    I8QL_TRY(check_strided(out, T, heads * D, out_stride));
+    if (T == 0) return I8QL_OK;
+    if (tangled(x, x_stride, out, out_stride, T, heads * D)) return I8QL_ERR_INVALID_ARG;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    return from_cuda(launch_rotary_apply(x, x_stride, make_rotary(table, table_rows, positions, rot), out, out_stride, T,
+                                         heads, D, interleaved != 0, backward != 0, env));
+}
+
+i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf16* q_out, int64_t q_out_stride,
+                                  const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_stride, int64_t v_stride,
+                                  const float* table, int64_t table_rows, const int64_t* positions,
+                                  const int64_t* slots, uint8_t* codes, i8ql_bf16* params, int64_t T, int64_t Hq,
+                                  int64_t H, int64_t D, int64_t bits, int64_t page_size, int64_t num_pages, int64_t rot,
+                                  int32_t interleaved, void* stream) {
+    I8QL_TRY(check_rows(T));
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    if (Hq < 0) return I8QL_ERR_INVALID_ARG;
+    if (Hq > 65535 || T * (Hq + H) >= ((int64_t)1 << 30)) return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_rotary(table, table_rows, positions, T, D, rot, 16, interleaved));
+    if (Hq > 0) {
+        I8QL_TRY(check_strided(q, T, Hq * D, q_stride));
+        I8QL_TRY(check_strided(q_out, T, Hq * D, q_out_stride));
+    }
+    I8QL_TRY(check_strided(k, T, H * D, k_stride));
+    I8QL_TRY(check_strided(v, T, H * D, v_stride));
+    I8QL_TRY(check_vec(slots, T, 8));
+    I8QL_TRY(check_matrix(codes, T));
+    I8QL_TRY(check_matrix(params, T));
+    if (T == 0) return I8QL_OK;
+    if (Hq > 0 && tangled(q, q_stride, q_out, q_out_stride, T, Hq * D)) return I8QL_ERR_INVALID_ARG;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    return from_cuda(launch_kv_store_rotary(q, q_stride, q_out, q_out_stride, k, v, k_stride, v_stride,
+                                            make_rotary(table, table_rows, positions, rot), interleaved != 0, slots,
+                                            make_kv_cache(codes, params, H, page_size, num_pages), T, Hq, D, bits, env));
+}
+
+i8ql_status i8ql_kv_weights_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
+                                      int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes) {
+    I8QL_TRY(check_kv(H, D, bits, page_size, 1));
+    I8QL_TRY(check_kv_attention(B, T_q, Hq, H, page_size, table_width, max_q));
+    if (bytes == nullptr) return I8QL_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (B == 0 || T_q == 0) return I8QL_OK;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(nullptr, &env, &s)) return s;
+    *bytes = (int64_t)kv_weights_workspace(B, T_q, Hq / H, H, table_width * page_size, max_q, env.sm_count);
+    return I8QL_OK;
+}
+
+i8ql_status kv_cache_weights(const i8ql_bf16* q, int64_t q_stride, const uint8_t* codes, const i8ql_bf16* params,
+                             const int32_t* page_table, int64_t table_width, const int32_t* kv_lens,
+                             const int32_t* q_offsets, const float* previous, float* weights, int64_t B, int64_t T_q,
+                             int64_t Hq, int64_t H, int64_t D, int64_t bits, int64_t page_size, int64_t num_pages,
+                             int64_t max_q, int64_t window, float softmax_scale, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    I8QL_TRY(check_kv_attention(B, T_q, Hq, H, page_size, table_width, max_q));
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (window < 0 || !std::isfinite(scale_log2)) return I8QL_ERR_INVALID_ARG;
+    if (q_offsets == nullptr && T_q != B) return I8QL_ERR_INVALID_ARG;
+    I8QL_TRY(check_strided(q, T_q, Hq * D, q_stride));
+    I8QL_TRY(check_matrix(codes, T_q));
+    I8QL_TRY(check_matrix(params, T_q));
+    I8QL_TRY(check_vec(page_table, T_q, 4));
+    I8QL_TRY(check_vec(kv_lens, T_q, 4));
+    if (q_offsets != nullptr && !aligned(q_offsets, 4)) return I8QL_ERR_INVALID_ARG;
+    if (previous != nullptr && !aligned(previous, 16)) return I8QL_ERR_INVALID_ARG;
+    I8QL_TRY(check_matrix(weights, T_q));
+    if (T_q == 0) return I8QL_OK;
+    if (B == 0) return I8QL_ERR_INVALID_ARG;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    const int64_t G = Hq / H, max_kv = table_width * page_size;
+    max_q = max_q < T_q ? max_q : T_q;
+    if (!kv_weights_fits(B, G, H, max_kv, max_q, env.sm_count)) return I8QL_ERR_UNSUPPORTED;
+    const int64_t need = (int64_t)kv_weights_workspace(B, T_q, G, H, max_kv, max_q, env.sm_count);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return I8QL_ERR_WORKSPACE_LIMIT;
+        if (!aligned(workspace, 16)) return I8QL_ERR_INVALID_ARG;
+    }
+    KvWeightsParams p = {};
+    p.a.cache = make_kv_cache(codes, params, H, page_size, num_pages);
+    p.a.q = q;
+    p.a.q_stride = q_stride;
+    p.a.table = page_table;
+    p.a.table_width = table_width;
+    p.a.kv_lens = kv_lens;
+    p.a.q_offsets = q_offsets;
+    p.a.B = B;
+    p.a.T_q = T_q;
+    p.a.G = (int)G;
+    p.a.window = window;
+    p.a.scale_log2 = scale_log2;
+    p.a.err = env.err;
+    p.max_q = max_q;
+    p.previous = previous;
+    p.weights = weights;
+    return from_cuda(launch_kv_weights(p, D, bits, workspace, env));
+}
+
+i8ql_status kv_cache_evict(uint8_t* codes, i8ql_bf16* params, float* weights, const int32_t* page_table,
+                           int64_t table_width, const int32_t* kv_lens, const int32_t* new_table, int64_t new_width,
+                           int32_t* new_lens, int32_t* kept, int64_t B, int64_t H, int64_t D, int64_t bits,
+                           int64_t page_size, int64_t num_pages, int64_t budget, int64_t first, int64_t last,
+                           void* stream) {
+    I8QL_TRY(check_kv(H, D, bits, page_size, num_pages));
+    if (B < 0 || table_width <= 0 || budget <= 0 || first < 0 || last < 0 || first > budget || last > budget - first)
+        return I8QL_ERR_INVALID_ARG;
+    if (new_table == nullptr) {
+        new_table = page_table;
+        new_width = table_width;
+    }
+    if (new_width <= 0 || (new_table == page_table && new_width != table_width)) return I8QL_ERR_INVALID_ARG;
+    if (B >= kMaxRows || table_width > (kMaxRows - 65536) / page_size || new_width > (kMaxRows - 65536) / page_size ||
+        budget > kMaxRows - 65536 || !kv_evict_fits(B, H, D * bits / 8, budget))
+        return I8QL_ERR_UNSUPPORTED;
+    I8QL_TRY(check_matrix(codes, B));
+    I8QL_TRY(check_matrix(params, B));
+    I8QL_TRY(check_matrix(weights, B));
+    I8QL_TRY(check_vec(page_table, B, 4));
+    I8QL_TRY(check_vec(new_table, B, 4));
+    I8QL_TRY(check_vec(kv_lens, B, 4));
+    I8QL_TRY(check_vec(new_lens, B, 4));
+    I8QL_TRY(check_vec(kept, B, 4));
+    if (B == 0) return I8QL_OK;
+    // (every head reads kv_lens while the first writes new_lens)
+    if (new_lens < kv_lens + B && kv_lens < new_lens + B) return I8QL_ERR_INVALID_ARG;
+    LaunchEnv env;
+    i8ql_status s;
+    if (!launch_env(stream, &env, &s)) return s;
+    KvEvictParams p = {};
+    p.cache = make_kv_cache(codes, params, H, page_size, num_pages);
+    p.weights = weights;
+    p.table = page_table;
+    p.table_width = table_width;
+    p.kv_lens = kv_lens;
+    p.new_table = new_table;
+    p.new_width = new_width;
+    p.new_lens = new_lens;
+    p.kept = kept;
+    p.B = B;
+    p.budget = (int)budget;
+    p.first = (int)first;
+    p.last = (int)last;
+    p.row_bytes = (int)(D * bits / 8);
+    p.err = env.err;
+    return from_cuda(launch_kv_evict(p, env));
+}
+
 i8ql_status i8ql_get_device_error(void* stream) {
     LaunchEnv env;
     i8ql_status s;
@@ -656,8 +874,8 @@ const char* i8ql_status_string(i8ql_status status) {
         case I8QL_ERR_NO_DEVICE: return "no usable sm_103 CUDA device";
         case I8QL_ERR_WORKSPACE_LIMIT:
             return "workspace too small (w8a8_gemm_noalloc: M * K > 16 Mi for M > 32 exceeds its fixed array; "
-                   "kv_cache_attention: less than i8ql_kv_attention_workspace reports)";
-        case I8QL_ERR_BAD_INDEX: return "a cache slot, page, length or query offset is out of range";
+                   "kv_cache_attention, kv_cache_weights: less than their workspace queries report)";
+        case I8QL_ERR_BAD_INDEX: return "a cache slot, page, length, query offset or position is out of range";
         default: return "unknown status";
     }
 }

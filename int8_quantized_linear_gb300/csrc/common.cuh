@@ -201,6 +201,28 @@ cudaError_t launch_kv_store(const uint16_t* k, const uint16_t* v, int64_t k_stri
                             const LaunchEnv& env);
 cudaError_t launch_kv_load(const KvCache& cache, const int64_t* slots, uint16_t* k, uint16_t* v, int64_t T, int64_t D,
                            int64_t bits, const LaunchEnv& env);
+// Rotary positions (rotary.cuh): the table of angles, rows turned by them, and the
+// cache's store with queries and keys turned on the way.
+struct RotaryTable;
+cudaError_t launch_rotary_table(const double* freqs, const int64_t* positions, float* table, int64_t P, int64_t F,
+                                float amplitude, const LaunchEnv& env);
+cudaError_t launch_rotary_apply(const uint16_t* x, int64_t x_stride, const RotaryTable& table, uint16_t* out,
+                                int64_t out_stride, int64_t T, int64_t heads, int64_t D, bool interleaved,
+                                bool backward, const LaunchEnv& env);
+cudaError_t launch_kv_store_rotary(const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                                   const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                                   const RotaryTable& table, bool interleaved, const int64_t* slots,
+                                   const KvCache& cache, int64_t T, int64_t q_heads, int64_t D, int64_t bits,
+                                   const LaunchEnv& env);
+// Attention weights summed per cached token (workspace bytes; whether the grids fit;
+// the launch), and eviction by them (kv_weights.cuh).
+struct KvWeightsParams;
+struct KvEvictParams;
+size_t kv_weights_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
+bool kv_weights_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
+cudaError_t launch_kv_weights(KvWeightsParams p, int64_t D, int64_t bits, void* workspace, const LaunchEnv& env);
+bool kv_evict_fits(int64_t B, int64_t H, int64_t row_bytes, int64_t budget);
+cudaError_t launch_kv_evict(KvEvictParams p, const LaunchEnv& env);
 // Workspace bytes launch_kv_attention wants for these sizes, and the launch:
 // the parts' addresses in `p` are set from `workspace`.
 size_t kv_attention_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t D, int64_t bits, int64_t max_kv,

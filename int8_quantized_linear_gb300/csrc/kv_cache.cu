@@ -22,11 +22,15 @@
 // 127.6 us against 139.9 with two unrelated rows (131072 tokens of 8 heads x 128
 // channels, 4 bits).  One row at a time, behind its slot, reached a third of the
 // bandwidth.
+//
+// A third kernel turns queries and keys by their positions (rotary.cuh) on the
+// way: the same store behind a key's rotation, and the queries written out.
 
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
 #include "quant_math.cuh"
+#include "rotary.cuh"
 
 namespace i8ql {
 namespace {
@@ -152,6 +156,44 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// A row's (lo, -hi) as a pair, in every lane of the row: one minimum does both, over
+// a thread's pairs, a pair's halves and the row's lanes (a row is a whole group of
+// lanes; all lanes of the warp shuffle).
+template <int LANES>
+__device__ __forceinline__ uint32_t row_ends(const uint4& a, const uint4& b) {
+    auto least4 = [](const uint4& x) { return min_bf16x2(min_bf16x2(x.x, x.y), min_bf16x2(x.z, x.w)); };
+    auto most4 = [](const uint4& x) { return max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w)); };
+    const uint32_t least = min_bf16x2(least4(a), least4(b));
+    const uint32_t most = max_bf16x2(most4(a), most4(b)) ^ 0x80008000u;
+    uint32_t ends = min_bf16x2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
+#pragma unroll
+    for (int m = 1; m < LANES; m <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+    return ends;
+}
+
+// The codes of 8 channels of a and 8 of b (4 bits: a word each; else two) of a row
+// with these ends, and the row's (scale, low).
+template <int BITS>
+__device__ __forceinline__ uint32_t row_codes(const uint4& a, const uint4& b, uint32_t ends, uint32_t (&out)[4]) {
+    const float lo = lo_bf16(ends), hi = -hi_bf16(ends);
+    const float ratio = divided_by<(1 << BITS) - 1>(__fsub_rn(hi, lo));  // >= 0
+    const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
+    const float s = __uint_as_float(s_bits);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (s > 0.0f) kv_codes(j ? b : a, lo, s, c);
+        if constexpr (BITS == 4) {
+            // (only the low byte of each sum matters, and its halves do not meet)
+            out[j] = low_bytes(c[0] + (c[1] << 4), c[2] + (c[3] << 4), c[4] + (c[5] << 4), c[6] + (c[7] << 4));
+        } else {
+            out[2 * j] = low_bytes(c[0], c[1], c[2], c[3]);
+            out[2 * j + 1] = low_bytes(c[4], c[5], c[6], c[7]);
+        }
+    }
+    return (s_bits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+}
+
 // 32768 tokens of 8 heads x 128 channels, 4 bits: 39.6 us, 4300 GB/s (63 % of a
 // copy; 131072 tokens: 128 us, 5320 GB/s).  Bound by instruction issue: what the
 // codes take an element, and what a row's scale takes.  10 blocks an SM: with the
@@ -180,41 +222,91 @@ __global__ void __launch_bounds__(kKvThreads, 10) kv_store_kernel(const uint16_t
     const int64_t key = cache_row(p, row, slot);
 #pragma unroll
     for (int i = 0; i < kKvRows; ++i) {
-        // Over the thread's pairs; then as a pair (lo, -hi), of which one minimum does
-        // both, over a pair's halves and over the row's lanes (a row is a whole group
-        // of lanes; all lanes of the warp shuffle).
-        auto least4 = [](const uint4& x) { return min_bf16x2(min_bf16x2(x.x, x.y), min_bf16x2(x.z, x.w)); };
-        auto most4 = [](const uint4& x) { return max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w)); };
-        const uint32_t least = min_bf16x2(least4(w[i][0]), least4(w[i][1]));
-        const uint32_t most = max_bf16x2(most4(w[i][0]), most4(w[i][1])) ^ 0x80008000u;
-        uint32_t ends = min_bf16x2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
-#pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+        const uint32_t ends = row_ends<kLanes>(w[i][0], w[i][1]);
         if (key < 0) continue;
         const int64_t index = i ? key + value_rows(p.cache) : key;
-        const float lo = lo_bf16(ends), hi = -hi_bf16(ends);
-        const float ratio = divided_by<(1 << BITS) - 1>(__fsub_rn(hi, lo));  // >= 0
-        const uint32_t s_bits = (__float_as_uint(ratio) + 0xffffu) & 0xffff0000u;
-        const float s = __uint_as_float(s_bits);
         uint32_t out[4];  // the 16 codes: 4 bits in the first half
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (s > 0.0f) kv_codes(w[i][j], lo, s, c);
-            if constexpr (BITS == 4) {
-                // (only the low byte of each sum matters, and its halves do not meet)
-                out[j] = low_bytes(c[0] + (c[1] << 4), c[2] + (c[3] << 4), c[4] + (c[5] << 4), c[6] + (c[7] << 4));
-            } else {
-                out[2 * j] = low_bytes(c[0], c[1], c[2], c[3]);
-                out[2 * j + 1] = low_bytes(c[4], c[5], c[6], c[7]);
-            }
-        }
+        const uint32_t param = row_codes<BITS>(w[i][0], w[i][1], ends, out);
         uint8_t* dst = p.cache.codes + index * (D * BITS / 8) + lane * (kKvChannels * BITS / 8);
         if constexpr (BITS == 4)
             *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
         else
             *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (lane == 0) p.cache.params[index] = (s_bits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+        if (lane == 0) p.cache.params[index] = param;
+    }
+}
+
+struct KvRotaryParams {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    uint16_t* q_out;
+    int64_t q_out_stride;
+    RotaryTable table;
+    int q_heads;
+    int heads;  // of a token: q_heads, then the cache's
+    uint32_t rows;  // T x heads
+};
+
+// A group of D / 16 lanes takes one query head of a token, or the key and the value
+// of a cache head.
+template <int D, int BITS, bool INTERLEAVED>
+__global__ void __launch_bounds__(kKvThreads) kv_store_rotary_kernel(const KvRotaryParams r, const KvMoveParams p) {
+    constexpr int kLanes = D / kKvChannels;
+    const int lane = threadIdx.x % kLanes;
+    const uint32_t row = blockIdx.x * (kKvThreads / kLanes) + threadIdx.x / kLanes;
+    const bool there = row < r.rows;
+    const uint32_t t = there ? row / (uint32_t)r.heads : 0;
+    const int head = there ? (int)(row - t * (uint32_t)r.heads) : 0;
+    const int h = head - r.q_heads;  // < 0: a query
+    const RotaryChunks<4, INTERLEAVED> at(lane, D, r.table.rot);
+    pdl_wait();
+    uint32_t w[kKvRows][2][4] = {};
+    int64_t slot = -1;
+    auto load = [&](const uint16_t* src, uint32_t (&x)[2][4]) {
+        const uint4 a = *(reinterpret_cast<const uint4*>(src) + at.a), b = *(reinterpret_cast<const uint4*>(src) + at.b);
+        x[0][0] = a.x, x[0][1] = a.y, x[0][2] = a.z, x[0][3] = a.w;
+        x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
+    };
+    auto word4 = [](const uint32_t (&x)[4]) { return make_uint4(x[0], x[1], x[2], x[3]); };
+    if (there) {
+        if (h < 0) {
+            load(r.q + t * r.q_stride + (int64_t)head * D, w[0]);
+        } else {
+            load(r.k + t * r.k_stride + (int64_t)h * D, w[0]);
+            load(r.v + t * r.v_stride + (int64_t)h * D, w[1]);
+            slot = __ldg(p.slots + t);
+        }
+        const float* angles = rotary_row(r.table, t, p.err);
+        if (angles != nullptr && at.angle >= 0) {
+            RotaryAngles<4, INTERLEAVED> angle;
+            angle.load(angles, r.table.rot, at, false);
+            angle.turn(w[0][0], w[0][1], at.b_turned);
+        }
+        if (h < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)head * D);
+            dst[at.a] = word4(w[0][0]);
+            dst[at.b] = word4(w[0][1]);
+        }
+    }
+    KvMoveRow place = {there && h >= 0, t, (uint32_t)max(h, 0)};
+    const int64_t key = cache_row(p, place, slot);
+#pragma unroll
+    for (int i = 0; i < kKvRows; ++i) {
+        const uint4 a = word4(w[i][0]), b = word4(w[i][1]);
+        const uint32_t ends = row_ends<kLanes>(a, b);
+        if (key < 0) continue;
+        const int64_t index = i ? key + value_rows(p.cache) : key;
+        uint32_t out[4];
+        const uint32_t param = row_codes<BITS>(a, b, ends, out);
+        uint8_t* dst = p.cache.codes + index * (D * BITS / 8);
+        if constexpr (BITS == 4) {
+            reinterpret_cast<uint32_t*>(dst)[at.a] = out[0];
+            reinterpret_cast<uint32_t*>(dst)[at.b] = out[1];
+        } else {
+            reinterpret_cast<uint2*>(dst)[at.a] = make_uint2(out[0], out[1]);
+            reinterpret_cast<uint2*>(dst)[at.b] = make_uint2(out[2], out[3]);
+        }
+        if (lane == 0) p.cache.params[index] = param;
     }
 }
 
@@ -335,6 +427,25 @@ cudaError_t launch_kv_load(const KvCache& cache, const int64_t* slots, uint16_t*
     auto kernel = D == 64 ? (bits == 4 ? kv_load_kernel<64, 4> : kv_load_kernel<64, 8>)
                           : (bits == 4 ? kv_load_kernel<128, 4> : kv_load_kernel<128, 8>);
     return launch_kernel(kernel, move_grid(p.rows, D), dim3(kKvThreads), 0, env.stream, kNoCluster, k, v, p);
+}
+
+cudaError_t launch_kv_store_rotary(const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                                   const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                                   const RotaryTable& table, bool interleaved, const int64_t* slots,
+                                   const KvCache& cache, int64_t T, int64_t q_heads, int64_t D, int64_t bits,
+                                   const LaunchEnv& env) {
+    const KvMoveParams p = move_params(cache, slots, T, env);
+    KvRotaryParams r = {q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, table, (int)q_heads,
+                        (int)q_heads + cache.H, 0};
+    r.rows = (uint32_t)(T * r.heads);
+    auto pick = [&](auto narrow4, auto narrow8, auto wide4, auto wide8) {
+        return D == 64 ? (bits == 4 ? narrow4 : narrow8) : (bits == 4 ? wide4 : wide8);
+    };
+    auto kernel = interleaved ? pick(kv_store_rotary_kernel<64, 4, true>, kv_store_rotary_kernel<64, 8, true>,
+                                     kv_store_rotary_kernel<128, 4, true>, kv_store_rotary_kernel<128, 8, true>)
+                              : pick(kv_store_rotary_kernel<64, 4, false>, kv_store_rotary_kernel<64, 8, false>,
+                                     kv_store_rotary_kernel<128, 4, false>, kv_store_rotary_kernel<128, 8, false>);
+    return launch_kernel(kernel, move_grid(r.rows, D), dim3(kKvThreads), 0, env.stream, kNoCluster, r, p);
 }
 
 }  // namespace i8ql

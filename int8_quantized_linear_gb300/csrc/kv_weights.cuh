@@ -1,0 +1,52 @@
+// Attention weights summed per cached token, and eviction by them: what their
+// kernels share.
+#pragma once
+
+#include "kv_schedule.cuh"
+
+namespace i8ql {
+
+struct KvWeightsParams {
+    KvAttnParams a;         // (out and the parts of its join unused)
+    int64_t max_q;          // the most query tokens a sequence may have
+    const float* previous;  // [pages][H][P]; null: nothing yet
+    float* weights;         // the same layout; may be `previous`
+    float2* stats;          // [T_q * Hq][splits]: a row's (maximum, sum) over a part of the tokens
+    int splits;
+    int chunk;              // tiles of a block that sums
+};
+
+struct KvEvictParams {
+    KvCache cache;
+    float* weights;  // [pages][H][P]
+    const int32_t* table;
+    int64_t table_width;
+    const int32_t* kv_lens;
+    const int32_t* new_table;  // `table` itself: in place
+    int64_t new_width;
+    int32_t* new_lens;  // [B]
+    int32_t* kept;      // [B][H][budget]
+    int64_t B;
+    int budget, first, last;
+    int row_bytes;  // of codes
+    int chunks;     // blocks of rows of a sequence's head
+    unsigned* err;
+};
+
+namespace {
+
+// A page of the table, or -1 where it is out of range (which is recorded).
+__device__ __forceinline__ int64_t kv_page(const KvCache& c, const int32_t* table, int64_t i, unsigned* err) {
+    const int64_t page = __ldg(table + i);
+    if (page >= 0 && page < c.pages) return page;
+    record_fault(err, kErrBitBadIndex);
+    return -1;
+}
+
+// Index of a token's weight: token `off` of page `page`, head h.
+__device__ __forceinline__ int64_t kv_weight(const KvCache& c, int64_t page, int h, int off) {
+    return ((page * c.H + h) << c.page_shift) + off;
+}
+
+}  // namespace
+}  // namespace i8ql
