@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libi8ql.so")
 SOURCES = ["capi.cu", "quant.cu", "decode_gemm.cu", "w8a8.cu", "w8a8_fused.cu", "noalloc.cu", "fp8_gemm.cu", "w4a16.cu", "moe.cu",
-           "kv_cache.cu", "kv_attention.cu", "kv_prompt.cu", "rotary.cu", "kv_weights.cu", "kv_evict.cu"]
+           "kv_cache.cu", "kv_attention.cu", "kv_prompt.cu", "rotary.cu", "kv_weights.cu", "kv_weights_many.cu", "kv_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

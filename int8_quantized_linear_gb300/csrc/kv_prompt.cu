@@ -51,7 +51,7 @@
 
 #include <cuda_runtime.h>
 
-#include "kv_math.cuh"
+#include "kv_tc.cuh"
 
 namespace i8ql {
 namespace {
@@ -88,114 +88,7 @@ struct Cfg {
     static constexpr int kSmem = kOffRawV + kRawV + 1024;  // (aligned to 1024 by hand)
 };
 
-// MMAs and commits of the lane with issue != 0.  The others run along: in a
-// branch of one lane the descriptors could not stay in uniform registers.
-template <int A_AT, int B_AT>
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t issue) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 ta, tb;\n\t.reg .b64 da, db;\n\t"
-        "add.u32 ta, %1, %7;\n\t"
-        "add.u32 tb, %2, %8;\n\t"
-        "mov.b64 da, {ta, %3};\n\t"
-        "mov.b64 db, {tb, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(issue), "n"(A_AT), "n"(B_AT)
-        : "memory");
-}
-
-template <int A_AT, int B_AT>
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t high, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t issue) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 ta, tb;\n\t.reg .b64 db;\n\t"
-        "add.u32 ta, %1, %7;\n\t"
-        "add.u32 tb, %2, %8;\n\t"
-        "mov.b64 db, {tb, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(issue), "n"(A_AT), "n"(B_AT)
-        : "memory");
-}
-
-__device__ __forceinline__ void commit_mma(uint64_t* bar, uint32_t issue) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
-        "r"(issue)
-        : "memory");
-}
-
-#define I8QL_R8(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3]), "=r"((r)[(i) + 4]), \
-                      "=r"((r)[(i) + 5]), "=r"((r)[(i) + 6]), "=r"((r)[(i) + 7])
-#define I8QL_W8(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3]), "r"((r)[(i) + 4]), \
-                      "r"((r)[(i) + 5]), "r"((r)[(i) + 6]), "r"((r)[(i) + 7])
-
-// 32 columns of this warp's lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : I8QL_R8(r, 0), I8QL_R8(r, 8), I8QL_R8(r, 16), I8QL_R8(r, 24)
-        : "r"(addr));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        I8QL_W8(r, 0), I8QL_W8(r, 8), I8QL_W8(r, 16), I8QL_W8(r, 24)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            addr),
-        I8QL_W8(r, 0), I8QL_W8(r, 8)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ void unpack_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kUnpackWarps * 32) : "memory"); }
-
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
-    return pair_u32(__float_as_uint(a), __float_as_uint(b));
-}
-__device__ __forceinline__ void split_f32(uint64_t p, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // Exponents of a tile, for the softmax.
 struct TileInfo {

@@ -399,15 +399,18 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
 }  // namespace
 
 size_t kv_weights_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
+    if (max_q * G > kKvWeightsFewRows) return kv_weights_many_workspace(B, T_q, G, H, max_kv, max_q, sms);
     return (size_t)(T_q * G * H) * (size_t)weights_plan(B, G, H, max_kv, max_q, sms).splits * sizeof(float2);
 }
 
 bool kv_weights_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
+    if (max_q * G > kKvWeightsFewRows) return kv_weights_many_fits(B, G, H, max_kv, max_q, sms);
     const WeightsPlan w = weights_plan(B, G, H, max_kv, max_q, sms);
     return w.stats_blocks < kMaxRows && w.sum_blocks < kMaxRows;
 }
 
 cudaError_t launch_kv_weights(KvWeightsParams p, int64_t D, int64_t bits, void* workspace, const LaunchEnv& env) {
+    if (p.max_q * p.a.G > kKvWeightsFewRows) return launch_kv_weights_many(p, D, bits, workspace, env);
     const WeightsPlan w =
         weights_plan(p.a.B, p.a.G, p.a.cache.H, p.a.table_width << p.a.cache.page_shift, p.max_q, env.sm_count);
     p.stats = static_cast<float2*>(workspace);

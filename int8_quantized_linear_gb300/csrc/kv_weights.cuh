@@ -14,7 +14,19 @@ struct KvWeightsParams {
     float2* stats;          // [T_q * Hq][splits]: a row's (maximum, sum) over a part of the tokens
     int splits;
     int chunk;              // tiles of a block that sums
+    // many query rows only:
+    int chunks;             // blocks of the tiles
+    int groups;             // of row blocks that are summed together
+    float* parts;           // [B][H][groups][2][part_stride]: sums over a group's rows, by halves of the row blocks
+    int64_t part_stride;    // tokens of a table row, in whole tiles
 };
+
+// Query rows of a cache head from which the kernels for many of them (kv_weights_many.cu)
+// take over.
+constexpr int64_t kKvWeightsFewRows = 32;
+size_t kv_weights_many_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
+bool kv_weights_many_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
+cudaError_t launch_kv_weights_many(KvWeightsParams p, int64_t D, int64_t bits, void* workspace, const LaunchEnv& env);
 
 struct KvEvictParams {
     KvCache cache;
