@@ -166,15 +166,13 @@ __device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, const flo
         if (EDGE) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = token + j + k <= hi && token + j + k >= lo ? v[k] : -INFINITY;
-            a = pair_f32(v[0], v[1]);
-            b = pair_f32(v[2], v[3]);
         }
         high[0] = max3(high[0], v[0], v[1]);
         high[1] = max3(high[1], v[2], v[3]);
         y[j / 2] = a;
         y[j / 2 + 1] = b;
     }
-    const float top = fmaxf(high[0], high[1]) * unit;  // (unit > 0; -inf stays so)
+    const float top = fmaxf(high[0], high[1]) * unit;  // (unit >= 0; no number for nothing seen at unit 0)
     if (__any_sync(0xffffffffu, top > r.ref + kSlack)) {
         if (top > r.ref + kSlack) {
             r.sum *= exp2_approx(r.ref - top);
@@ -188,7 +186,14 @@ __device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, const flo
     for (int j = 0; j < 16; ++j) {
         float a, b;
         split_f32(fma_f32x2(y[j], u2, shift2), a, b);
-        sum[j & 1] = add_f32x2(sum[j & 1], pair_f32(exp2_approx(a), exp2_approx(b)));
+        a = exp2_approx(a);
+        b = exp2_approx(b);
+        if (EDGE) {
+            const int tok = token + 2 * j;
+            a = tok <= hi && tok >= lo ? a : 0.0f;
+            b = tok + 1 <= hi && tok + 1 >= lo ? b : 0.0f;
+        }
+        sum[j & 1] = add_f32x2(sum[j & 1], pair_f32(a, b));
     }
     float a, b;
     split_f32(add_f32x2(sum[0], sum[1]), a, b);
