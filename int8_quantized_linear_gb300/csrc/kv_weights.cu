@@ -4,12 +4,17 @@
 //   a_ij = c * sum_d q_id k_jd   (c = softmax scale * log2 e, j over the tokens that row i sees)
 //   w_j  = previous_j + sum_i 2^(a_ij - m_i) / l_i,   m_i = max_j a_ij, l_i = sum_j 2^(a_ij - m_i)
 // over the query rows of a cache head (its group's heads, all query tokens).
-// As in the attention kernels k_jd = low_j + s_j code_jd, the products run on
-// centred codes in fp16 (exact: q is scaled by a power of two per row, elements
-// 2^32 below its largest round), and the scales are applied outside:
-//   sum_d q_d k_jd = s_j sum_d q_d c_jd + (low_j + z s_j) sum_d q_d.
-// Logits, maxima and sums are fp32.  Maximum and sum are kept apart (2^(a - m) / l, not
-// 2^(a - m - log2 l)): beside a large m the logarithm would lose its bits.
+// With k_jd = low_j + s_j code_jd the products run on the codes themselves, and the
+// scales are applied outside:
+//   sum_d q_d k_jd = s_j sum_d q_d code_jd + low_j sum_d q_d.
+// A code is an fp16 number as it lies: the integer c in the low bits of a half is
+// 2^-24 c (subnormal, exact), and a nibble one place up 2^-24 16 c, which the query's
+// element makes up for by a 16th.  So unpacking is masks alone, five instructions for
+// eight 4-bit codes (and nine to make centred integers of them: see kv_math.cuh).
+// q is scaled by a power of two per row that brings its largest element to 2^14;
+// elements 2^-28 of that round.  Logits, maxima and sums are fp32.  Maximum and sum are
+// kept apart (2^(a - m) / l, not 2^(a - m - log2 l)): beside a large m the logarithm
+// would lose its bits.
 //
 // A weight needs its row's maximum and sum, which need all keys: two kernels
 // that both go over the keys.  The first leaves each row's (m, l) over a part of
@@ -23,17 +28,26 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
-#include "kv_math.cuh"
+#include "kv_tc.cuh"
 #include "kv_weights.cuh"
 
 namespace i8ql {
 namespace {
 
+// The two kernels:
 constexpr int kTile = 128;   // tokens a block works on at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 8;    // most tiles of a block of the second kernel
+template <int D, int BITS>
+constexpr int kStages = D * BITS == 128 * 8 ? 3 : 4;
+// All in one:
+constexpr int kOneTile = 256;
+constexpr int kOneWarps = 8;
+constexpr int kOneThreads = kOneWarps * 32;
+constexpr int kOneStages = 2;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -58,8 +72,8 @@ template <int D, int BITS, int HALVES>
 struct Queries {
     uint32_t f[D / 16][HALVES][2];  // B operand: rows g + 8 x, permuted as the keys' unpacking pairs channels
     // of rows 2t + y + 8 x, whose logits the lane holds:
-    float sum[HALVES][2];          // the scaled row's sum
-    float unit[HALVES][2];         // what a scaled logit counts, in log2 units
+    float sum[HALVES][2];          // the scaled row's sum, times 2^-24
+    float unit[HALVES][2];         // what a product counts, in log2 units
     int hi[HALVES][2], lo[HALVES][2];  // the tokens the row sees: lo .. hi (none: hi < lo)
 
     __device__ __forceinline__ void load(const KvAttnParams& p, const KvSeq& seq, int h, int row0, int rows) {
@@ -87,8 +101,8 @@ struct Queries {
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = max((int)(top >> 23), 9) - 127;
-            const float by = p.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
+            const int e = max((int)(top >> 23), 15) - 127;
+            const float by = p.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
             float total = 0.0f;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
@@ -99,9 +113,9 @@ struct Queries {
                 uint32_t (&f0)[2] = f[2 * w][x], (&f1)[2] = f[2 * w + 1][x];
                 if constexpr (BITS == 4) {  // 8 channels: (0,4) (1,5) | (2,6) (3,7)
                     f0[0] = pack_f16(y[0], y[4]);
-                    f0[1] = pack_f16(y[1], y[5]);
+                    f0[1] = pack_f16(y[1] * 0.0625f, y[5] * 0.0625f);
                     f1[0] = pack_f16(y[2], y[6]);
-                    f1[1] = pack_f16(y[3], y[7]);
+                    f1[1] = pack_f16(y[3] * 0.0625f, y[7] * 0.0625f);
                 } else {  // twice 4 channels: (0,1) (2,3)
                     f0[0] = pack_f16(y[0], y[1]);
                     f0[1] = pack_f16(y[2], y[3]);
@@ -111,7 +125,9 @@ struct Queries {
             }
             total += __shfl_xor_sync(0xffffffffu, total, 1);
             total += __shfl_xor_sync(0xffffffffu, total, 2);
-            const float u = pow2(e - 8) * fabsf(p.scale_log2);
+            // (not 0: what is not seen, -inf, times 0 would be no number)
+            const float u = fmaxf(pow2(e - 14) * (fabsf(p.scale_log2) * 0x1p24f), 0x1p-126f);
+            total *= 0x1p-24f;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int from = 4 * (2 * t + y);  // a lane that loaded row 2t + y
@@ -133,39 +149,9 @@ struct Keys {
     uint32_t w[4][kWords];
     uint32_t param[4];
 
-    // Pages of the tile's tokens; token 0's for those outside begin .. end (not read from).
-    static __device__ __forceinline__ void pages(const KvAttnParams& p, const int32_t* table, int token, int begin,
-                                                 int end, int (&page)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = token + 8 * i;
-            page[i] = j >= begin && j < end ? __ldg(table + (j >> p.cache.page_shift)) : -1;
-        }
-    }
-
-    __device__ __forceinline__ void load(const KvAttnParams& p, int h, int token, int begin, int end, const int (&page)[4]) {
-        const int t = threadIdx.x % 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = token + 8 * i;
-            param[i] = 0;
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) w[i][k] = 0;
-            if (j < begin || j >= end) continue;
-            int64_t at = page[i];
-            if (at < 0 || at >= p.cache.pages) {
-                record_fault(p.err, kErrBitBadIndex);
-                at = 0;
-            }
-            const int64_t row = kv_row(p.cache, at, 0, h, j & ((1 << p.cache.page_shift) - 1));
-            lds<kWords>(p.cache.codes + row * (D * BITS / 8) + t * (kWords * 4), w[i]);
-            param[i] = p.cache.params[row];
-        }
-    }
-
-    // Logits in log2 units of tokens g + 16 i (+ 8) and rows 2t, 2t + 1 (+ 8 x); -inf where
-    // a row does not see a token.
-    template <int HALVES>
+    // Logits, in units of their rows, of tokens g + 16 i (+ 8) and rows 2t, 2t + 1 (+ 8 x).
+    // EDGE: some row does not see some token: -inf there.
+    template <bool EDGE, int HALVES>
     __device__ __forceinline__ void logits(const Queries<D, BITS, HALVES>& q, int token, float (&s)[2][HALVES][4]) const {
         constexpr int kPairs = 16 / BITS;
 #pragma unroll
@@ -177,8 +163,8 @@ struct Keys {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a[kPairs], b[kPairs];
-                unpack_key<BITS, true>(w[2 * i][k], a);
-                unpack_key<BITS, true>(w[2 * i + 1][k], b);
+                kv_small_codes<BITS>(w[2 * i][k], a);
+                kv_small_codes<BITS>(w[2 * i + 1][k], b);
 #pragma unroll
                 for (int j = 0; j < kPairs; j += 2)
 #pragma unroll
@@ -191,29 +177,376 @@ struct Keys {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                const uint32_t pk = param[2 * i + z];
-                const float scale = kv_scale(pk), off = fmaf(scale, kCentre<BITS>, kv_low(pk));
+                const float scale = kv_scale(param[2 * i + z]), low = kv_low(param[2 * i + z]);
                 const int j = token + 16 * i + 8 * z;
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float a = fmaf(scale, s[i][x][2 * z + y], off * q.sum[x][y]) * q.unit[x][y];
-                        s[i][x][2 * z + y] = j >= q.lo[x][y] && j <= q.hi[x][y] ? a : -INFINITY;
+                        float& v = s[i][x][2 * z + y];
+                        v = fmaf(scale, v, low * q.sum[x][y]);
+                        if (EDGE) v = j >= q.lo[x][y] && j <= q.hi[x][y] ? v : -INFINITY;
                     }
             }
+    }
+
+    // The same in log2 units.
+    template <int HALVES>
+    __device__ __forceinline__ void scaled_logits(const Queries<D, BITS, HALVES>& q, int token, float (&s)[2][HALVES][4]) const {
+        logits<true>(q, token, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s[i][x][y] *= q.unit[x][y % 2];
+    }
+};
+
+// A warp's tokens on their way: a ring of STAGES steps of 32 tokens, WARPS * 32 tokens
+// (the block's tile) apart, each lane copying (cp.async) what it will itself unpack, and one token's scale
+// and low value, so that no barrier beyond the warp is needed and no register waits
+// for memory.  Pages are looked up a step before they are copied from.
+template <int D, int BITS, int WARPS, int STAGES>
+struct KeyRing {
+    static constexpr int kLaneBytes = D * BITS / 32;  // of a row: a quarter
+    static constexpr int kStageBytes = 32 * 4 * kLaneBytes + 32 * 4;
+    static constexpr int kBytes = WARPS * STAGES * kStageBytes;
+
+    const KvAttnParams& p;
+    const int32_t* table;
+    uint8_t* mine;          // this warp's part
+    const uint8_t* codes;   // this lane's part of page 0's first rows of the head, and its parameter
+    const uint32_t* params;
+    int begin, end;
+    int next, last;  // the warp's next step's first token; tokens from `last` on are not wanted
+    int page[2];     // of the next step's two groups of 16 tokens
+    int put, get;    // stages
+
+    __device__ __forceinline__ int page_of(int token) const {
+        // (a group may begin before `begin`, but lies in one page)
+        return token < last && token < end && token + 16 > begin ? __ldg(table + (token >> p.cache.page_shift)) : -1;
+    }
+
+    // Tiles t0 .. t1 - 1; tokens outside begin .. end come as zeros.
+    __device__ __forceinline__ KeyRing(const KvAttnParams& p, const int32_t* table, uint8_t* ring, int h, int t0, int t1,
+                                       int begin, int end)
+        : p(p), table(table), begin(begin), end(end), put(0), get(0) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        mine = ring + warp * (STAGES * kStageBytes);
+        const int64_t row = (int64_t)h << p.cache.page_shift;
+        codes = p.cache.codes + (row + lane / 4) * (D * BITS / 8) + lane % 4 * kLaneBytes;
+        params = p.cache.params + row + lane % 16;
+        next = t0 * (WARPS * 32) + warp * 32;
+        last = t1 * (WARPS * 32);
+        page[0] = page_of(next);
+        page[1] = page_of(next + 16);
+#pragma unroll 1
+        for (int i = 0; i < STAGES - 1; ++i) issue();
+    }
+
+    __device__ __forceinline__ static void copy(uint32_t dst, const void* src, bool there) {
+        // (not there: zeros, nothing is read)
+        constexpr int kSize = kLaneBytes < 16 ? kLaneBytes : 16;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kSize), "r"(there ? kSize : 0)
+                     : "memory");
+    }
+
+    __device__ __forceinline__ void issue() {
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        if (next < last) {
+            constexpr int kRow = D * BITS / 8;
+            const int mask = (1 << p.cache.page_shift) - 1;
+            const uint32_t stage = tc::smem_u32(mine) + put * kStageBytes;
+            const bool all = next >= begin && next + 32 <= end;  // every token is wanted
+            int64_t at[2];  // rows from page 0's
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int token = next + 16 * i;
+                if ((uint32_t)page[i] >= (uint64_t)p.cache.pages) {
+                    if (token < end && token + 16 > begin) record_fault(p.err, kErrBitBadIndex);
+                    page[i] = 0;
+                }
+                at[i] = ((int64_t)page[i] * (2 * p.cache.H) << p.cache.page_shift) + (token & mask);
+            }
+            auto wanted = [&](int token) { return all || (token >= begin && token < end); };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* src = codes + at[i / 2] * kRow + (i % 2) * (8 * kRow);
+                const bool there = wanted(next + 8 * i + g);
+                if constexpr (kLaneBytes == 32) {
+                    // (16 bytes of all lanes, then the other 16: banks)
+                    const uint32_t dst = stage + i * 32 * kLaneBytes + lane * 16;
+                    copy(dst, src, there);
+                    copy(dst + 512, src + 16, there);
+                } else {
+                    copy(stage + (i * 32 + lane) * kLaneBytes, src, there);
+                }
+            }
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stage + 128 * kLaneBytes + lane * 4),
+                         "l"(params + (lane < 16 ? at[0] : at[1])), "r"(wanted(next + lane) ? 4 : 0)
+                         : "memory");
+            next += (WARPS * 32);
+            page[0] = page_of(next);
+            page[1] = page_of(next + 16);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put = put + 1 == STAGES ? 0 : put + 1;
+    }
+
+    // The oldest step; the next one goes on its way.
+    __device__ __forceinline__ void take(Keys<D, BITS>& k) {
+        constexpr int kWords = Keys<D, BITS>::kWords;
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();  // the other lanes' scales; and all lanes are done with the step before
+        issue();
+        const uint8_t* stage = mine + get * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kLaneBytes == 32) {
+                uint32_t a[4], b[4];
+                lds<4>(stage + i * 32 * kLaneBytes + lane * 16, a);
+                lds<4>(stage + i * 32 * kLaneBytes + lane * 16 + 512, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    k.w[i][j] = a[j];
+                    k.w[i][4 + j] = b[j];
+                }
+            } else {
+                lds<kWords>(stage + (i * 32 + lane) * kLaneBytes, k.w[i]);
+            }
+            k.param[i] = *reinterpret_cast<const uint32_t*>(stage + 128 * kLaneBytes + (g + 8 * i) * 4);
+        }
+        get = get + 1 == STAGES ? 0 : get + 1;
     }
 };
 
 // 2^(a - m), 0 where a is -inf (and m too).
 __device__ __forceinline__ float weight_of(float a, float m) { return exp2_approx(a - (m == -INFINITY ? 0.0f : m)); }
 
+// (m, l) over two sets of tokens.
+__device__ __forceinline__ void join_stats(float& m, float& l, float om, float ol) {
+    const float to = fmaxf(m, om);
+    l = l * weight_of(m, to) + ol * weight_of(om, to);
+    m = to;
+}
+
+// Adds a step's logits to a lane's (m, l).
+template <int HALVES>
+__device__ __forceinline__ void add_logits(float (&m)[HALVES][2], float (&l)[HALVES][2], const float (&s)[2][HALVES][4]) {
+#pragma unroll
+    for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const float top = fmaxf(fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y]));
+            const float to = fmaxf(m[x][y], top);
+            const float sum = (weight_of(s[0][x][y], to) + weight_of(s[0][x][2 + y], to)) +
+                              (weight_of(s[1][x][y], to) + weight_of(s[1][x][2 + y], to));
+            l[x][y] = fmaf(l[x][y], weight_of(m[x][y], to), sum);
+            m[x][y] = to;
+        }
+}
+
+// The lanes' (m, l) of a warp, into part[row].
+template <int HALVES>
+__device__ __forceinline__ void warp_stats(float (&m)[HALVES][2], float (&l)[HALVES][2], float2* part) {
+    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                join_stats(m[x][y], l[x][y], __shfl_xor_sync(0xffffffffu, m[x][y], d),
+                           __shfl_xor_sync(0xffffffffu, l[x][y], d));
+            if (g == 0) part[8 * x + 2 * t + y] = make_float2(m[x][y], l[x][y]);
+        }
+}
+
+// All in one, while a cluster's shared memory holds the logits: a cluster takes one
+// cache head of one sequence, each CTA a part of its tiles.  Keys are read once:
+// logits stay in shared memory, the CTAs exchange each row's (m, l), and the
+// weights are summed from there.
+template <int D, int BITS, int HALVES>
+__global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsParams p) {
+    constexpr int ROWS = 8 * HALVES;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float part[kOneWarps][ROWS];         // a warp's maxima, then its sums
+    __shared__ float units[ROWS];
+    __shared__ __align__(16) float2 mine[ROWS];  // this CTA's (m, l)
+    __shared__ __align__(8) float factors[ROWS];              // of this CTA's weights: 2^(its m - m) / l
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int size = p.splits, rank = (int)tc::cluster_rank();
+    const int64_t item = blockIdx.x / size;
+    const int64_t b = item / p.a.cache.H;
+    const int h = (int)(item - b * p.a.cache.H);
+    pdl_wait();
+    const KvSeq seq = weights_sequence(p, b);
+    if (seq.nq == 0) return;  // (the whole cluster)
+    const KvSpan span = kv_span<ROWS, kOneTile>(p.a, seq, 0);
+    const int rows = min(ROWS, seq.nq * p.a.G);
+    const int tile0 = span.first + (int)((int64_t)span.tiles * rank / size);
+    const int tile1 = span.first + (int)((int64_t)span.tiles * (rank + 1) / size);
+    const int32_t* table = p.a.table + b * p.a.table_width;
+    // [pairs of rows][tokens]; 8 more tokens keep a warp's stores off each other's banks
+    float2* logits = reinterpret_cast<float2*>(smem + KeyRing<D, BITS, kOneWarps, kOneStages>::kBytes);
+    const int stride = p.chunk * kOneTile + 8, tokens = (tile1 - tile0) * kOneTile;
+    // the products
+    {
+        float top[HALVES][2];
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x) top[x][0] = top[x][1] = -INFINITY;
+        KeyRing<D, BITS, kOneWarps, kOneStages> ring(p.a, table, smem, h, tile0, tile1, span.begin, span.end);
+        Queries<D, BITS, HALVES> q;
+        q.load(p.a, seq, h, 0, rows);
+        // tokens [all_lo, all_hi] are seen by every row
+        const int base = seq.len - seq.nq, all_hi = base;
+        const int all_lo = p.a.window > 0 ? (int)max(base + (rows - 1) / p.a.G + 1 - p.a.window, (int64_t)0) : 0;
+        if (warp == 0 && g == 0) {
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) units[8 * x + 2 * t + y] = q.unit[x][y];
+        }
+        int token = tile0 * kOneTile + warp * 32 + g;
+        float2* to = logits + t * stride + warp * 32 + g;
+        auto step = [&](auto edge) {
+            Keys<D, BITS> now;
+            ring.take(now);
+            float s[2][HALVES][4];
+            now.template logits<decltype(edge)::value>(q, token, s);
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x) {
+                if (8 * x + 2 * t < rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        to[4 * x * stride + 8 * k] = make_float2(s[k / 2][x][2 * (k % 2)], s[k / 2][x][2 * (k % 2) + 1]);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    top[x][y] = max3(top[x][y], s[0][x][y], s[0][x][2 + y]);
+                    top[x][y] = max3(top[x][y], s[1][x][y], s[1][x][2 + y]);
+                }
+            }
+        };
+#pragma unroll 1
+        for (int i = tile0; i < tile1; ++i, token += kOneTile, to += kOneTile) {
+            const int first = i * kOneTile;
+            if (first >= all_lo && first + kOneTile - 1 <= all_hi)
+                step(std::false_type{});
+            else
+                step(std::true_type{});
+        }
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) top[x][y] = fmaxf(top[x][y], __shfl_xor_sync(0xffffffffu, top[x][y], d));
+                if (g == 0) part[warp][8 * x + 2 * t + y] = top[x][y];
+            }
+    }
+    __syncthreads();
+    // weights relative to this CTA's maxima, and their sums; a pair of rows at a time
+    if (threadIdx.x < ROWS) {
+        float m = part[0][threadIdx.x];
+        for (int w = 1; w < kOneWarps; ++w) m = fmaxf(m, part[w][threadIdx.x]);
+        m = threadIdx.x < rows ? m * units[threadIdx.x] : 0.0f;
+        mine[threadIdx.x].x = m;
+    }
+    __syncthreads();
+    for (int r = 0; 2 * r < rows; ++r) {
+        const float u0 = units[2 * r], u1 = units[2 * r + 1];
+        const float m0 = mine[2 * r].x == -INFINITY ? 0.0f : -mine[2 * r].x;
+        const float m1 = mine[2 * r + 1].x == -INFINITY ? 0.0f : -mine[2 * r + 1].x;
+        float l0 = 0.0f, l1 = 0.0f;
+        float4* a = reinterpret_cast<float4*>(logits + r * stride);  // two tokens at a time
+#pragma unroll 4
+        for (int i = threadIdx.x; i < tokens / 2; i += kOneThreads) {
+            const float4 v = a[i];
+            const float4 e = make_float4(exp2_approx(fmaf(v.x, u0, m0)), exp2_approx(fmaf(v.y, u1, m1)),
+                                         exp2_approx(fmaf(v.z, u0, m0)), exp2_approx(fmaf(v.w, u1, m1)));
+            a[i] = e;
+            l0 += e.x + e.z;
+            l1 += e.y + e.w;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+        }
+        if (lane == 0) {
+            part[warp][2 * r] = l0;
+            part[warp][2 * r + 1] = l1;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        float l = 0.0f;
+        for (int w = 0; w < kOneWarps; ++w) l += part[w][threadIdx.x];
+        mine[threadIdx.x].y = l;
+    }
+    tc::cluster_sync_all();
+    if (threadIdx.x < ROWS) {
+        float rm = -INFINITY, rl = 0.0f;
+        if (threadIdx.x < rows)
+            for (int c = 0; c < size; ++c) {
+                float om, ol;
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(om), "=f"(ol)
+                             : "r"(tc::mapa(tc::smem_u32(&mine[threadIdx.x]), c))
+                             : "memory");
+                join_stats(rm, rl, om, ol);
+            }
+        factors[threadIdx.x] = rl > 0.0f ? weight_of(mine[threadIdx.x].x, rm) / rl : 0.0f;
+    }
+    __syncthreads();
+    // (no CTA leaves while another reads its part)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // four tokens a thread at a time, which lie in one page
+    const int mask = (1 << p.a.cache.page_shift) - 1, older = p.previous != nullptr ? seq.len - seq.nq : 0;
+    for (int i = threadIdx.x * 4; i < tokens; i += 4 * kOneThreads) {
+        const int j = tile0 * kOneTile + i;
+        if (j + 4 <= span.begin || j >= span.end) continue;
+        const int64_t page = kv_page(p.a.cache, table, j >> p.a.cache.page_shift, p.a.err);
+        if (page < 0) continue;
+        const int64_t to = kv_weight(p.a.cache, page, h, j & mask);
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < older) w = *reinterpret_cast<const float4*>(p.previous + to);
+        if (j + 1 >= older) w.y = 0.0f;
+        if (j + 2 >= older) w.z = 0.0f;
+        if (j + 3 >= older) w.w = 0.0f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; 2 * r < rows; ++r) {
+            const float4 a = *reinterpret_cast<const float4*>(logits + r * stride + i);
+            const float4 c = *reinterpret_cast<const float4*>(logits + r * stride + i + 2);
+            const float2 f = *reinterpret_cast<const float2*>(factors + 2 * r);
+            sum.x = fmaf(a.y, f.y, fmaf(a.x, f.x, sum.x));
+            sum.y = fmaf(a.w, f.y, fmaf(a.z, f.x, sum.y));
+            sum.z = fmaf(c.y, f.y, fmaf(c.x, f.x, sum.z));
+            sum.w = fmaf(c.w, f.y, fmaf(c.z, f.x, sum.w));
+        }
+        w = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+        if (j >= span.begin && j + 4 <= span.end) {
+            *reinterpret_cast<float4*>(p.weights + to) = w;
+        } else {
+            const float v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j + k >= span.begin && j + k < span.end) p.weights[to + k] = v[k];
+        }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // (m, l) over a part of the tokens, for a block of rows.
 template <int D, int BITS, int HALVES>
 __global__ void __launch_bounds__(kThreads) kv_stats_kernel(const KvWeightsParams p) {
     constexpr int ROWS = 8 * HALVES;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 part[kWarps][ROWS];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4;
     // split fastest, then head, so that neighbours share rows and pages
     int64_t at = blockIdx.x;
     const int split = (int)(at % p.splits);
@@ -242,48 +575,21 @@ __global__ void __launch_bounds__(kThreads) kv_stats_kernel(const KvWeightsParam
         q.load(p.a, seq, h, row0, rows);
         const int32_t* table = p.a.table + b * p.a.table_width;
         int token = (span.first + first) * kTile + warp * 32 + g;
-        int page[4];
-        Keys<D, BITS> keys;
-        Keys<D, BITS>::pages(p.a, table, token, span.begin, span.end, page);
-        keys.load(p.a, h, token, span.begin, span.end, page);
-        Keys<D, BITS>::pages(p.a, table, token + kTile, span.begin, span.end, page);
+        KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, span.first + first, span.first + last, span.begin,
+                                                          span.end);
         for (int i = first; i < last; ++i, token += kTile) {
-            Keys<D, BITS> now = keys;
-            if (i + 1 < last) keys.load(p.a, h, token + kTile, span.begin, span.end, page);
-            if (i + 2 < last) Keys<D, BITS>::pages(p.a, table, token + 2 * kTile, span.begin, span.end, page);
+            Keys<D, BITS> now;
+            ring.take(now);
             float s[2][HALVES][4];
-            now.logits(q, token, s);
-#pragma unroll
-            for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float top = fmaxf(fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y]));
-                    const float to = fmaxf(m[x][y], top);
-                    const float sum = (weight_of(s[0][x][y], to) + weight_of(s[0][x][2 + y], to)) +
-                                      (weight_of(s[1][x][y], to) + weight_of(s[1][x][2 + y], to));
-                    l[x][y] = fmaf(l[x][y], weight_of(m[x][y], to), sum);
-                    m[x][y] = to;
-                }
+            now.scaled_logits(q, token, s);
+            add_logits<HALVES>(m, l, s);
         }
     }
-    auto join = [](float& m, float& l, float om, float ol) {
-        const float to = fmaxf(m, om);
-        l = l * weight_of(m, to) + ol * weight_of(om, to);
-        m = to;
-    };
-#pragma unroll
-    for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1)
-                join(m[x][y], l[x][y], __shfl_xor_sync(0xffffffffu, m[x][y], d), __shfl_xor_sync(0xffffffffu, l[x][y], d));
-            if (g == 0) part[warp][8 * x + 2 * t + y] = make_float2(m[x][y], l[x][y]);
-        }
+    warp_stats<HALVES>(m, l, part[warp]);
     __syncthreads();
     if (threadIdx.x < rows) {
         float2 r = part[0][threadIdx.x];
-        for (int w = 1; w < kWarps; ++w) join(r.x, r.y, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
+        for (int w = 1; w < kWarps; ++w) join_stats(r.x, r.y, part[w][threadIdx.x].x, part[w][threadIdx.x].y);
         const int i = (row0 + threadIdx.x) / p.a.G;
         const int64_t row = (seq.q0 + i) * ((int64_t)p.a.G * p.a.cache.H) + h * p.a.G + row0 + threadIdx.x - i * p.a.G;
         p.stats[row * p.splits + split] = r;
@@ -294,6 +600,7 @@ __global__ void __launch_bounds__(kThreads) kv_stats_kernel(const KvWeightsParam
 template <int D, int BITS, int HALVES>
 __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams p) {
     constexpr int ROWS = 8 * HALVES;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sums[kChunk * kTile];
     __shared__ float2 stats[ROWS];  // (m, 1 / l)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -340,17 +647,12 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
 #pragma unroll
             for (int y = 0; y < 2; ++y) st[x][y] = stats[8 * x + 2 * t + y];
         int token = first * kTile + warp * 32 + g;
-        int page[4];
-        Keys<D, BITS> keys;
-        Keys<D, BITS>::pages(p.a, table, token, span.begin, span.end, page);
-        keys.load(p.a, h, token, span.begin, span.end, page);
-        Keys<D, BITS>::pages(p.a, table, token + kTile, span.begin, span.end, page);
+        KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, first, last, span.begin, span.end);
         for (int i = first; i < last; ++i, token += kTile) {
-            Keys<D, BITS> now = keys;
-            if (i + 1 < last) keys.load(p.a, h, token + kTile, span.begin, span.end, page);
-            if (i + 2 < last) Keys<D, BITS>::pages(p.a, table, token + 2 * kTile, span.begin, span.end, page);
+            Keys<D, BITS> now;
+            ring.take(now);
             float s[2][HALVES][4];
-            now.logits(q, token, s);
+            now.scaled_logits(q, token, s);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float sum = 0.0f;
@@ -380,15 +682,33 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
 
 struct WeightsPlan {
     int halves, splits, chunk;
+    bool fused;  // one launch of clusters of `splits` CTAs, of `chunk` tiles at most each
     int64_t stats_blocks, sum_blocks;
+    size_t smem;  // of the logits
 };
 
+// Shared memory of the logits that lets two blocks run on an SM.
+constexpr size_t kMostLogits = 64 * 1024;
+
 WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
-    WeightsPlan w;
+    WeightsPlan w = {};
     const int64_t rows = max_q * G;
     w.halves = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const int64_t blocks = (rows + 8 * w.halves - 1) / (8 * w.halves), tiles = (max_kv + kTile - 1) / kTile;
     const int64_t wanted = 8 * (int64_t)sms, base = std::max<int64_t>(B * H * blocks, 1);
+    const int64_t one_tiles = (max_kv + kOneTile - 1) / kOneTile;
+    for (int64_t size = 1; size <= 8 && blocks == 1; size *= 2) {
+        const int64_t chunk = (one_tiles + size - 1) / size;
+        const size_t smem = (size_t)((rows + 1) / 2) * (size_t)(chunk * kOneTile + 8) * sizeof(float2);
+        if (smem > kMostLogits) continue;
+        if (size < 8 && base * size < wanted && size < one_tiles) continue;
+        w.fused = true;
+        w.splits = (int)size;
+        w.chunk = (int)chunk;
+        w.smem = smem;
+        w.stats_blocks = w.sum_blocks = base * size;
+        return w;
+    }
     w.splits = (int)std::min<int64_t>(std::min<int64_t>(64, tiles), std::max<int64_t>(1, (wanted + base - 1) / base));
     w.chunk = (int)std::min<int64_t>(kChunk, std::max<int64_t>(1, B * H * tiles / wanted));
     w.stats_blocks = B * H * blocks * w.splits;
@@ -396,11 +716,39 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
     return w;
 }
 
+template <int D, int BITS, int HALVES>
+cudaError_t launch_form(const KvWeightsParams& p, const WeightsPlan& w, const LaunchEnv& env) {
+    constexpr int kRing = KeyRing<D, BITS, kWarps, kStages<D, BITS>>::kBytes;
+    if (w.fused) {
+        constexpr int kOneRing = KeyRing<D, BITS, kOneWarps, kOneStages>::kBytes;
+        const cudaError_t e = allow_smem<kv_weigh_kernel<D, BITS, HALVES>>(kOneRing + kMostLogits);
+        if (e != cudaSuccess) return e;
+        return launch_kernel(kv_weigh_kernel<D, BITS, HALVES>, dim3((unsigned)w.stats_blocks), dim3(kOneThreads),
+                             kOneRing + w.smem, env.stream, dim3(w.splits, 1, 1), p);
+    }
+    cudaError_t e = allow_smem<kv_stats_kernel<D, BITS, HALVES>>(kRing);
+    if (e == cudaSuccess) e = allow_smem<kv_sum_kernel<D, BITS, HALVES>>(kRing);
+    if (e == cudaSuccess)
+        e = launch_kernel(kv_stats_kernel<D, BITS, HALVES>, dim3((unsigned)w.stats_blocks), dim3(kThreads), kRing,
+                          env.stream, kNoCluster, p);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kv_sum_kernel<D, BITS, HALVES>, dim3((unsigned)w.sum_blocks), dim3(kThreads), kRing, env.stream,
+                         kNoCluster, p);
+}
+
+template <int D, int BITS>
+cudaError_t launch_rows(const KvWeightsParams& p, const WeightsPlan& w, const LaunchEnv& env) {
+    return w.halves == 1   ? launch_form<D, BITS, 1>(p, w, env)
+           : w.halves == 2 ? launch_form<D, BITS, 2>(p, w, env)
+                           : launch_form<D, BITS, 4>(p, w, env);
+}
+
 }  // namespace
 
 size_t kv_weights_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
     if (max_q * G > kKvWeightsFewRows) return kv_weights_many_workspace(B, T_q, G, H, max_kv, max_q, sms);
-    return (size_t)(T_q * G * H) * (size_t)weights_plan(B, G, H, max_kv, max_q, sms).splits * sizeof(float2);
+    const WeightsPlan w = weights_plan(B, G, H, max_kv, max_q, sms);
+    return w.fused ? 0 : (size_t)(T_q * G * H) * (size_t)w.splits * sizeof(float2);
 }
 
 bool kv_weights_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
@@ -416,20 +764,8 @@ cudaError_t launch_kv_weights(KvWeightsParams p, int64_t D, int64_t bits, void* 
     p.stats = static_cast<float2*>(workspace);
     p.splits = w.splits;
     p.chunk = w.chunk;
-    auto run = [&](auto stats, auto sum) {
-        const cudaError_t e = p.max_q == 0 ? cudaSuccess
-                                           : launch_kernel(stats, dim3((unsigned)w.stats_blocks), dim3(kThreads), 0,
-                                                           env.stream, kNoCluster, p);
-        if (e != cudaSuccess) return e;
-        return launch_kernel(sum, dim3((unsigned)w.sum_blocks), dim3(kThreads), 0, env.stream, kNoCluster, p);
-    };
-#define I8QL_WEIGHTS(D_, B_)                                                                 \
-    (w.halves == 1   ? run(kv_stats_kernel<D_, B_, 1>, kv_sum_kernel<D_, B_, 1>)             \
-     : w.halves == 2 ? run(kv_stats_kernel<D_, B_, 2>, kv_sum_kernel<D_, B_, 2>)             \
-                     : run(kv_stats_kernel<D_, B_, 4>, kv_sum_kernel<D_, B_, 4>))
-    if (D == 64) return bits == 4 ? I8QL_WEIGHTS(64, 4) : I8QL_WEIGHTS(64, 8);
-    return bits == 4 ? I8QL_WEIGHTS(128, 4) : I8QL_WEIGHTS(128, 8);
-#undef I8QL_WEIGHTS
+    if (D == 64) return bits == 4 ? launch_rows<64, 4>(p, w, env) : launch_rows<64, 8>(p, w, env);
+    return bits == 4 ? launch_rows<128, 4>(p, w, env) : launch_rows<128, 8>(p, w, env);
 }
 
 }  // namespace i8ql

@@ -12,8 +12,8 @@ struct KvWeightsParams {
     const float* previous;  // [pages][H][P]; null: nothing yet
     float* weights;         // the same layout; may be `previous`
     float2* stats;          // [T_q * Hq][splits]: a row's (maximum, sum) over a part of the tokens
-    int splits;
-    int chunk;              // tiles of a block that sums
+    int splits;             // (one launch: CTAs of a cluster)
+    int chunk;              // tiles of a block that sums (one launch: at most, of a CTA)
     // many query rows only:
     int chunks;             // blocks of the tiles
     int groups;             // of row blocks that are summed together
@@ -46,6 +46,23 @@ struct KvEvictParams {
 };
 
 namespace {
+
+// The codes of a key word as pairs of fp16 along the channels, (j, j + 4) of 8 or
+// (2j, 2j + 1) of 4: 2^-24 times the code, as it lies (a subnormal number), and 2^-20
+// times it in the odd pairs of 4-bit codes.
+template <int BITS>
+__device__ __forceinline__ void kv_small_codes(uint32_t w, uint32_t (&pair)[16 / BITS]) {
+    if constexpr (BITS == 4) {
+        const uint32_t u = w >> 8;
+        pair[0] = w & 0x000f000fu;
+        pair[1] = w & 0x00f000f0u;
+        pair[2] = u & 0x000f000fu;
+        pair[3] = u & 0x00f000f0u;
+    } else {
+        pair[0] = __byte_perm(w, 0, 0x4140);
+        pair[1] = __byte_perm(w, 0, 0x4342);
+    }
+}
 
 // A page of the table, or -1 where it is out of range (which is recorded).
 __device__ __forceinline__ int64_t kv_page(const KvCache& c, const int32_t* table, int64_t i, unsigned* err) {

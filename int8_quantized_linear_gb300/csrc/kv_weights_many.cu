@@ -4,12 +4,12 @@
 //
 // A block (one per SM) holds 256 query rows of one cache head (query tokens x the
 // head group's heads) as two operand tiles of 128, and walks the cache in tiles of
-// 128 tokens, whose codes become centred fp16 integers (exact) once for both:
+// 128 tokens, whose codes become fp16 operands (as they lie: see kv_weights.cu) once for both:
 //   first pass:   S = Q C^T  (rows x tokens), a thread a row: its maximum and sum
 //   second pass:  S^T = C Q^T  (tokens x rows), a thread a token: the sum of its weights
 // so that neither needs a shuffle; the operand tiles are the same, only their roles
 // in the product change.  The scales stay outside the products, in fp32:
-//   y = s_j S + (low_j + z s_j) sum_d q_d,   a = unit_i y.
+//   y = s_j S + low_j sum_d q_d,   a = unit_i y.
 // In the second pass a row's maximum and sum are one number, n_i = m_i + log2 l_i,
 // rounded to 2^-24 of it, as the logits themselves are.
 //
@@ -359,9 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     uint32_t pk = 0;
                     if (token + tid >= r.span.begin && token + tid < r.span.end)
                         pk = reinterpret_cast<const uint32_t*>(raw + kTile * C::kRowBytes)[tid];
-                    const float s = kv_scale(pk);
-                    scales[kt % kFactors][tid] = s;
-                    offsets[kt % kFactors][tid] = fmaf(s, kCentre<BITS>, kv_low(pk));
+                    scales[kt % kFactors][tid] = kv_scale(pk);
+                    offsets[kt % kFactors][tid] = kv_low(pk);
                 }
                 tc::mbar_arrive(&info_full[kt % kFactors]);
                 if (!dead) {
@@ -379,14 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         for (int j = 0; j < kChunks; ++j) {
                             uint32_t h[4];
                             if constexpr (BITS == 4) {
-                                unpack_nibbles<true>(flip ? w[j ^ 1] : w[j], h);
+                                kv_small_codes<4>(flip ? w[j ^ 1] : w[j], h);
                             } else {
-                                const uint32_t a = flip ? w[2 * (j ^ 1)] : w[2 * j];
-                                const uint32_t b = flip ? w[2 * (j ^ 1) + 1] : w[2 * j + 1];
-                                h[0] = unpack_bytes<true>(a, 0x5150);
-                                h[1] = unpack_bytes<true>(a, 0x5352);
-                                h[2] = unpack_bytes<true>(b, 0x5150);
-                                h[3] = unpack_bytes<true>(b, 0x5352);
+                                uint32_t lo[2], hi[2];
+                                kv_small_codes<8>(flip ? w[2 * (j ^ 1)] : w[2 * j], lo);
+                                kv_small_codes<8>(flip ? w[2 * (j ^ 1) + 1] : w[2 * j + 1], hi);
+                                h[0] = lo[0], h[1] = lo[1], h[2] = hi[0], h[3] = hi[1];
                             }
                             sts16(row + (((pos0 + (j ^ flip)) ^ (tok & 7)) << 4), h[0], h[1], h[2], h[3]);
                         }
@@ -479,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
             const int hi = base + i, lo = p.a.window > 0 ? (int)max(base + i + 1 - p.a.window, (int64_t)0) : 0;
             RowStats stats = {-INFINITY, 0.0f};
             if (active) {
-                // the row goes into its operand tile, scaled to 2^8, permuted as the keys unpack
+                // the row goes into its operand tile, scaled to 2^14, permuted as the keys unpack
                 const uint4* src = reinterpret_cast<const uint4*>(p.a.q + (work.seq.q0 + i) * p.a.q_stride + (int64_t)head * D);
                 uint32_t top = 0;
 #pragma unroll 8
@@ -492,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
                     }
                 }
-                const int e = max((int)(top >> 23), 9) - 127;
-                const float f = p.a.scale_log2 < 0.0f ? -pow2(8 - e) : pow2(8 - e);
-                const float unit = pow2(e - 8) * fabsf(p.a.scale_log2);
+                const int e = max((int)(top >> 23), 15) - 127;
+                const float f = p.a.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
+                const float unit = pow2(e - 14) * (fabsf(p.a.scale_log2) * 0x1p24f);
                 const uint32_t dst = smem_at + C::kOffQ + m * (128 * D * 2) + r_m * 128;
                 float q_sum = 0.0f;
 #pragma unroll 4
@@ -505,10 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     q_sum += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
                     const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r_m & 7)) << 4);
                     if constexpr (BITS == 4)
-                        sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]), pack_f16(y[3], y[7]));
+                        sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1] * 0.0625f, y[5] * 0.0625f), pack_f16(y[2], y[6]),
+                              pack_f16(y[3] * 0.0625f, y[7] * 0.0625f));
                     else
                         sts16(at, pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
                 }
+                q_sum *= 0x1p-24f;
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(&q_full[m]);
                 if constexpr (SUM) {
