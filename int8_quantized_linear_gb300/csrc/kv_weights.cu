@@ -47,7 +47,7 @@ constexpr int kStages = D * BITS == 128 * 8 ? 3 : 4;
 constexpr int kOneTile = 256;
 constexpr int kOneWarps = 8;
 constexpr int kOneThreads = kOneWarps * 32;
-constexpr int kOneStages = 2;
+constexpr int kOneStages = 1;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -142,6 +142,82 @@ struct Queries {
     }
 };
 
+// Query rows ready for the lanes, made once per block: a warp a row.
+template <int D, int BITS, int ROWS>
+struct SharedQueries {
+    static constexpr int kChunks = D / 8;
+    uint4 row[ROWS][kChunks + 1];  // (one more: banks)
+    float sum[ROWS], unit[ROWS];
+    int hi[ROWS], lo[ROWS];
+
+    template <int WARPS>
+    __device__ __forceinline__ void make(const KvAttnParams& p, const KvSeq& seq, int h, int rows) {
+        const int lane = threadIdx.x % 32;
+#pragma unroll
+        for (int r = threadIdx.x / 32; r < ROWS; r += WARPS) {
+            const bool live = r < rows;
+            const int i = live ? r / p.G : 0;
+            const int head = h * p.G + (live ? r - i * p.G : 0);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (live && lane < kChunks)
+                v = __ldg(reinterpret_cast<const uint4*>(p.q + (seq.q0 + i) * p.q_stride + (int64_t)head * D) + lane);
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            uint32_t top = 0;  // largest finite magnitude, as bits
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
+                top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e = max((int)(top >> 23), 15) - 127;
+            const float by = p.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
+            const float y[8] = {lo_bf16(v.x) * by, hi_bf16(v.x) * by, lo_bf16(v.y) * by, hi_bf16(v.y) * by,
+                                lo_bf16(v.z) * by, hi_bf16(v.z) * by, lo_bf16(v.w) * by, hi_bf16(v.w) * by};
+            float total = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+            if (lane < kChunks) {
+                row[r][lane] = BITS == 4 ? make_uint4(pack_f16(y[0], y[4]), pack_f16(y[1] * 0.0625f, y[5] * 0.0625f),
+                                                      pack_f16(y[2], y[6]), pack_f16(y[3] * 0.0625f, y[7] * 0.0625f))
+                                         : make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]),
+                                                      pack_f16(y[6], y[7]));
+            }
+            if (lane == 0) {
+                sum[r] = total * 0x1p-24f;
+                // (not 0: what is not seen, -inf, times 0 would be no number)
+                unit[r] = fmaxf(pow2(e - 14) * (fabsf(p.scale_log2) * 0x1p24f), 0x1p-126f);
+                const int at = seq.len - seq.nq + i;
+                hi[r] = live ? at : -1;
+                lo[r] = p.window > 0 ? (int)max(at + 1 - p.window, (int64_t)0) : 0;
+            }
+        }
+    }
+
+    template <int HALVES>
+    __device__ __forceinline__ void load(Queries<D, BITS, HALVES>& q) const {
+        const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                const uint4 v = row[g + 8 * x][t * (D / 32) + w];
+                q.f[2 * w][x][0] = v.x;
+                q.f[2 * w][x][1] = v.y;
+                q.f[2 * w + 1][x][0] = v.z;
+                q.f[2 * w + 1][x][1] = v.w;
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int r = 8 * x + 2 * t + y;
+                q.sum[x][y] = sum[r];
+                q.unit[x][y] = unit[r];
+                q.hi[x][y] = hi[r];
+                q.lo[x][y] = lo[r];
+            }
+        }
+    }
+};
+
 // A warp's 32 tokens of a tile: token g + 8 i, a lane's quarter of each row.
 template <int D, int BITS>
 struct Keys {
@@ -209,7 +285,8 @@ struct Keys {
 // for memory.  Pages are looked up a step before they are copied from.
 template <int D, int BITS, int WARPS, int STAGES>
 struct KeyRing {
-    static constexpr int kLaneBytes = D * BITS / 32;  // of a row: a quarter
+    static constexpr int kRow = D * BITS / 8;
+    static constexpr int kLaneBytes = kRow / 4;
     static constexpr int kStageBytes = 32 * 4 * kLaneBytes + 32 * 4;
     static constexpr int kBytes = WARPS * STAGES * kStageBytes;
 
@@ -220,12 +297,17 @@ struct KeyRing {
     const uint32_t* params;
     int begin, end;
     int next, last;  // the warp's next step's first token; tokens from `last` on are not wanted
-    int page[2];     // of the next step's two groups of 16 tokens
+    int page[2];     // of the next step (of its second 16 tokens, where pages have 16)
     int put, get;    // stages
+    uint32_t page_rows;
 
-    __device__ __forceinline__ int page_of(int token) const {
-        // (a group may begin before `begin`, but lies in one page)
-        return token < last && token < end && token + 16 > begin ? __ldg(table + (token >> p.cache.page_shift)) : -1;
+    __device__ __forceinline__ void look_up() {
+        if (next >= last) return;
+        // (the first tokens may lie before `begin`, in a page that may be anything, or all of
+        // them behind `end`)
+        const int32_t* at = table + (next >> p.cache.page_shift);
+        page[0] = next < end ? __ldg(at) : -1;
+        if (p.cache.page_shift == 4) page[1] = next + 16 < end ? __ldg(at + 1) : -1;
     }
 
     // Tiles t0 .. t1 - 1; tokens outside begin .. end come as zeros.
@@ -235,60 +317,91 @@ struct KeyRing {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         mine = ring + warp * (STAGES * kStageBytes);
         const int64_t row = (int64_t)h << p.cache.page_shift;
-        codes = p.cache.codes + (row + lane / 4) * (D * BITS / 8) + lane % 4 * kLaneBytes;
+        codes = p.cache.codes + (row + lane / 4) * kRow + lane % 4 * kLaneBytes;
         params = p.cache.params + row + lane % 16;
         next = t0 * (WARPS * 32) + warp * 32;
         last = t1 * (WARPS * 32);
-        page[0] = page_of(next);
-        page[1] = page_of(next + 16);
+        page_rows = (uint32_t)(2 * p.cache.H) << p.cache.page_shift;  // < 2^25
+        look_up();
 #pragma unroll 1
-        for (int i = 0; i < STAGES - 1; ++i) issue();
+        for (int i = 0; i < max(STAGES - 1, 1); ++i) issue();
     }
 
+    static constexpr int kCopy = kLaneBytes < 16 ? kLaneBytes : 16;
+    __device__ __forceinline__ static void copy(uint32_t dst, const void* src) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kCopy) : "memory");
+    }
     __device__ __forceinline__ static void copy(uint32_t dst, const void* src, bool there) {
-        // (not there: zeros, nothing is read)
-        constexpr int kSize = kLaneBytes < 16 ? kLaneBytes : 16;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kSize), "r"(there ? kSize : 0)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kCopy), "r"(there ? kCopy : 0)
+                     : "memory");
+    }
+
+    // A step whose tokens lie in one page and are all wanted: addresses are constants apart.
+    __device__ __forceinline__ void issue_whole(uint32_t stage) {
+        const int lane = threadIdx.x % 32;
+        const uint32_t off = (uint32_t)next & ((1u << p.cache.page_shift) - 1u);
+        const uint64_t row = (uint64_t)(uint32_t)page[0] * page_rows + off;
+        const uint8_t* src = codes + row * kRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kLaneBytes == 32) {
+                // (16 bytes of all lanes, then the other 16: banks)
+                copy(stage + i * 32 * kLaneBytes + lane * 16, src + i * (8 * kRow));
+                copy(stage + i * 32 * kLaneBytes + lane * 16 + 512, src + i * (8 * kRow) + 16);
+            } else {
+                copy(stage + (i * 32 + lane) * kLaneBytes, src + i * (8 * kRow));
+            }
+        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stage + 128 * kLaneBytes + lane * 4),
+                     "l"(params + row + (lane & 16))
+                     : "memory");
+    }
+
+    // Any step: tokens that are not wanted come as zeros (and nothing is read for them).
+    // (Rare, so a function; of values, so that the ring stays in registers.)
+    static __device__ __noinline__ void issue_parts(const uint8_t* codes, const uint32_t* params, int64_t pages,
+                                                    int page_shift, uint32_t page_rows, int page0, int page1, int next,
+                                                    int begin, int end, uint32_t stage, unsigned* err) {
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        const int mask = (1 << page_shift) - 1;
+        int64_t at[2];  // rows from page 0's
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int token = next + 16 * i;
+            int64_t from = i == 0 || page_shift > 4 ? page0 : page1;
+            if (from < 0 || from >= pages) {
+                if (token < end && token + 16 > begin) record_fault(err, kErrBitBadIndex);
+                from = 0;
+            }
+            at[i] = from * page_rows + (token & mask);
+        }
+        auto wanted = [&](int token) { return token >= begin && token < end; };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t* src = codes + at[i / 2] * kRow + (i % 2) * (8 * kRow);
+            const bool there = wanted(next + 8 * i + g);
+            if constexpr (kLaneBytes == 32) {
+                copy(stage + i * 32 * kLaneBytes + lane * 16, src, there);
+                copy(stage + i * 32 * kLaneBytes + lane * 16 + 512, src + 16, there);
+            } else {
+                copy(stage + (i * 32 + lane) * kLaneBytes, src, there);
+            }
+        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stage + 128 * kLaneBytes + lane * 4),
+                     "l"(params + (lane < 16 ? at[0] : at[1])), "r"(wanted(next + lane) ? 4 : 0)
                      : "memory");
     }
 
     __device__ __forceinline__ void issue() {
-        const int lane = threadIdx.x % 32, g = lane / 4;
         if (next < last) {
-            constexpr int kRow = D * BITS / 8;
-            const int mask = (1 << p.cache.page_shift) - 1;
             const uint32_t stage = tc::smem_u32(mine) + put * kStageBytes;
-            const bool all = next >= begin && next + 32 <= end;  // every token is wanted
-            int64_t at[2];  // rows from page 0's
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int token = next + 16 * i;
-                if ((uint32_t)page[i] >= (uint64_t)p.cache.pages) {
-                    if (token < end && token + 16 > begin) record_fault(p.err, kErrBitBadIndex);
-                    page[i] = 0;
-                }
-                at[i] = ((int64_t)page[i] * (2 * p.cache.H) << p.cache.page_shift) + (token & mask);
-            }
-            auto wanted = [&](int token) { return all || (token >= begin && token < end); };
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* src = codes + at[i / 2] * kRow + (i % 2) * (8 * kRow);
-                const bool there = wanted(next + 8 * i + g);
-                if constexpr (kLaneBytes == 32) {
-                    // (16 bytes of all lanes, then the other 16: banks)
-                    const uint32_t dst = stage + i * 32 * kLaneBytes + lane * 16;
-                    copy(dst, src, there);
-                    copy(dst + 512, src + 16, there);
-                } else {
-                    copy(stage + (i * 32 + lane) * kLaneBytes, src, there);
-                }
-            }
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stage + 128 * kLaneBytes + lane * 4),
-                         "l"(params + (lane < 16 ? at[0] : at[1])), "r"(wanted(next + lane) ? 4 : 0)
-                         : "memory");
-            next += (WARPS * 32);
-            page[0] = page_of(next);
-            page[1] = page_of(next + 16);
+            if (next >= begin && next + 32 <= end && p.cache.page_shift > 4 && (uint32_t)page[0] < (uint32_t)p.cache.pages)
+                issue_whole(stage);
+            else
+                issue_parts(codes, params, p.cache.pages, p.cache.page_shift, page_rows, page[0], page[1], next, begin, end,
+                            stage, p.err);
+            next += WARPS * 32;
+            look_up();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         put = put + 1 == STAGES ? 0 : put + 1;
@@ -298,9 +411,9 @@ struct KeyRing {
     __device__ __forceinline__ void take(Keys<D, BITS>& k) {
         constexpr int kWords = Keys<D, BITS>::kWords;
         const int lane = threadIdx.x % 32, g = lane / 4;
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
         __syncwarp();  // the other lanes' scales; and all lanes are done with the step before
-        issue();
+        if (STAGES > 1) issue();
         const uint8_t* stage = mine + get * kStageBytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -319,6 +432,10 @@ struct KeyRing {
             k.param[i] = *reinterpret_cast<const uint32_t*>(stage + 128 * kLaneBytes + (g + 8 * i) * 4);
         }
         get = get + 1 == STAGES ? 0 : get + 1;
+        if (STAGES == 1) {  // (what has been taken is in registers)
+            __syncwarp();
+            issue();
+        }
     }
 };
 
@@ -369,25 +486,27 @@ __device__ __forceinline__ void warp_stats(float (&m)[HALVES][2], float (&l)[HAL
 // logits stay in shared memory, the CTAs exchange each row's (m, l), and the
 // weights are summed from there.
 template <int D, int BITS, int HALVES>
-__global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsParams p) {
+__global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2 : 1) kv_weigh_kernel(const KvWeightsParams p) {
     constexpr int ROWS = 8 * HALVES;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[kOneWarps][ROWS];         // a warp's maxima, then its sums
-    __shared__ float units[ROWS];
+    __shared__ float part[kOneWarps][ROWS];      // a warp's maxima, then its sums
+    __shared__ SharedQueries<D, BITS, ROWS> queries;
     __shared__ __align__(16) float2 mine[ROWS];  // this CTA's (m, l)
-    __shared__ __align__(8) float factors[ROWS];              // of this CTA's weights: 2^(its m - m) / l
+    __shared__ __align__(8) float factors[ROWS]; // of this CTA's weights: 2^(its m - m) / l
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int size = p.splits, rank = (int)tc::cluster_rank();
-    const int64_t item = blockIdx.x / size;
-    const int64_t b = item / p.a.cache.H;
-    const int h = (int)(item - b * p.a.cache.H);
+    const uint32_t item = blockIdx.x / (uint32_t)size;
+    const uint32_t b = item / (uint32_t)p.a.cache.H;
+    const int h = (int)(item - b * (uint32_t)p.a.cache.H);
     pdl_wait();
     const KvSeq seq = weights_sequence(p, b);
     if (seq.nq == 0) return;  // (the whole cluster)
-    const KvSpan span = kv_span<ROWS, kOneTile>(p.a, seq, 0);
-    const int rows = min(ROWS, seq.nq * p.a.G);
-    const int tile0 = span.first + (int)((int64_t)span.tiles * rank / size);
-    const int tile1 = span.first + (int)((int64_t)span.tiles * (rank + 1) / size);
+    // what the rows see: tokens begin .. end - 1, and each of them all_lo .. all_hi
+    const int base = seq.len - seq.nq, rows = min(ROWS, seq.nq * p.a.G);
+    const int begin = p.a.window > 0 ? (int)min(max(base + 1 - p.a.window, (int64_t)0), (int64_t)seq.len) : 0, end = seq.len;
+    const int all_lo = p.a.window > 0 ? (int)max(seq.len - p.a.window, (int64_t)0) : 0, all_hi = base;
+    const int first_tile = begin / kOneTile, tiles = (end + kOneTile - 1) / kOneTile - first_tile;
+    const int tile0 = first_tile + tiles * rank / size, tile1 = first_tile + tiles * (rank + 1) / size;
     const int32_t* table = p.a.table + b * p.a.table_width;
     // [pairs of rows][tokens]; 8 more tokens keep a warp's stores off each other's banks
     float2* logits = reinterpret_cast<float2*>(smem + KeyRing<D, BITS, kOneWarps, kOneStages>::kBytes);
@@ -397,18 +516,11 @@ __global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsPa
         float top[HALVES][2];
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) top[x][0] = top[x][1] = -INFINITY;
-        KeyRing<D, BITS, kOneWarps, kOneStages> ring(p.a, table, smem, h, tile0, tile1, span.begin, span.end);
+        KeyRing<D, BITS, kOneWarps, kOneStages> ring(p.a, table, smem, h, tile0, tile1, begin, end);
+        queries.template make<kOneWarps>(p.a, seq, h, rows);
+        __syncthreads();
         Queries<D, BITS, HALVES> q;
-        q.load(p.a, seq, h, 0, rows);
-        // tokens [all_lo, all_hi] are seen by every row
-        const int base = seq.len - seq.nq, all_hi = base;
-        const int all_lo = p.a.window > 0 ? (int)max(base + (rows - 1) / p.a.G + 1 - p.a.window, (int64_t)0) : 0;
-        if (warp == 0 && g == 0) {
-#pragma unroll
-            for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) units[8 * x + 2 * t + y] = q.unit[x][y];
-        }
+        queries.load(q);
         int token = tile0 * kOneTile + warp * 32 + g;
         float2* to = logits + t * stride + warp * 32 + g;
         auto step = [&](auto edge) {
@@ -452,12 +564,12 @@ __global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsPa
     if (threadIdx.x < ROWS) {
         float m = part[0][threadIdx.x];
         for (int w = 1; w < kOneWarps; ++w) m = fmaxf(m, part[w][threadIdx.x]);
-        m = threadIdx.x < rows ? m * units[threadIdx.x] : 0.0f;
+        m = threadIdx.x < rows ? m * queries.unit[threadIdx.x] : 0.0f;
         mine[threadIdx.x].x = m;
     }
     __syncthreads();
     for (int r = 0; 2 * r < rows; ++r) {
-        const float u0 = units[2 * r], u1 = units[2 * r + 1];
+        const float u0 = queries.unit[2 * r], u1 = queries.unit[2 * r + 1];
         const float m0 = mine[2 * r].x == -INFINITY ? 0.0f : -mine[2 * r].x;
         const float m1 = mine[2 * r + 1].x == -INFINITY ? 0.0f : -mine[2 * r + 1].x;
         float l0 = 0.0f, l1 = 0.0f;
@@ -508,7 +620,7 @@ __global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsPa
     const int mask = (1 << p.a.cache.page_shift) - 1, older = p.previous != nullptr ? seq.len - seq.nq : 0;
     for (int i = threadIdx.x * 4; i < tokens; i += 4 * kOneThreads) {
         const int j = tile0 * kOneTile + i;
-        if (j + 4 <= span.begin || j >= span.end) continue;
+        if (j + 4 <= begin || j >= end) continue;
         const int64_t page = kv_page(p.a.cache, table, j >> p.a.cache.page_shift, p.a.err);
         if (page < 0) continue;
         const int64_t to = kv_weight(p.a.cache, page, h, j & mask);
@@ -528,13 +640,13 @@ __global__ void __launch_bounds__(kOneThreads) kv_weigh_kernel(const KvWeightsPa
             sum.w = fmaf(c.w, f.y, fmaf(c.z, f.x, sum.w));
         }
         w = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
-        if (j >= span.begin && j + 4 <= span.end) {
+        if (j >= begin && j + 4 <= end) {
             *reinterpret_cast<float4*>(p.weights + to) = w;
         } else {
             const float v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (j + k >= span.begin && j + k < span.end) p.weights[to + k] = v[k];
+                if (j + k >= begin && j + k < end) p.weights[to + k] = v[k];
         }
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
