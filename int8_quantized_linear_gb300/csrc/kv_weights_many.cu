@@ -4,25 +4,40 @@
 //
 // A block (one per SM) holds 256 query rows of one cache head (query tokens x the
 // head group's heads) as two operand tiles of 128, and walks the cache in tiles of
-// 128 tokens, whose codes become fp16 operands (as they lie: see kv_weights.cu) once for both:
-//   first pass:   S = Q C^T  (rows x tokens), a thread a row: its maximum and sum
-//   second pass:  S^T = C Q^T  (tokens x rows), a thread a token: the sum of its weights
+// 128 tokens, which become fp16 operands once for both:
+//   first pass:   S = Q K^T  (rows x tokens), a thread a row: its maximum and sum
+//   second pass:  S^T = K Q^T  (tokens x rows), a thread a token: the sum of its weights
 // so that neither needs a shuffle; the operand tiles are the same, only their roles
-// in the product change.  The scales stay outside the products, in fp32:
-//   y = s_j S + low_j sum_d q_d,   a = unit_i y.
-// In the second pass a row's maximum and sum are one number, n_i = m_i + log2 l_i,
-// rounded to 2^-24 of it, as the logits themselves are.
+// in the product change.
+//
+// What a column of S needs of its own would come from shared memory, whose reads give
+// each lane 4 bytes a cycle even where all read the same: a number per column costs
+// as much as the exponential.  So scale and low value are inside the product, without
+// rounding what they scale: with x = low + s c of 4-bit codes
+//   x = s (c - 8) + o,   o = low + 8 s
+// s (c - 8) has 8 + 3 bits, which fp16 holds exactly, and o meets only the sum of the
+// row's q, so both go into 16 channels more, as sums of two fp16 numbers each (o_hi q_hi +
+// o_hi q_lo + o_lo q_hi: 2^-22 of o sum q).  A byte is two such nibbles,
+//   low + s c = 16 s (c_hi - 8) + s (c_lo - 8) + low + 136 s,
+// products with the same q.  (With the scales outside the products instead, as two and
+// three numbers a column, two chunks of 2048 tokens over 8192 took 970 us.)
+// A tile is held times the power of two that brings its largest element to 2^7: tokens
+// 2^21 below it lose bits.  A row of Q is scaled to 2^14 (first pass) or its 16 rows
+// together are (second pass, where rows are columns: rows 2^14 below the largest of
+// their 16 keep 2^-25 of it).  In the second pass a row's maximum and sum are
+// one number, n_i = m_i + log2 l_i, rounded to 2^-24 of it, as the logits themselves are.
 //
 // The second pass leaves sums over up to 128-row halves of a group of row blocks per
 // token in a workspace (a thread adds to its own place, in order), and a third kernel
 // adds those up: no atomics, the same bits whatever the timing.
 //
-// Roles: warps 0-3 and 4-7 the softmax of the two halves, warps 8-11 unpack codes
-// into the swizzled operand tiles, warp 12 copies pages, warp 13 issues the MMAs.
-// S is held twice per half (all 512 columns of TMEM), so products run ahead of the
-// softmax.  Operand layout: K-major, 128-byte swizzle, channels in the order in which
-// key words unpack.
+// Roles: 16 softmax warps, a set of 8 for the even steps and one for the odd ones, each
+// four warps for a half; 4 warps unpack codes into the swizzled operand tiles, one
+// copies pages, one issues the MMAs.  S is held twice per half (all 512 columns of TMEM):
+// a set works on one step's while the other's products run.  Operand layout: K-major,
+// 128-byte swizzle, channels in the order in which key words unpack.
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,23 +50,27 @@ namespace {
 
 constexpr int kTile = kKvPromptTile;  // cache tokens per tile
 constexpr int kRows = kKvPromptRows;  // query rows per block: two halves
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 16;
 constexpr int kUnpackWarps = 4;
 constexpr int kCopyWarp = kSoftmaxWarps + kUnpackWarps;
 constexpr int kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kStages = 2;     // unpacked tiles
 constexpr int kRaw = 2;        // raw tiles
-constexpr int kFactors = 4;    // tiles whose scales are kept
+constexpr int kInfo = 4;       // tiles whose exponents are kept
 constexpr float kSlack = 8.0f; // a row's maximum may exceed what its sum is relative to by this (log2)
 
 template <int D, int BITS>
 struct Cfg {
     static constexpr int kRowBytes = D * BITS / 8;
-    static constexpr int kKTile = kTile * D * 2;
+    static constexpr int kNibbles = BITS / 4;
+    static constexpr int kStages = D == 128 && BITS == 8 ? 1 : 2;  // unpacked tiles
+    static constexpr int kMore = kTile * 128;  // a tile of the 16 channels more (of a swizzle atom's 64)
+    static constexpr int kPart = kTile * D * 2;
+    static constexpr int kKTile = kNibbles * kPart + kMore;
+    static constexpr int kQTile = kPart + kMore;  // 128 rows
     static constexpr int kRawBytes = kTile * kRowBytes + kTile * 4;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + kRows * D * 2;
+    static constexpr int kOffK = kOffQ + 2 * kQTile;
     static constexpr int kOffRaw = kOffK + kStages * kKTile;
     // (at least what keeps a second block, which would wait for TMEM, off the SM)
     static constexpr int kSmem = std::max(kOffRaw + kRaw * kRawBytes + 1024, 116 * 1024);
@@ -138,92 +157,98 @@ __device__ __forceinline__ Part find_part(const KvWeightsParams& p, const Work& 
     return r;
 }
 
-// A row's sum so far, relative to 2^ref.
+// A row's sum so far, relative to 2^ref; nothing yet: ref is -inf.
 struct RowStats {
     float ref, sum;
 };
 
-// 32 columns of S of a row: tokens `token`.. with their scales and offsets.
-template <bool EDGE>
-__device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, const float* scale, const float* offset,
-                                           float q_sum, float unit, int token, int lo, int hi) {
-    uint32_t x[32];
-    tmem_ld32(s_at, x);
-    const uint64_t q2 = pair_f32(q_sum, q_sum);
-    uint64_t y[16];
-    float high[2] = {-INFINITY, -INFINITY};
-    tc::tmem_wait_ld();
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(scale + j);
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(offset + j);
-        const uint64_t zero = 0;
-        uint64_t a = fma_f32x2(pair_u32(x[j], x[j + 1]), s.x, fma_f32x2(o.x, q2, zero));
-        uint64_t b = fma_f32x2(pair_u32(x[j + 2], x[j + 3]), s.y, fma_f32x2(o.y, q2, zero));
-        float v[4];
-        split_f32(a, v[0], v[1]);
-        split_f32(b, v[2], v[3]);
-        if (EDGE) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = token + j + k <= hi && token + j + k >= lo ? v[k] : -INFINITY;
-        }
-        high[0] = max3(high[0], v[0], v[1]);
-        high[1] = max3(high[1], v[2], v[3]);
-        y[j / 2] = a;
-        y[j / 2 + 1] = b;
-    }
-    const float top = fmaxf(high[0], high[1]) * unit;  // (unit >= 0; no number for nothing seen at unit 0)
-    if (__any_sync(0xffffffffu, top > r.ref + kSlack)) {
-        if (top > r.ref + kSlack) {
-            r.sum *= exp2_approx(r.ref - top);
-            r.ref = top;
-        }
-    }
-    const float shift = r.ref == -INFINITY ? 0.0f : -r.ref;
-    const uint64_t u2 = pair_f32(unit, unit), shift2 = pair_f32(shift, shift);
-    uint64_t sum[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float a, b;
-        split_f32(fma_f32x2(y[j], u2, shift2), a, b);
-        a = exp2_approx(a);
-        b = exp2_approx(b);
-        if (EDGE) {
-            const int tok = token + 2 * j;
-            a = tok <= hi && tok >= lo ? a : 0.0f;
-            b = tok + 1 <= hi && tok + 1 >= lo ? b : 0.0f;
-        }
-        sum[j & 1] = add_f32x2(sum[j & 1], pair_f32(a, b));
-    }
-    float a, b;
-    split_f32(add_f32x2(sum[0], sum[1]), a, b);
-    r.sum += a + b;
+// Raises a row's reference to the maximum.
+__device__ __forceinline__ void raise(RowStats& r, float to) {
+    r.sum *= r.ref == -INFINITY ? 0.0f : exp2_approx(r.ref - to);
+    r.ref = to;
 }
 
-// What the columns of S^T need of their rows: unit, unit times the sum of the scaled
-// row, and -n; the last token that the row sees.
+// 32 columns of S of a row, all of them tokens that it sees.
+__device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, float unit) {
+    uint32_t x[32];
+    tmem_ld32(s_at, x);
+    const uint64_t u2 = pair_f32(unit, unit);
+    tc::tmem_wait_ld();
+    // The exponents relative to what the sum is: where one exceeds the slack (rare: the
+    // first time, and then as larger logits come), the reference is raised and all is
+    // done again.
+    for (bool again = r.ref == -INFINITY;;) {
+        const float ref = r.ref == -INFINITY ? 0.0f : -r.ref;
+        const uint64_t ref2 = pair_f32(ref, ref);
+        uint64_t sum[2] = {0, 0};
+        float high[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float y, z;
+            split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), u2, ref2), y, z);
+            high[(j / 2) & 1] = max3(high[(j / 2) & 1], y, z);
+            sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(exp2_approx(y), exp2_approx(z)));
+        }
+        const float top = fmaxf(high[0], high[1]);
+        again = again || top > kSlack;
+        if (!__any_sync(0xffffffffu, again)) {
+            float a, b;
+            split_f32(add_f32x2(sum[0], sum[1]), a, b);
+            r.sum += a + b;
+            return;
+        }
+        if (again) raise(r, top - ref);
+        again = false;
+    }
+}
+
+// A tile where some row does not see some token: this one sees lo .. hi.
+__device__ __noinline__ RowStats add_some_tokens(RowStats r, uint32_t s_at, float unit, int token, int lo, int hi) {
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        uint32_t x[32];
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int tok = token + q * 32 + j;
+            x[j] = __float_as_uint(tok <= hi && tok >= lo ? __uint_as_float(x[j]) * unit : -INFINITY);
+            top = fmaxf(top, __uint_as_float(x[j]));
+        }
+        if (top > r.ref + kSlack || (r.ref == -INFINITY && top > -INFINITY)) raise(r, top);
+        const float ref = r.ref == -INFINITY ? 0.0f : -r.ref;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum += exp2_approx(__uint_as_float(x[j]) + ref);
+        r.sum += sum;
+    }
+    return r;
+}
+
+// What the softmax needs of a half's rows: what a product counts (in log2 units, times
+// the tile's), where rows are columns -n, and the last token that the row sees.
+constexpr int kGroup = 16;  // rows that share a unit where they are columns
 struct RowFactors {
-    float unit[kTile], sum[kTile], minus_n[kTile];
+    float unit[kTile], minus_n[kTile];
     int hi[kTile];
 };
 
 // The sum of 32 rows' weights of a token.
 template <bool EDGE>
-__device__ __forceinline__ void add_rows(uint64_t (&sum)[2], uint32_t s_at, const RowFactors& f, int c0, float scale,
-                                         float offset, int token, int64_t window) {
+__device__ __forceinline__ void add_rows(uint64_t (&sum)[2], uint32_t s_at, const RowFactors& f, int c0, float unit, int token,
+                                         int64_t window) {
     uint32_t x[32];
     tmem_ld32(s_at, x);
-    const uint64_t s2 = pair_f32(scale, scale), o2 = pair_f32(offset, offset);
     tc::tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(f.unit + c0 + j);
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(f.sum + c0 + j);
+        const float u = f.unit[c0 + j / kGroup * kGroup] * unit;
+        const uint64_t u2 = pair_f32(u, u);
         const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(f.minus_n + c0 + j);
-        const uint64_t zero = 0;
         float v[4];
-        split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), fma_f32x2(u.x, s2, zero), fma_f32x2(q.x, o2, n.x)), v[0], v[1]);
-        split_f32(fma_f32x2(pair_u32(x[j + 2], x[j + 3]), fma_f32x2(u.y, s2, zero), fma_f32x2(q.y, o2, n.y)), v[2], v[3]);
+        split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), u2, n.x), v[0], v[1]);
+        split_f32(fma_f32x2(pair_u32(x[j + 2], x[j + 3]), u2, n.y), v[2], v[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             v[k] = exp2_approx(v[k]);
@@ -237,14 +262,24 @@ __device__ __forceinline__ void add_rows(uint64_t (&sum)[2], uint32_t s_at, cons
     }
 }
 
+// fp16 parts of x: x = hi + lo but for 2^-22 of it.
+__device__ __forceinline__ void split_f16(float x, uint32_t& hi, uint32_t& lo) {
+    const __half h = __float2half_rn(x);
+    hi = __half_as_ushort(h);
+    lo = __half_as_ushort(__float2half_rn(x - __half2float(h)));
+}
+
 template <int D, int BITS, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWeightsParams p) {
     using C = Cfg<D, BITS>;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages];
-    __shared__ uint64_t q_full[2], s_full[2][2], s_empty[2][2], info_full[kFactors], drained;
-    __shared__ __align__(16) float scales[kFactors][kTile], offsets[kFactors][kTile];
-    __shared__ __align__(16) RowFactors row_factors[SUM ? 2 : 1];
+    __shared__ uint64_t q_full[2], s_full[2][2], s_empty[2][2], info_full[kInfo], drained;
+    __shared__ __align__(16) uint32_t exp_red[2][kUnpackWarps];  // largest magnitudes, as bits
+    __shared__ int tile_exp[kInfo];     // a tile is held times 2^(134 - tile_exp)
+    __shared__ uint32_t factor[kTile];  // a token's scale, twice, as halves
+    __shared__ __align__(16) RowFactors row_factors[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -268,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 tc::mbar_init(&s_empty[i][j], 128);
             }
         }
-        for (int i = 0; i < kFactors; ++i) tc::mbar_init(&info_full[i], kUnpackWarps * 32);
+        for (int i = 0; i < kInfo; ++i) tc::mbar_init(&info_full[i], kUnpackWarps);
         tc::mbar_init(&drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -342,9 +377,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
     } else if (warp >= kSoftmaxWarps && warp < kCopyWarp) {
         // ------------------------------------------------------------ unpacking
         const int tid = threadIdx.x - kSoftmaxWarps * 32;  // 0 .. 127
+        const int w4 = warp - kSoftmaxWarps;
+        auto unpack_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kUnpackWarps * 32) : "memory"); };
         constexpr int kLanesPerKey = C::kRowBytes / 16;
         constexpr int kChunks = BITS == 4 ? 4 : 2;  // operand chunks (8 channels) per 16 raw bytes
+        constexpr float kMiddle = BITS == 4 ? 8.0f : 136.0f;  // what the products leave of a code
+        constexpr float kTop = BITS == 4 ? 8.0f : 128.0f;     // the largest of what they have, in scales
         const int key_lane = tid % kLanesPerKey;
+        // of the channels more the second chunk stays 0
+        for (int i = 0; i < kStages; ++i)
+            sts16(smem_at + C::kOffK + i * C::kKTile + C::kNibbles * C::kPart + tid * 128 + ((1 ^ (tid & 7)) << 4), 0, 0, 0, 0);
         uint32_t kt = 0;
         for (int rb = work.rb0; rb < work.rb1; ++rb) {
             const Part r = find_part<SUM>(p, work, rb);
@@ -353,39 +395,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 const uint32_t slot = kt % kRaw, stage = kt % kStages;
                 const uint8_t* raw = smem + C::kOffRaw + slot * C::kRawBytes;
                 wait(&raw_full[slot], (kt / kRaw) & 1);
+                // the tile's exponent: of its largest scaled code, and of its largest offset
+                uint32_t pk = 0;
+                if (!dead && token + tid >= r.span.begin && token + tid < r.span.end)
+                    pk = reinterpret_cast<const uint32_t*>(raw + kTile * C::kRowBytes)[tid];
+                const float offset = fmaf(kv_scale(pk), kMiddle, kv_low(pk));
+                const uint32_t bits = max(__float_as_uint(kv_scale(pk) * kTop) & 0x7fffffffu, __float_as_uint(offset) & 0x7fffffffu);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
+                if (lane == 0) exp_red[kt & 1][w4] = top;
+                unpack_sync();  // (and the tile before is done with its factors)
+                const uint4 tops = *reinterpret_cast<const uint4*>(exp_red[kt & 1]);
+                const uint32_t e = max(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23, 8u);
+                const float f = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
+                factor[tid] = pack_f16(kv_scale(pk) * f, kv_scale(pk) * f);
                 // this stage's last products are done: so is the softmax of four tiles ago
                 wait(&k_empty[stage], ((kt / kStages) & 1) ^ 1);
-                if (!dead) {
-                    uint32_t pk = 0;
-                    if (token + tid >= r.span.begin && token + tid < r.span.end)
-                        pk = reinterpret_cast<const uint32_t*>(raw + kTile * C::kRowBytes)[tid];
-                    scales[kt % kFactors][tid] = kv_scale(pk);
-                    offsets[kt % kFactors][tid] = kv_low(pk);
-                }
-                tc::mbar_arrive(&info_full[kt % kFactors]);
+                if (tid == 0) tile_exp[kt % kInfo] = (int)e;
+                unpack_sync();
+                if (lane == 0) tc::mbar_arrive(&info_full[kt % kInfo]);
                 if (!dead) {
                     const uint32_t dst = smem_at + C::kOffK + stage * C::kKTile;
+                    {
+                        uint32_t o_hi, o_lo;
+                        split_f16(offset * f * 128.0f, o_hi, o_lo);
+                        sts16(dst + C::kNibbles * C::kPart + tid * 128 + ((tid & 7) << 4), o_hi | o_hi << 16, o_lo, 0, 0);
+                    }
 #pragma unroll 1
                     for (int i = 0; i < kLanesPerKey; ++i) {
                         const int tok = tid / kLanesPerKey + i * (kTile / kLanesPerKey);
                         uint32_t w[4];
                         lds<4>(raw + tok * C::kRowBytes + key_lane * 16, w);
+                        const uint32_t scale = factor[tok];
                         const int chunk0 = key_lane * kChunks;  // of the row's D / 8
                         const int block = chunk0 / 8, pos0 = chunk0 % 8;
                         const int flip = block & 1;  // lanes of the two blocks take their chunks in opposite order (banks)
                         const uint32_t row = dst + block * (kTile * 128) + tok * 128;
+                        auto scaled = [&](uint32_t v) { return fma_f16x2(v, scale, 0x80008000u); };  // (exact; -0: a product)
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
-                            uint32_t h[4];
+                            const uint32_t at = row + (((pos0 + (j ^ flip)) ^ (tok & 7)) << 4);
                             if constexpr (BITS == 4) {
-                                kv_small_codes<4>(flip ? w[j ^ 1] : w[j], h);
+                                uint32_t h[4];
+                                unpack_nibbles<true>(flip ? w[j ^ 1] : w[j], h);
+                                sts16(at, scaled(h[0]), scaled(h[1]), scaled(h[2]), scaled(h[3]));
                             } else {
-                                uint32_t lo[2], hi[2];
-                                kv_small_codes<8>(flip ? w[2 * (j ^ 1)] : w[2 * j], lo);
-                                kv_small_codes<8>(flip ? w[2 * (j ^ 1) + 1] : w[2 * j + 1], hi);
-                                h[0] = lo[0], h[1] = lo[1], h[2] = hi[0], h[3] = hi[1];
+                                // of 8 channels (0,2) (1,3) (4,6) (5,7): low nibbles, and 16 times the high ones
+                                uint32_t lo[4], hi[4];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t v = flip ? w[2 * (j ^ 1) + k] : w[2 * j + k], u = v >> 8;
+                                    lo[2 * k] = sub_f16x2(and_or(v, 0x000f000fu, 0x64006400u), 0x64086408u);  // 1024 + c - 1032
+                                    lo[2 * k + 1] = sub_f16x2(and_or(u, 0x000f000fu, 0x64006400u), 0x64086408u);
+                                    hi[2 * k] = sub_f16x2(and_or(v, 0x00f000f0u, 0x64006400u), 0x64806480u);  // 1024 + 16 c - 1152
+                                    hi[2 * k + 1] = sub_f16x2(and_or(u, 0x00f000f0u, 0x64006400u), 0x64806480u);
+                                }
+                                sts16(at, scaled(lo[0]), scaled(lo[1]), scaled(lo[2]), scaled(lo[3]));
+                                sts16(at + C::kPart, scaled(hi[0]), scaled(hi[1]), scaled(hi[2]), scaled(hi[3]));
                             }
-                            sts16(row + (((pos0 + (j ^ flip)) ^ (tok & 7)) << 4), h[0], h[1], h[2], h[3]);
                         }
                     }
                     tc::fence_proxy_async_smem();
@@ -410,9 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 wait(&q_full[m], items[m] & 1);
                 ++items[m];
             }
-            // A half that sits out is done with its last tile, whose scales the tiles to
-            // come would overwrite (one that takes part says so with its row block's Q).
-            if (halves == 1 && steps[1] > 0) wait(&s_empty[1][(steps[1] - 1) & 1], ((steps[1] - 1) / 2) & 1);
+            // A half that sits out is done with its last tiles (one of each set), whose scales
+            // the tiles to come would overwrite (one that takes part says so with its Q).
+            for (uint32_t i = 1; halves == 1 && i <= min(steps[1], 2u); ++i)
+                wait(&s_empty[1][(steps[1] - i) & 1], ((steps[1] - i) / 2) & 1);
             for (int tile = r.t0; tile < r.t1; ++tile, ++kt) {
                 wait(&k_full[kt % kStages], (kt / kStages) & 1);
                 for (int m = 0; m < halves; ++m, __syncwarp()) {
@@ -420,21 +487,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     wait(&s_empty[m][buf], ((steps[m] / 2) & 1) ^ 1);
                     ++steps[m];
                     tc::tc_fence_after();
-                    const uint32_t q = q_base + m * (128 * D * 2 / 16), k = k_base + (kt % kStages) * (C::kKTile / 16);
+                    const uint32_t q = q_base + m * (C::kQTile / 16), k = k_base + (kt % kStages) * (C::kKTile / 16);
                     const uint32_t a = SUM ? k : q, b = SUM ? q : k;
                     const uint32_t d = tmem + (m * 2 + buf) * kTile, issue = !dead && lane == 0;
+                    constexpr int kNext = 128 * 128 / 16;  // the second 64 channels
+                    constexpr int kHigh = C::kPart / 16;   // the high nibbles, beside the same Q
+                    constexpr int kMoreK = C::kNibbles * C::kPart / 16, kMoreQ = C::kPart / 16;
                     __syncwarp();
                     mma_ss<0, 0>(d, a, b, high, idesc, 0, issue);
                     mma_ss<2, 2>(d, a, b, high, idesc, 1, issue);
                     mma_ss<4, 4>(d, a, b, high, idesc, 1, issue);
                     mma_ss<6, 6>(d, a, b, high, idesc, 1, issue);
                     if constexpr (D == 128) {
-                        constexpr int kNext = 128 * 128 / 16;  // the second 64 channels
                         mma_ss<kNext, kNext>(d, a, b, high, idesc, 1, issue);
                         mma_ss<kNext + 2, kNext + 2>(d, a, b, high, idesc, 1, issue);
                         mma_ss<kNext + 4, kNext + 4>(d, a, b, high, idesc, 1, issue);
                         mma_ss<kNext + 6, kNext + 6>(d, a, b, high, idesc, 1, issue);
                     }
+                    if constexpr (BITS == 8) {
+                        constexpr int A = SUM ? kHigh : 0, B = SUM ? 0 : kHigh;
+                        mma_ss<A, B>(d, a, b, high, idesc, 1, issue);
+                        mma_ss<A + 2, B + 2>(d, a, b, high, idesc, 1, issue);
+                        mma_ss<A + 4, B + 4>(d, a, b, high, idesc, 1, issue);
+                        mma_ss<A + 6, B + 6>(d, a, b, high, idesc, 1, issue);
+                        if constexpr (D == 128) {
+                            mma_ss<A + kNext, B + kNext>(d, a, b, high, idesc, 1, issue);
+                            mma_ss<A + kNext + 2, B + kNext + 2>(d, a, b, high, idesc, 1, issue);
+                            mma_ss<A + kNext + 4, B + kNext + 4>(d, a, b, high, idesc, 1, issue);
+                            mma_ss<A + kNext + 6, B + kNext + 6>(d, a, b, high, idesc, 1, issue);
+                        }
+                    }
+                    mma_ss<SUM ? kMoreK : kMoreQ, SUM ? kMoreQ : kMoreK>(d, a, b, high, idesc, 1, issue);
                     commit_mma(&s_full[m][buf], issue);
                 }
                 commit_mma(&k_empty[kt % kStages], !dead && lane == 0);
@@ -447,15 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
         tc::mbar_wait(&drained, 0, &none, p.a.err);
     } else {
         // ------------------------------------------------------------ softmax
-        const int m = warp / 4;
-        const int r_m = threadIdx.x & 127;  // row of the half
-        const uint32_t s_at = tmem + ((uint32_t)((warp % 4) * 32) << 16) + m * 2 * kTile;
+        const int set = warp / 8, m = (warp / 4) % 2;  // the steps and the half that the warp works on
+        const int r_m = threadIdx.x & 127;             // row of the half
+        const uint32_t s_at = tmem + ((uint32_t)((warp % 4) * 32) << 16) + (m * 2 + set) * kTile;
+        auto half_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(2 + m) : "memory"); };
+        RowFactors& rf = row_factors[m];
         uint32_t kt = 0, steps = 0;
         float* part = nullptr;
         if constexpr (SUM) {
             const int64_t row = ((work.b * p.a.cache.H + work.h) * p.groups + work.part) * 2 + m;
             part = p.parts + row * p.part_stride + r_m;
-            if (work.rb0 == work.rb1)  // fewer row blocks than groups
+            if (work.rb0 == work.rb1 && set == 0)  // fewer row blocks than groups
                 for (int tile = work.chunk0; tile < work.chunk1; ++tile) part[(int64_t)tile * kTile] = 0.0f;
         }
         for (int rb = work.rb0; rb < work.rb1; ++rb) {
@@ -463,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
             const bool active = r.t0 < r.t1 && r.rows > 128 * m;
             if constexpr (SUM) {
                 // tiles that the first block does not see begin at 0
-                if (rb == work.rb0)
+                if (rb == work.rb0 && set == 0)
                     for (int tile = work.chunk0; tile < work.chunk1; ++tile)
                         if (!active || tile < r.t0 || tile >= r.t1) part[(int64_t)tile * kTile] = 0.0f;
             }
@@ -476,112 +561,133 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
             const int hi = base + i, lo = p.a.window > 0 ? (int)max(base + i + 1 - p.a.window, (int64_t)0) : 0;
             RowStats stats = {-INFINITY, 0.0f};
             if (active) {
-                // the row goes into its operand tile, scaled to 2^14, permuted as the keys unpack
-                const uint4* src = reinterpret_cast<const uint4*>(p.a.q + (work.seq.q0 + i) * p.a.q_stride + (int64_t)head * D);
-                uint32_t top = 0;
-#pragma unroll 8
-                for (int w = 0; w < D / 8; ++w) {
-                    const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
-                        top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
-                    }
-                }
-                const int e = max((int)(top >> 23), 15) - 127;
-                const float f = p.a.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
-                const float unit = pow2(e - 14) * (fabsf(p.a.scale_log2) * 0x1p24f);
-                const uint32_t dst = smem_at + C::kOffQ + m * (128 * D * 2) + r_m * 128;
-                float q_sum = 0.0f;
+                // The other set may still be at the row block before: its rows' factors, its
+                // operand tile (every product of this half is done once its last two steps
+                // have been waited for, one by each set) and its sums.
+                half_sync();
+                if (set == 0) {
+                    // the row goes into its operand tile, scaled to 2^14, permuted as the keys unpack
+                    const uint4* src =
+                        reinterpret_cast<const uint4*>(p.a.q + (work.seq.q0 + i) * p.a.q_stride + (int64_t)head * D);
+                    uint32_t top = 0;
 #pragma unroll 4
-                for (int w = 0; w < D / 8; ++w) {
-                    const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                    const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
-                                        lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
-                    q_sum += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-                    const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r_m & 7)) << 4);
-                    if constexpr (BITS == 4)
-                        sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1] * 0.0625f, y[5] * 0.0625f), pack_f16(y[2], y[6]),
-                              pack_f16(y[3] * 0.0625f, y[7] * 0.0625f));
-                    else
-                        sts16(at, pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
-                }
-                q_sum *= 0x1p-24f;
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&q_full[m]);
-                if constexpr (SUM) {
-                    float top_m = -INFINITY, l = 0.0f;
-                    if (live) {
-                        for (int s = 0; s < p.splits; ++s) top_m = fmaxf(top_m, p.stats[stat + s].x);
-                        for (int s = 0; s < p.splits; ++s) {
-                            const float2 x = p.stats[stat + s];
-                            l = fmaf(x.y, exp2_approx(x.x - (top_m == -INFINITY ? 0.0f : top_m)), l);
+                    for (int w = 0; w < D / 8; ++w) {
+                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
+                            top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
                         }
                     }
-                    RowFactors& rf = row_factors[m];
-                    asm volatile("bar.sync %0, 128;" ::"r"(2 + m) : "memory");  // the last row block's are read
-                    const bool some = l > 0.0f;
-                    rf.unit[r_m] = some ? unit : 0.0f;
-                    rf.sum[r_m] = some ? unit * q_sum : 0.0f;
-                    rf.minus_n[r_m] = some ? -(top_m + log2f(l)) : -INFINITY;
-                    rf.hi[r_m] = live ? hi : -1;
-                    asm volatile("bar.sync %0, 128;" ::"r"(2 + m) : "memory");
+                    if constexpr (SUM) {
+#pragma unroll
+                        for (int d = 1; d < kGroup; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    }
+                    const int e = max((int)(top >> 23), 15) - 127;
+                    const float f = p.a.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
+                    const float unit = pow2(e - 14) * fabsf(p.a.scale_log2);
+                    const uint32_t dst = smem_at + C::kOffQ + m * C::kQTile + r_m * 128;
+                    float q_sum = 0.0f;
+#pragma unroll 2
+                    for (int w = 0; w < D / 8; ++w) {
+                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+                        const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
+                                            lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
+                        q_sum += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r_m & 7)) << 4);
+                        if constexpr (BITS == 4)
+                            sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]), pack_f16(y[3], y[7]));
+                        else
+                            sts16(at, pack_f16(y[0], y[2]), pack_f16(y[1], y[3]), pack_f16(y[4], y[6]), pack_f16(y[5], y[7]));
+                    }
+                    uint32_t q_hi, q_lo;
+                    split_f16(q_sum * 0.0078125f, q_hi, q_lo);
+                    sts16(dst + C::kPart + ((r_m & 7) << 4), q_hi | q_lo << 16, q_hi, 0, 0);
+                    sts16(dst + C::kPart + ((1 ^ (r_m & 7)) << 4), 0, 0, 0, 0);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&q_full[m]);
+                    rf.unit[r_m] = unit;
+                    if constexpr (SUM) {
+                        float top_m = -INFINITY, l = 0.0f;
+                        if (live) {
+                            for (int s = 0; s < p.splits; ++s) top_m = fmaxf(top_m, p.stats[stat + s].x);
+                            for (int s = 0; s < p.splits; ++s) {
+                                const float2 x = p.stats[stat + s];
+                                l = fmaf(x.y, exp2_approx(x.x - (top_m == -INFINITY ? 0.0f : top_m)), l);
+                            }
+                        }
+                        rf.minus_n[r_m] = l > 0.0f ? -(top_m + log2f(l)) : -INFINITY;
+                        rf.hi[r_m] = live ? hi : -1;
+                    }
                 }
+                half_sync();
+                const float own_unit = SUM ? 1.0f : rf.unit[r_m];
                 // tokens [all_lo, all_hi] are seen by every row of the half
                 const int all_hi = base + (r.row0 + m * 128) / p.a.G;
                 const int last = r.row0 + min(r.rows, m * 128 + 128) - 1;
                 const int all_lo = p.a.window > 0 ? (int)max(base + last / p.a.G + 1 - p.a.window, (int64_t)0) : 0;
                 const int columns = (min(r.rows - m * 128, 128) + 31) / 32;
                 const bool warp_live = SUM || (warp % 4) * 32 < r.rows - m * 128;
-                for (int tile = r.t0; tile < r.t1; ++tile, ++steps) {
-                    const uint32_t k = kt + (tile - r.t0), buf = steps & 1;
+                const uint32_t skip = (steps & 1) ^ set;  // the set's first step
+                for (int tile = r.t0 + (int)skip; tile < r.t1; tile += 2) {
+                    const uint32_t k = kt + (tile - r.t0), step = steps + (tile - r.t0);
                     const int token = tile * kTile;
                     float before = 0.0f;
                     if constexpr (SUM) {
                         if (rb > work.rb0) before = part[(int64_t)tile * kTile];
                     }
-                    // S first: its scales are there then, so one test of their barrier (whose
-                    // earlier rounds a half that sat out a row block has not waited for)
-                    // passes, and acquires them
-                    wait(&s_full[m][buf], (steps / 2) & 1);
-                    const bool there = tc::mbar_test(tc::smem_u32(&info_full[k % kFactors]), (k / kFactors) & 1);
+                    // S first: its exponent is there then, so one test of its barrier (whose
+                    // earlier rounds this set has not waited for) passes, and acquires it
+                    wait(&s_full[m][set], (step / 2) & 1);
+                    const bool there = tc::mbar_test(tc::smem_u32(&info_full[k % kInfo]), (k / kInfo) & 1);
                     tc::tc_fence_after();
                     if (!dead && __all_sync(0xffffffffu, there) && warp_live) {
                         const bool edge = token + kTile - 1 > all_hi || token < all_lo;
-                        const uint32_t at = s_at + buf * kTile;
+                        const float unit = own_unit * pow2(tile_exp[k % kInfo] - 134);
                         if constexpr (SUM) {
-                            const float scale = scales[k % kFactors][r_m], offset = offsets[k % kFactors][r_m];
                             uint64_t sum[2] = {0, 0};
 #pragma unroll 1
                             for (int q = 0; q < columns; ++q) {
                                 if (edge)
-                                    add_rows<true>(sum, at + q * 32, row_factors[m], q * 32, scale, offset, token + r_m, p.a.window);
+                                    add_rows<true>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, p.a.window);
                                 else
-                                    add_rows<false>(sum, at + q * 32, row_factors[m], q * 32, scale, offset, token + r_m, 0);
+                                    add_rows<false>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, 0);
                             }
                             float a, b;
                             split_f32(add_f32x2(sum[0], sum[1]), a, b);
                             part[(int64_t)tile * kTile] = before + (a + b);
+                        } else if (edge) {
+                            stats = add_some_tokens(stats, s_at, unit, token, lo, hi);
                         } else {
 #pragma unroll 1
-                            for (int q = 0; q < kTile / 32; ++q) {
-                                const float* s = &scales[k % kFactors][q * 32];
-                                const float* o = &offsets[k % kFactors][q * 32];
-                                if (edge)
-                                    add_tokens<true>(stats, at + q * 32, s, o, q_sum, unit, token + q * 32, lo, hi);
-                                else
-                                    add_tokens<false>(stats, at + q * 32, s, o, q_sum, unit, token + q * 32, lo, hi);
-                            }
+                            for (int q = 0; q < kTile / 32; ++q) add_tokens(stats, s_at + q * 32, unit);
                         }
                     }
                     tc::tc_fence_before();
-                    tc::mbar_arrive(&s_empty[m][buf]);
+                    tc::mbar_arrive(&s_empty[m][set]);
                 }
+                steps += r.t1 - r.t0;
             }
             kt += max(r.t1 - r.t0, 0);
             if constexpr (!SUM) {
-                if (live && r.rows > 128 * m) p.stats[stat + work.part] = make_float2(stats.ref, stats.sum);
+                // the two sets' sums of a row
+                if (active) half_sync();
+                if (set == 1) {
+                    rf.unit[r_m] = stats.ref;
+                    rf.minus_n[r_m] = stats.sum;
+                }
+                half_sync();
+                if (set == 0 && live) {
+                    RowStats other = {rf.unit[r_m], rf.minus_n[r_m]};
+                    if (other.ref > stats.ref) {
+                        const RowStats swap = stats;
+                        stats = other;
+                        other = swap;
+                    }
+                    if (other.ref > -INFINITY) stats.sum = fmaf(other.sum, exp2_approx(other.ref - stats.ref), stats.sum);
+                    p.stats[stat + work.part] = make_float2(stats.ref, stats.sum);
+                }
             }
         }
     }
