@@ -32,8 +32,8 @@
 // adds those up: no atomics, the same bits whatever the timing.
 //
 // Roles: 16 softmax warps, a set of 8 for the even steps and one for the odd ones, each
-// four warps for a half; 4 warps unpack codes into the swizzled operand tiles, one
-// copies pages, one issues the MMAs.  S is held twice per half (all 512 columns of TMEM):
+// four warps for a half; 8 warps unpack codes into the swizzled operand tiles, four the
+// even tiles and four the odd ones; one copies pages, one issues the MMAs.  S is held twice per half (all 512 columns of TMEM):
 // a set works on one step's while the other's products run.  Operand layout: K-major,
 // 128-byte swizzle, channels in the order in which key words unpack.
 
@@ -51,8 +51,8 @@ namespace {
 constexpr int kTile = kKvPromptTile;  // cache tokens per tile
 constexpr int kRows = kKvPromptRows;  // query rows per block: two halves
 constexpr int kSoftmaxWarps = 16;
-constexpr int kUnpackWarps = 4;
-constexpr int kCopyWarp = kSoftmaxWarps + kUnpackWarps;
+constexpr int kUnpackWarps = 4;  // of a group; one works on the even tiles, one on the odd
+constexpr int kCopyWarp = kSoftmaxWarps + 2 * kUnpackWarps;
 constexpr int kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kRaw = 2;        // raw tiles
@@ -228,7 +228,7 @@ __device__ __noinline__ RowStats add_some_tokens(RowStats r, uint32_t s_at, floa
 
 // What the softmax needs of a half's rows: what a product counts (in log2 units, times
 // the tile's), where rows are columns -n, and the last token that the row sees.
-constexpr int kGroup = 16;  // rows that share a unit where they are columns
+constexpr int kGroup = 16;  // rows that share a unit where they are columns: those a warp takes up
 struct RowFactors {
     float unit[kTile], minus_n[kTile];
     int hi[kTile];
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
     __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages];
     __shared__ uint64_t q_full[2], s_full[2][2], s_empty[2][2], info_full[kInfo], drained;
     __shared__ __align__(16) uint32_t exp_red[2][kUnpackWarps];  // largest magnitudes, as bits
-    __shared__ int tile_exp[kInfo];     // a tile is held times 2^(134 - tile_exp)
-    __shared__ uint32_t factor[kTile];  // a token's scale, twice, as halves
+    __shared__ int tile_exp[kInfo];        // a tile is held times 2^(134 - tile_exp)
+    __shared__ uint32_t factors[2][kTile];  // a token's scale, twice, as halves
     __shared__ __align__(16) RowFactors row_factors[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
             tc::mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&q_full[i], 128);
+            tc::mbar_init(&q_full[i], 256);
             for (int j = 0; j < 2; ++j) {
                 tc::mbar_init(&s_full[i][j], 1);
                 tc::mbar_init(&s_empty[i][j], 128);
@@ -376,21 +376,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
             tc::mbar_wait(&raw_full[k % kRaw], (k / kRaw) & 1, &none, p.a.err);
     } else if (warp >= kSoftmaxWarps && warp < kCopyWarp) {
         // ------------------------------------------------------------ unpacking
-        const int tid = threadIdx.x - kSoftmaxWarps * 32;  // 0 .. 127
-        const int w4 = warp - kSoftmaxWarps;
-        auto unpack_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kUnpackWarps * 32) : "memory"); };
+        const int tid = threadIdx.x & 127;
+        const int w4 = warp % kUnpackWarps;
+        const uint32_t group = (warp - kSoftmaxWarps) / kUnpackWarps;
+        auto unpack_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group * 3 + 1), "n"(kUnpackWarps * 32) : "memory"); };
+        uint32_t* const factor = factors[group];
         constexpr int kLanesPerKey = C::kRowBytes / 16;
         constexpr int kChunks = BITS == 4 ? 4 : 2;  // operand chunks (8 channels) per 16 raw bytes
         constexpr float kMiddle = BITS == 4 ? 8.0f : 136.0f;  // what the products leave of a code
         constexpr float kTop = BITS == 4 ? 8.0f : 128.0f;     // the largest of what they have, in scales
         const int key_lane = tid % kLanesPerKey;
         // of the channels more the second chunk stays 0
-        for (int i = 0; i < kStages; ++i)
+        for (int i = (int)group; i < kStages; i += 2)
             sts16(smem_at + C::kOffK + i * C::kKTile + C::kNibbles * C::kPart + tid * 128 + ((1 ^ (tid & 7)) << 4), 0, 0, 0, 0);
         uint32_t kt = 0;
         for (int rb = work.rb0; rb < work.rb1; ++rb) {
             const Part r = find_part<SUM>(p, work, rb);
             for (int tile = r.t0; tile < r.t1; ++tile, ++kt) {
+                if (kt % 2 != group) continue;
                 const int token = tile * kTile;
                 const uint32_t slot = kt % kRaw, stage = kt % kStages;
                 const uint8_t* raw = smem + C::kOffRaw + slot * C::kRawBytes;
@@ -402,13 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 const float offset = fmaf(kv_scale(pk), kMiddle, kv_low(pk));
                 const uint32_t bits = max(__float_as_uint(kv_scale(pk) * kTop) & 0x7fffffffu, __float_as_uint(offset) & 0x7fffffffu);
                 const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
-                if (lane == 0) exp_red[kt & 1][w4] = top;
-                unpack_sync();  // (and the tile before is done with its factors)
-                const uint4 tops = *reinterpret_cast<const uint4*>(exp_red[kt & 1]);
+                if (lane == 0) exp_red[group][w4] = top;
+                unpack_sync();  // (and the group's tile before is done with its factors)
+                const uint4 tops = *reinterpret_cast<const uint4*>(exp_red[group]);
                 const uint32_t e = max(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23, 8u);
                 const float f = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
                 factor[tid] = pack_f16(kv_scale(pk) * f, kv_scale(pk) * f);
                 // this stage's last products are done: so is the softmax of four tiles ago
+                // (with one stage, round by round: of two rounds on, the parity would pass at once)
+                if (kStages == 1 && kt >= 2) wait(&k_empty[0], kt & 1);
                 wait(&k_empty[stage], ((kt / kStages) & 1) ^ 1);
                 if (tid == 0) tile_exp[kt % kInfo] = (int)e;
                 unpack_sync();
@@ -565,50 +570,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 // operand tile (every product of this half is done once its last two steps
                 // have been waited for, one by each set) and its sums.
                 half_sync();
-                if (set == 0) {
-                    // the row goes into its operand tile, scaled to 2^14, permuted as the keys unpack
-                    const uint4* src =
-                        reinterpret_cast<const uint4*>(p.a.q + (work.seq.q0 + i) * p.a.q_stride + (int64_t)head * D);
-                    uint32_t top = 0;
-#pragma unroll 4
-                    for (int w = 0; w < D / 8; ++w) {
-                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                {
+                    // Rows go into the operand tile, scaled to 2^14, permuted as the keys
+                    // unpack: 16 rows a warp, a lane 8 channels of each of kMine of them.
+                    constexpr int kLanes = D / 8, kSide = 32 / kLanes, kMine = 16 / kSide;
+                    const int first = (set * 4 + warp % 4) * 16, w = lane % kLanes;
+                    uint4 v[kMine];
+                    uint32_t top[kMine];
+#pragma unroll
+                    for (int k = 0; k < kMine; ++k) {
+                        const int row = r.row0 + m * 128 + first + k * kSide + lane / kLanes;
+                        v[k] = make_uint4(0, 0, 0, 0);
+                        if (row < r.row0 + r.rows) {
+                            const int at = row / p.a.G;
+                            v[k] = __ldg(reinterpret_cast<const uint4*>(p.a.q + (work.seq.q0 + at) * p.a.q_stride +
+                                                                       (int64_t)(work.h * p.a.G + row - at * p.a.G) * D) + w);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kMine; ++k) {
+                        const uint32_t words[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        top[k] = 0;  // largest finite magnitude, as bits
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t a = words[j] & 0x7fff0000u, b = (words[j] << 16) & 0x7fff0000u;
-                            top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+                            top[k] = max(top[k], max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
                         }
                     }
-                    if constexpr (SUM) {
+                    if constexpr (SUM) {  // the group's
 #pragma unroll
-                        for (int d = 1; d < kGroup; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        for (int k = 1; k < kMine; ++k) top[0] = max(top[0], top[k]);
+                        top[0] = __reduce_max_sync(0xffffffffu, top[0]);
+#pragma unroll
+                        for (int k = 1; k < kMine; ++k) top[k] = top[0];
+                    } else {
+#pragma unroll
+                        for (int d = 1; d < kLanes; d <<= 1)
+#pragma unroll
+                            for (int k = 0; k < kMine; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
                     }
-                    const int e = max((int)(top >> 23), 15) - 127;
-                    const float f = p.a.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
-                    const float unit = pow2(e - 14) * fabsf(p.a.scale_log2);
-                    const uint32_t dst = smem_at + C::kOffQ + m * C::kQTile + r_m * 128;
-                    float q_sum = 0.0f;
-#pragma unroll 2
-                    for (int w = 0; w < D / 8; ++w) {
-                        const uint4 v = live ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                        const float y[8] = {lo_bf16(v.x) * f, hi_bf16(v.x) * f, lo_bf16(v.y) * f, hi_bf16(v.y) * f,
-                                            lo_bf16(v.z) * f, hi_bf16(v.z) * f, lo_bf16(v.w) * f, hi_bf16(v.w) * f};
-                        q_sum += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (r_m & 7)) << 4);
+#pragma unroll
+                    for (int k = 0; k < kMine; ++k) {
+                        const int row = first + k * kSide + lane / kLanes;  // of the half
+                        const int e = max((int)(top[k] >> 23), 15) - 127;
+                        const float f = p.a.scale_log2 < 0.0f ? -pow2(14 - e) : pow2(14 - e);
+                        const float y[8] = {lo_bf16(v[k].x) * f, hi_bf16(v[k].x) * f, lo_bf16(v[k].y) * f, hi_bf16(v[k].y) * f,
+                                            lo_bf16(v[k].z) * f, hi_bf16(v[k].z) * f, lo_bf16(v[k].w) * f, hi_bf16(v[k].w) * f};
+                        float q_sum = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+#pragma unroll
+                        for (int d = 1; d < kLanes; d <<= 1) q_sum += __shfl_xor_sync(0xffffffffu, q_sum, d);
+                        const uint32_t dst = smem_at + C::kOffQ + m * C::kQTile + row * 128;
+                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (row & 7)) << 4);
                         if constexpr (BITS == 4)
                             sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]), pack_f16(y[3], y[7]));
                         else
                             sts16(at, pack_f16(y[0], y[2]), pack_f16(y[1], y[3]), pack_f16(y[4], y[6]), pack_f16(y[5], y[7]));
+                        if (w < 2) {  // of the channels more: the sum's parts, and zeros
+                            uint32_t q_hi, q_lo;
+                            split_f16(q_sum * 0.0078125f, q_hi, q_lo);
+                            sts16(dst + C::kPart + ((w ^ (row & 7)) << 4), w ? 0 : q_hi | q_lo << 16, w ? 0 : q_hi, 0, 0);
+                        }
+                        if (w == 0) rf.unit[row] = pow2(e - 14) * fabsf(p.a.scale_log2);
                     }
-                    uint32_t q_hi, q_lo;
-                    split_f16(q_sum * 0.0078125f, q_hi, q_lo);
-                    sts16(dst + C::kPart + ((r_m & 7) << 4), q_hi | q_lo << 16, q_hi, 0, 0);
-                    sts16(dst + C::kPart + ((1 ^ (r_m & 7)) << 4), 0, 0, 0, 0);
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&q_full[m]);
-                    rf.unit[r_m] = unit;
-                    if constexpr (SUM) {
+                    if (SUM && set == 0) {
                         float top_m = -INFINITY, l = 0.0f;
                         if (live) {
                             for (int s = 0; s < p.splits; ++s) top_m = fmaxf(top_m, p.stats[stat + s].x);
