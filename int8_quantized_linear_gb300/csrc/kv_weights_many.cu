@@ -55,7 +55,6 @@ constexpr int kUnpackWarps = 4;  // of a group; one works on the even tiles, one
 constexpr int kCopyWarp = kSoftmaxWarps + 2 * kUnpackWarps;
 constexpr int kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kRaw = 2;        // raw tiles
 constexpr int kInfo = 4;       // tiles whose exponents are kept
 constexpr float kSlack = 8.0f; // a row's maximum may exceed what its sum is relative to by this (log2)
 
@@ -63,15 +62,20 @@ template <int D, int BITS>
 struct Cfg {
     static constexpr int kRowBytes = D * BITS / 8;
     static constexpr int kNibbles = BITS / 4;
-    static constexpr int kStages = D == 128 && BITS == 8 ? 1 : 2;  // unpacked tiles
-    static constexpr int kMore = kTile * 128;  // a tile of the 16 channels more (of a swizzle atom's 64)
+    // Unpacked tiles, and raw ones: even numbers, of which each unpacking group has its own
+    // (a group that skipped rounds of a barrier could not tell them apart), or one, with one group.
+    static constexpr int kStages = D == 128 && BITS == 8 ? 1 : 2;
+    static constexpr int kRaw = D == 128 && BITS == 8 ? 2 : 4;
     static constexpr int kPart = kTile * D * 2;
-    static constexpr int kKTile = kNibbles * kPart + kMore;
-    static constexpr int kQTile = kPart + kMore;  // 128 rows
+    static constexpr int kKTile = kNibbles * kPart;
+    // the 16 channels more: a swizzle atom's 64 channels hold those of four tiles, or of both halves of Q
+    static constexpr int kMore = kTile * 128;
     static constexpr int kRawBytes = kTile * kRowBytes + kTile * 4;
-    static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + 2 * kQTile;
-    static constexpr int kOffRaw = kOffK + kStages * kKTile;
+    static constexpr int kOffQ = 0;  // [halves]
+    static constexpr int kOffMoreQ = kOffQ + 2 * kPart;
+    static constexpr int kOffK = kOffMoreQ + kMore;
+    static constexpr int kOffMoreK = kOffK + kStages * kKTile;
+    static constexpr int kOffRaw = kOffMoreK + kMore;
     // (at least what keeps a second block, which would wait for TMEM, off the SM)
     static constexpr int kSmem = std::max(kOffRaw + kRaw * kRawBytes + 1024, 116 * 1024);
 };
@@ -168,26 +172,30 @@ __device__ __forceinline__ void raise(RowStats& r, float to) {
     r.ref = to;
 }
 
-// 32 columns of S of a row, all of them tokens that it sees.
+// A tile of S of a row that sees all its tokens.  The exponents are relative to what the
+// sum is: where one exceeds the slack (rare: the first time, and then as larger logits
+// come), the reference is raised and all is done again.  (Asked once a tile: a vote
+// after every 32 columns keeps the next ones from being loaded, 295 against 221 us for
+// the softmax alone of two chunks of 2048 tokens over 8192.)
 __device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, float unit) {
-    uint32_t x[32];
-    tmem_ld32(s_at, x);
     const uint64_t u2 = pair_f32(unit, unit);
-    tc::tmem_wait_ld();
-    // The exponents relative to what the sum is: where one exceeds the slack (rare: the
-    // first time, and then as larger logits come), the reference is raised and all is
-    // done again.
     for (bool again = r.ref == -INFINITY;;) {
         const float ref = r.ref == -INFINITY ? 0.0f : -r.ref;
         const uint64_t ref2 = pair_f32(ref, ref);
         uint64_t sum[2] = {0, 0};
         float high[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int q = 0; q < kTile / 32; ++q) {
+            uint32_t x[32];
+            tmem_ld32(s_at + q * 32, x);
+            tc::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            float y, z;
-            split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), u2, ref2), y, z);
-            high[(j / 2) & 1] = max3(high[(j / 2) & 1], y, z);
-            sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(exp2_approx(y), exp2_approx(z)));
+            for (int j = 0; j < 32; j += 2) {
+                float y, z;
+                split_f32(fma_f32x2(pair_u32(x[j], x[j + 1]), u2, ref2), y, z);
+                high[(j / 2) & 1] = max3(high[(j / 2) & 1], y, z);
+                sum[(j / 2) & 1] = add_f32x2(sum[(j / 2) & 1], pair_f32(exp2_approx(y), exp2_approx(z)));
+            }
         }
         const float top = fmaxf(high[0], high[1]);
         again = again || top > kSlack;
@@ -272,7 +280,7 @@ __device__ __forceinline__ void split_f16(float x, uint32_t& hi, uint32_t& lo) {
 template <int D, int BITS, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWeightsParams p) {
     using C = Cfg<D, BITS>;
-    constexpr int kStages = C::kStages;
+    constexpr int kStages = C::kStages, kRaw = C::kRaw;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages];
     __shared__ uint64_t q_full[2], s_full[2][2], s_empty[2][2], info_full[kInfo], drained;
@@ -386,14 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
         constexpr float kMiddle = BITS == 4 ? 8.0f : 136.0f;  // what the products leave of a code
         constexpr float kTop = BITS == 4 ? 8.0f : 128.0f;     // the largest of what they have, in scales
         const int key_lane = tid % kLanesPerKey;
-        // of the channels more the second chunk stays 0
+        // of a tile's 16 channels more the second eight stay 0
         for (int i = (int)group; i < kStages; i += 2)
-            sts16(smem_at + C::kOffK + i * C::kKTile + C::kNibbles * C::kPart + tid * 128 + ((1 ^ (tid & 7)) << 4), 0, 0, 0, 0);
+            sts16(smem_at + C::kOffMoreK + tid * 128 + (((2 * i + 1) ^ (tid & 7)) << 4), 0, 0, 0, 0);
         uint32_t kt = 0;
         for (int rb = work.rb0; rb < work.rb1; ++rb) {
             const Part r = find_part<SUM>(p, work, rb);
             for (int tile = r.t0; tile < r.t1; ++tile, ++kt) {
-                if (kt % 2 != group) continue;
+                if (group != (kStages == 1 ? 0 : kt % 2)) continue;
                 const int token = tile * kTile;
                 const uint32_t slot = kt % kRaw, stage = kt % kStages;
                 const uint8_t* raw = smem + C::kOffRaw + slot * C::kRawBytes;
@@ -412,8 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 const float f = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
                 factor[tid] = pack_f16(kv_scale(pk) * f, kv_scale(pk) * f);
                 // this stage's last products are done: so is the softmax of four tiles ago
-                // (with one stage, round by round: of two rounds on, the parity would pass at once)
-                if (kStages == 1 && kt >= 2) wait(&k_empty[0], kt & 1);
                 wait(&k_empty[stage], ((kt / kStages) & 1) ^ 1);
                 if (tid == 0) tile_exp[kt % kInfo] = (int)e;
                 unpack_sync();
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     {
                         uint32_t o_hi, o_lo;
                         split_f16(offset * f * 128.0f, o_hi, o_lo);
-                        sts16(dst + C::kNibbles * C::kPart + tid * 128 + ((tid & 7) << 4), o_hi | o_hi << 16, o_lo, 0, 0);
+                        sts16(smem_at + C::kOffMoreK + tid * 128 + (((2 * stage) ^ (tid & 7)) << 4), o_hi | o_hi << 16, o_lo, 0, 0);
                     }
 #pragma unroll 1
                     for (int i = 0; i < kLanesPerKey; ++i) {
@@ -468,64 +474,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMAs
-        const uint32_t idesc = tc::f16_idesc(kTile);
         const uint32_t q_base = (uint32_t)tc::sw128_desc(smem_at + C::kOffQ);
         const uint32_t k_base = (uint32_t)tc::sw128_desc(smem_at + C::kOffK);
-        const uint32_t high = (uint32_t)(tc::sw128_desc(smem_at) >> 32);
-        uint32_t kt = 0, items[2] = {0, 0}, steps[2] = {0, 0};
+        const uint32_t more_q = (uint32_t)tc::sw128_desc(smem_at + C::kOffMoreQ);
+        const uint32_t more_k = (uint32_t)tc::sw128_desc(smem_at + C::kOffMoreK);
+        const uint32_t high = (uint32_t)(tc::sw128_desc(smem_at) >> 32), idesc = tc::f16_idesc(kTile);
+        // All channels of a half and a stage's tile.
+        auto product = [&](uint32_t d, uint32_t m, uint32_t stage, uint32_t issue) {
+            const uint32_t q = q_base + m * (C::kPart / 16), k = k_base + stage * (C::kKTile / 16);
+            const uint32_t a = SUM ? k : q, b = SUM ? q : k;
+            constexpr int kNext = 128 * 128 / 16;  // the second 64 channels
+            constexpr int kHigh = C::kPart / 16;   // the high nibbles, beside the same Q
+            constexpr int A = SUM ? kHigh : 0, B = SUM ? 0 : kHigh;
+            __syncwarp();
+            mma_ss<0, 0>(d, a, b, high, idesc, 0, issue);
+            mma_ss<2, 2>(d, a, b, high, idesc, 1, issue);
+            mma_ss<4, 4>(d, a, b, high, idesc, 1, issue);
+            mma_ss<6, 6>(d, a, b, high, idesc, 1, issue);
+            if constexpr (D == 128) {
+                mma_ss<kNext, kNext>(d, a, b, high, idesc, 1, issue);
+                mma_ss<kNext + 2, kNext + 2>(d, a, b, high, idesc, 1, issue);
+                mma_ss<kNext + 4, kNext + 4>(d, a, b, high, idesc, 1, issue);
+                mma_ss<kNext + 6, kNext + 6>(d, a, b, high, idesc, 1, issue);
+            }
+            if constexpr (BITS == 8) {
+                mma_ss<A, B>(d, a, b, high, idesc, 1, issue);
+                mma_ss<A + 2, B + 2>(d, a, b, high, idesc, 1, issue);
+                mma_ss<A + 4, B + 4>(d, a, b, high, idesc, 1, issue);
+                mma_ss<A + 6, B + 6>(d, a, b, high, idesc, 1, issue);
+                if constexpr (D == 128) {
+                    mma_ss<A + kNext, B + kNext>(d, a, b, high, idesc, 1, issue);
+                    mma_ss<A + kNext + 2, B + kNext + 2>(d, a, b, high, idesc, 1, issue);
+                    mma_ss<A + kNext + 4, B + kNext + 4>(d, a, b, high, idesc, 1, issue);
+                    mma_ss<A + kNext + 6, B + kNext + 6>(d, a, b, high, idesc, 1, issue);
+                }
+            }
+            const uint32_t mq = more_q + 2 * m, mk = more_k + 2 * stage;
+            mma_ss<0, 0>(d, SUM ? mk : mq, SUM ? mq : mk, high, idesc, 1, issue);
+        };
+        // (Every step of half 0 is a tile, and so is every one of half 1, which only the last
+        // row block may leave out: the tile's number says all.)
+        uint32_t kt = 0, item = 0;
         for (int rb = work.rb0; rb < work.rb1; ++rb) {
             const Part r = find_part<SUM>(p, work, rb);
             if (r.t0 >= r.t1) continue;
-            const int halves = r.rows > 128 ? 2 : 1;
-            for (int m = 0; m < halves; ++m) {
-                wait(&q_full[m], items[m] & 1);
-                ++items[m];
-            }
-            // A half that sits out is done with its last tiles (one of each set), whose scales
-            // the tiles to come would overwrite (one that takes part says so with its Q).
-            for (uint32_t i = 1; halves == 1 && i <= min(steps[1], 2u); ++i)
-                wait(&s_empty[1][(steps[1] - i) & 1], ((steps[1] - i) / 2) & 1);
+            const bool both = r.rows > 128;
+            wait(&q_full[0], item & 1);
+            if (both) wait(&q_full[1], item & 1);
+            ++item;
+            // A half that sits out is done with its last tiles (one of each set), whose
+            // exponents the tiles to come would overwrite (one that takes part says so with its Q).
+            for (uint32_t i = 1; !both && i <= min(kt, 2u); ++i) wait(&s_empty[1][(kt - i) & 1], ((kt - i) / 2) & 1);
             for (int tile = r.t0; tile < r.t1; ++tile, ++kt) {
-                wait(&k_full[kt % kStages], (kt / kStages) & 1);
-                for (int m = 0; m < halves; ++m, __syncwarp()) {
-                    const uint32_t buf = steps[m] & 1;
-                    wait(&s_empty[m][buf], ((steps[m] / 2) & 1) ^ 1);
-                    ++steps[m];
+                const uint32_t stage = kt % kStages, buf = kt % 2, round = (kt / 2) & 1;
+                wait(&k_full[stage], (kt / kStages) & 1);
+                const uint32_t d = tmem + buf * (2 * kTile);
+                wait(&s_empty[0][buf], round ^ 1);
+                tc::tc_fence_after();
+                product(d, 0, stage, !dead && lane == 0);
+                commit_mma(&s_full[0][buf], !dead && lane == 0);
+                if (both) {
+                    wait(&s_empty[1][buf], round ^ 1);
                     tc::tc_fence_after();
-                    const uint32_t q = q_base + m * (C::kQTile / 16), k = k_base + (kt % kStages) * (C::kKTile / 16);
-                    const uint32_t a = SUM ? k : q, b = SUM ? q : k;
-                    const uint32_t d = tmem + (m * 2 + buf) * kTile, issue = !dead && lane == 0;
-                    constexpr int kNext = 128 * 128 / 16;  // the second 64 channels
-                    constexpr int kHigh = C::kPart / 16;   // the high nibbles, beside the same Q
-                    constexpr int kMoreK = C::kNibbles * C::kPart / 16, kMoreQ = C::kPart / 16;
-                    __syncwarp();
-                    mma_ss<0, 0>(d, a, b, high, idesc, 0, issue);
-                    mma_ss<2, 2>(d, a, b, high, idesc, 1, issue);
-                    mma_ss<4, 4>(d, a, b, high, idesc, 1, issue);
-                    mma_ss<6, 6>(d, a, b, high, idesc, 1, issue);
-                    if constexpr (D == 128) {
-                        mma_ss<kNext, kNext>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<kNext + 2, kNext + 2>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<kNext + 4, kNext + 4>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<kNext + 6, kNext + 6>(d, a, b, high, idesc, 1, issue);
-                    }
-                    if constexpr (BITS == 8) {
-                        constexpr int A = SUM ? kHigh : 0, B = SUM ? 0 : kHigh;
-                        mma_ss<A, B>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<A + 2, B + 2>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<A + 4, B + 4>(d, a, b, high, idesc, 1, issue);
-                        mma_ss<A + 6, B + 6>(d, a, b, high, idesc, 1, issue);
-                        if constexpr (D == 128) {
-                            mma_ss<A + kNext, B + kNext>(d, a, b, high, idesc, 1, issue);
-                            mma_ss<A + kNext + 2, B + kNext + 2>(d, a, b, high, idesc, 1, issue);
-                            mma_ss<A + kNext + 4, B + kNext + 4>(d, a, b, high, idesc, 1, issue);
-                            mma_ss<A + kNext + 6, B + kNext + 6>(d, a, b, high, idesc, 1, issue);
-                        }
-                    }
-                    mma_ss<SUM ? kMoreK : kMoreQ, SUM ? kMoreQ : kMoreK>(d, a, b, high, idesc, 1, issue);
-                    commit_mma(&s_full[m][buf], issue);
+                    product(d + kTile, 1, stage, !dead && lane == 0);
+                    commit_mma(&s_full[1][buf], !dead && lane == 0);
                 }
-                commit_mma(&k_empty[kt % kStages], !dead && lane == 0);
+                __syncwarp();
+                commit_mma(&k_empty[stage], !dead && lane == 0);
             }
         }
         // nothing may be in flight when the TMEM is given back
@@ -537,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
         // ------------------------------------------------------------ softmax
         const int set = warp / 8, m = (warp / 4) % 2;  // the steps and the half that the warp works on
         const int r_m = threadIdx.x & 127;             // row of the half
-        const uint32_t s_at = tmem + ((uint32_t)((warp % 4) * 32) << 16) + (m * 2 + set) * kTile;
+        const uint32_t s_at = tmem + ((uint32_t)((warp % 4) * 32) << 16) + (set * 2 + m) * kTile;
         auto half_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(2 + m) : "memory"); };
         RowFactors& rf = row_factors[m];
-        uint32_t kt = 0, steps = 0;
+        uint32_t kt = 0;
         float* part = nullptr;
         if constexpr (SUM) {
             const int64_t row = ((work.b * p.a.cache.H + work.h) * p.groups + work.part) * 2 + m;
@@ -619,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         float q_sum = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
 #pragma unroll
                         for (int d = 1; d < kLanes; d <<= 1) q_sum += __shfl_xor_sync(0xffffffffu, q_sum, d);
-                        const uint32_t dst = smem_at + C::kOffQ + m * C::kQTile + row * 128;
-                        const uint32_t at = dst + (w / 8) * (128 * 128) + (((w & 7) ^ (row & 7)) << 4);
+                        const uint32_t at = smem_at + C::kOffQ + m * C::kPart + (w / 8) * (128 * 128) + row * 128 +
+                                            (((w & 7) ^ (row & 7)) << 4);
                         if constexpr (BITS == 4)
                             sts16(at, pack_f16(y[0], y[4]), pack_f16(y[1], y[5]), pack_f16(y[2], y[6]), pack_f16(y[3], y[7]));
                         else
@@ -628,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         if (w < 2) {  // of the channels more: the sum's parts, and zeros
                             uint32_t q_hi, q_lo;
                             split_f16(q_sum * 0.0078125f, q_hi, q_lo);
-                            sts16(dst + C::kPart + ((w ^ (row & 7)) << 4), w ? 0 : q_hi | q_lo << 16, w ? 0 : q_hi, 0, 0);
+                            sts16(smem_at + C::kOffMoreQ + row * 128 + (((2 * m + w) ^ (row & 7)) << 4), w ? 0 : q_hi | q_lo << 16,
+                                  w ? 0 : q_hi, 0, 0);
                         }
                         if (w == 0) rf.unit[row] = pow2(e - 14) * fabsf(p.a.scale_log2);
                     }
@@ -655,9 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 const int all_lo = p.a.window > 0 ? (int)max(base + last / p.a.G + 1 - p.a.window, (int64_t)0) : 0;
                 const int columns = (min(r.rows - m * 128, 128) + 31) / 32;
                 const bool warp_live = SUM || (warp % 4) * 32 < r.rows - m * 128;
-                const uint32_t skip = (steps & 1) ^ set;  // the set's first step
-                for (int tile = r.t0 + (int)skip; tile < r.t1; tile += 2) {
-                    const uint32_t k = kt + (tile - r.t0), step = steps + (tile - r.t0);
+                for (int tile = r.t0 + (int)((kt & 1) ^ set); tile < r.t1; tile += 2) {
+                    const uint32_t k = kt + (tile - r.t0);
                     const int token = tile * kTile;
                     float before = 0.0f;
                     if constexpr (SUM) {
@@ -665,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     }
                     // S first: its exponent is there then, so one test of its barrier (whose
                     // earlier rounds this set has not waited for) passes, and acquires it
-                    wait(&s_full[m][set], (step / 2) & 1);
+                    wait(&s_full[m][set], (k / 2) & 1);
                     const bool there = tc::mbar_test(tc::smem_u32(&info_full[k % kInfo]), (k / kInfo) & 1);
                     tc::tc_fence_after();
                     if (!dead && __all_sync(0xffffffffu, there) && warp_live) {
@@ -686,14 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         } else if (edge) {
                             stats = add_some_tokens(stats, s_at, unit, token, lo, hi);
                         } else {
-#pragma unroll 1
-                            for (int q = 0; q < kTile / 32; ++q) add_tokens(stats, s_at + q * 32, unit);
+                            add_tokens(stats, s_at, unit);
                         }
                     }
                     tc::tc_fence_before();
                     tc::mbar_arrive(&s_empty[m][set]);
                 }
-                steps += r.t1 - r.t0;
             }
             kt += max(r.t1 - r.t0, 0);
             if constexpr (!SUM) {
