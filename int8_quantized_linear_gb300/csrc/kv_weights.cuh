@@ -41,6 +41,8 @@ struct KvEvictParams {
     int64_t B;
     int budget, first, last;
     int row_bytes;  // of codes
+    int cluster;    // CTAs that choose a sequence's head together
+    bool cached;    // their shared memory holds the keys of as many tokens as the table has
     int chunks;     // blocks of rows of a sequence's head
     unsigned* err;
 };

@@ -252,8 +252,10 @@ def test_binding_refusals():
         with pytest.raises(TypeError, match=name):
             capi.kv_cache_weights(**{**ok, name: bad})
     small = torch.empty(15, dtype=torch.uint8, device="cuda")
+    many = {**ok, "q": torch.zeros((40, 4, 64), dtype=torch.bfloat16, device="cuda")}
     with pytest.raises(capi.I8qlError):
-        capi.kv_cache_weights(**ok, q_offsets=torch.zeros(3, dtype=torch.int32, device="cuda"), max_q=2, workspace=small)
+        capi.kv_cache_weights(**many, q_offsets=torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda"), max_q=20,
+                              workspace=small)
     ok = {"codes": codes, "params": params, "weights": w, "page_table": table, "kv_lens": lens, "budget": 8}
     for name, bad in (("weights", w[:5]), ("page_table", lens), ("new_table", lens), ("budget", 0), ("new_table", table[:1]),
                       ("new_lens", lens[:1]), ("weights", w.cpu()), ("codes", codes[0])):
