@@ -28,6 +28,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv_common.cuh"
 #include "quant_math.cuh"
 #include "rotary.cuh"
@@ -41,6 +43,9 @@ constexpr int kKvThreads = 128;
 constexpr int kKvChannels = 16;  // channels per thread
 constexpr int kKvRows = 2;       // rows per thread: a token's key and value of a head
 constexpr unsigned kKvOneWave = 1024;  // blocks that surely run at once
+// Rotated store: query heads a group of lanes takes, and the threads an SM from which on it does.
+constexpr int kQueries = 4;
+constexpr int kManyThreads = 16384;
 
 struct KvMoveParams {
     KvCache cache;
@@ -243,24 +248,26 @@ struct KvRotaryParams {
     int64_t q_out_stride;
     RotaryTable table;
     int q_heads;
-    int heads;  // of a token: q_heads, then the cache's
-    uint32_t rows;  // T x heads
+    int q_units;  // groups of query heads of a token
+    int units;    // of a token: those, then the cache's heads
+    uint32_t rows;  // T x units
 };
 
-// A group of D / 16 lanes takes one query head of a token, or the key and the value
+// A group of D / 16 lanes takes QUERIES query heads of a token, or the key and the value
 // of a cache head.
-template <int D, int BITS, bool INTERLEAVED>
+template <int D, int BITS, bool INTERLEAVED, int QUERIES>
 __global__ void __launch_bounds__(kKvThreads) kv_store_rotary_kernel(const KvRotaryParams r, const KvMoveParams p) {
-    constexpr int kLanes = D / kKvChannels;
+    constexpr int kLanes = D / kKvChannels, kMost = QUERIES > kKvRows ? QUERIES : kKvRows;
     const int lane = threadIdx.x % kLanes;
     const uint32_t row = blockIdx.x * (kKvThreads / kLanes) + threadIdx.x / kLanes;
     const bool there = row < r.rows;
-    const uint32_t t = there ? row / (uint32_t)r.heads : 0;
-    const int head = there ? (int)(row - t * (uint32_t)r.heads) : 0;
-    const int h = head - r.q_heads;  // < 0: a query
+    const uint32_t t = there ? row / (uint32_t)r.units : 0;
+    const int unit = there ? (int)(row - t * (uint32_t)r.units) : 0;
+    const int h = unit - r.q_units;  // < 0: queries
+    const int q0 = unit * QUERIES;
     const RotaryChunks<4, INTERLEAVED> at(lane, D, r.table.rot);
     pdl_wait();
-    uint32_t w[kKvRows][2][4] = {};
+    uint32_t w[kMost][2][4] = {};
     int64_t slot = -1;
     auto load = [&](const uint16_t* src, uint32_t (&x)[2][4]) {
         const uint4 a = *(reinterpret_cast<const uint4*>(src) + at.a), b = *(reinterpret_cast<const uint4*>(src) + at.b);
@@ -268,24 +275,47 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_rotary_kernel(const KvRot
         x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
     };
     auto word4 = [](const uint32_t (&x)[4]) { return make_uint4(x[0], x[1], x[2], x[3]); };
+    RotaryAngles<4, INTERLEAVED> angle;
+    bool turned = false;
     if (there) {
         if (h < 0) {
-            load(r.q + t * r.q_stride + (int64_t)head * D, w[0]);
+#pragma unroll
+            for (int i = 0; i < QUERIES; ++i)
+                if (q0 + i < r.q_heads) load(r.q + t * r.q_stride + (int64_t)(q0 + i) * D, w[i]);
         } else {
             load(r.k + t * r.k_stride + (int64_t)h * D, w[0]);
             load(r.v + t * r.v_stride + (int64_t)h * D, w[1]);
             slot = __ldg(p.slots + t);
         }
         const float* angles = rotary_row(r.table, t, p.err);
-        if (angles != nullptr && at.angle >= 0) {
-            RotaryAngles<4, INTERLEAVED> angle;
+        turned = angles != nullptr && at.angle >= 0;
+        if (turned) {
             angle.load(angles, r.table.rot, at, false);
             angle.turn(w[0][0], w[0][1], at.b_turned);
         }
-        if (h < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)head * D);
-            dst[at.a] = word4(w[0][0]);
-            dst[at.b] = word4(w[0][1]);
+    }
+    if (__all_sync(0xffffffffu, !there || h < 0)) {  // nothing to quantize
+        if (!there) return;
+#pragma unroll
+        for (int i = 0; i < QUERIES; ++i) {
+            if (q0 + i >= r.q_heads) break;
+            if (i > 0 && turned) angle.turn(w[i][0], w[i][1], at.b_turned);
+            uint4* dst = reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)(q0 + i) * D);
+            dst[at.a] = word4(w[i][0]);
+            dst[at.b] = word4(w[i][1]);
+        }
+        return;
+    }
+    if (there && h < 0) {
+#pragma unroll 1
+        for (int i = 0; i < QUERIES; ++i) {
+            if (q0 + i >= r.q_heads) break;
+            uint32_t x[2][4];
+            load(r.q + t * r.q_stride + (int64_t)(q0 + i) * D, x);
+            if (turned) angle.turn(x[0], x[1], at.b_turned);
+            uint4* dst = reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)(q0 + i) * D);
+            dst[at.a] = word4(x[0]);
+            dst[at.b] = word4(x[1]);
         }
     }
     KvMoveRow place = {there && h >= 0, t, (uint32_t)max(h, 0)};
@@ -435,17 +465,25 @@ cudaError_t launch_kv_store_rotary(const uint16_t* q, int64_t q_stride, uint16_t
                                    const KvCache& cache, int64_t T, int64_t q_heads, int64_t D, int64_t bits,
                                    const LaunchEnv& env) {
     const KvMoveParams p = move_params(cache, slots, T, env);
-    KvRotaryParams r = {q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, table, (int)q_heads,
-                        (int)q_heads + cache.H, 0};
-    r.rows = (uint32_t)(T * r.heads);
+    KvRotaryParams r = {q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, table, (int)q_heads, 0, 0, 0};
     auto pick = [&](auto narrow4, auto narrow8, auto wide4, auto wide8) {
         return D == 64 ? (bits == 4 ? narrow4 : narrow8) : (bits == 4 ? wide4 : wide8);
     };
-    auto kernel = interleaved ? pick(kv_store_rotary_kernel<64, 4, true>, kv_store_rotary_kernel<64, 8, true>,
-                                     kv_store_rotary_kernel<128, 4, true>, kv_store_rotary_kernel<128, 8, true>)
-                              : pick(kv_store_rotary_kernel<64, 4, false>, kv_store_rotary_kernel<64, 8, false>,
-                                     kv_store_rotary_kernel<128, 4, false>, kv_store_rotary_kernel<128, 8, false>);
-    return launch_kernel(kernel, move_grid(r.rows, D), dim3(kKvThreads), 0, env.stream, kNoCluster, r, p);
+    auto launch = [&](auto queries) {
+        constexpr int Q = decltype(queries)::value;
+        r.q_units = ((int)q_heads + Q - 1) / Q;
+        r.units = r.q_units + cache.H;
+        r.rows = (uint32_t)(T * r.units);
+        auto kernel = interleaved ? pick(kv_store_rotary_kernel<64, 4, true, Q>, kv_store_rotary_kernel<64, 8, true, Q>,
+                                         kv_store_rotary_kernel<128, 4, true, Q>, kv_store_rotary_kernel<128, 8, true, Q>)
+                                  : pick(kv_store_rotary_kernel<64, 4, false, Q>, kv_store_rotary_kernel<64, 8, false, Q>,
+                                         kv_store_rotary_kernel<128, 4, false, Q>, kv_store_rotary_kernel<128, 8, false, Q>);
+        return launch_kernel(kernel, move_grid(r.rows, D), dim3(kKvThreads), 0, env.stream, kNoCluster, r, p);
+    };
+    // several query heads a group of lanes, which share the angles, where enough groups are left
+    if (T * (q_heads + cache.H) * (D / kKvChannels) >= (int64_t)kManyThreads * env.sm_count)
+        return launch(std::integral_constant<int, kQueries>{});
+    return launch(std::integral_constant<int, 1>{});
 }
 
 }  // namespace i8ql
