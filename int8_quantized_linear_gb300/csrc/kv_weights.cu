@@ -40,7 +40,7 @@ namespace {
 constexpr int kTile = 128;   // tokens a block works on at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 8;    // most tiles of a block of the second kernel
+constexpr int kChunk = 32;   // most tiles of a block of the second kernel
 template <int D, int BITS>
 constexpr int kStages = D * BITS == 128 * 8 ? 3 : 4;
 // All in one:
@@ -799,8 +799,10 @@ struct WeightsPlan {
     size_t smem;  // of the logits
 };
 
-// Shared memory of the logits that lets two blocks run on an SM.
-constexpr size_t kMostLogits = 64 * 1024;
+// Shared memory of the logits up to which four blocks run on an SM, and two: with fewer the
+// two kernels are quicker.
+constexpr size_t kFewLogits = 36 * 1024;
+constexpr size_t kMostLogits = 72 * 1024;
 
 WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms) {
     WeightsPlan w = {};
@@ -809,11 +811,16 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
     const int64_t blocks = (rows + 8 * w.halves - 1) / (8 * w.halves), tiles = (max_kv + kTile - 1) / kTile;
     const int64_t wanted = 8 * (int64_t)sms, base = std::max<int64_t>(B * H * blocks, 1);
     const int64_t one_tiles = (max_kv + kOneTile - 1) / kOneTile;
+    // One launch: 96 sequences of 16384 tokens (4 bits, 8 x 128, four queries a head) 249 us
+    // with 8 CTAs a cluster and 277 with 4; 48 of 32768, twice the logits a CTA, 283, and 450
+    // by the two kernels; 64 of 4096 with 16 rows 72 and 124.  With more rows its registers
+    // leave one block an SM: only where there is no more.
     for (int64_t size = 1; size <= 8 && blocks == 1; size *= 2) {
         const int64_t chunk = (one_tiles + size - 1) / size;
         const size_t smem = (size_t)((rows + 1) / 2) * (size_t)(chunk * kOneTile + 8) * sizeof(float2);
-        if (smem > kMostLogits) continue;
+        if (smem > (size < 8 ? kFewLogits : kMostLogits)) continue;
         if (size < 8 && base * size < wanted && size < one_tiles) continue;
+        if (w.halves == 4 && base * size > 2 * sms) break;
         w.fused = true;
         w.splits = (int)size;
         w.chunk = (int)chunk;

@@ -23,7 +23,7 @@ struct KvWeightsParams {
 
 // Query rows of a cache head from which the kernels for many of them (kv_weights_many.cu)
 // take over.
-constexpr int64_t kKvWeightsFewRows = 32;
+constexpr int64_t kKvWeightsFewRows = 64;
 size_t kv_weights_many_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
 bool kv_weights_many_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
 cudaError_t launch_kv_weights_many(KvWeightsParams p, int64_t D, int64_t bits, void* workspace, const LaunchEnv& env);
