@@ -4,13 +4,19 @@ int8 weight-only projections (``w8a16_gemm``), keys and values quantized into
 a paged 4- or 8-bit cache as the fused projection produces them
 (``kv_cache_store``, straight from its rows), attention over the cache
 (``kv_cache_attention``) for prompt chunks and single tokens in one batch, and
-the output projection.  Rotary or other position encodings are the caller's:
-they act on the q and k slices between the projection and the store.
+the output projection.  With ``rotary`` the queries and keys are turned by their
+positions as they are stored (``kv_cache_store_rotary``, from a table made by
+``rotary_table``); other position encodings are the caller's: they act on the q
+and k slices between the projection and the store.  With ``budget`` a sequence
+keeps at most that many tokens: the block sums up how much attention each gets
+(``kv_cache_weights``) and after a step that left more drops those that got least
+(``kv_cache_evict``).
 
     python examples/attention_block.py
 
 runs a prompt of two sequences and a few decode steps, reads the cache back
-(``kv_cache_load``) and compares with plain attention over what it reads.
+(``kv_cache_load``) and compares with plain attention over what it reads; then
+the same with rotary positions and contexts cut to a budget.
 """
 
 from __future__ import annotations
@@ -29,7 +35,9 @@ class AttentionBlock:
     """Projections, a pool of cache pages, and the sequences living in it."""
 
     def __init__(self, hidden, q_heads, heads, head_dim, *, bits=4, pages=64, page_size=64, max_tokens=4096, seed=0,
-                 device="cuda"):
+                 rotary=None, budget=None, recent=16, device="cuda"):
+        """rotary: frequencies (``rotary_frequencies``) of the rotary channels, or None.  budget: tokens a sequence
+        keeps, its first 4 and its last `recent` among them, or None."""
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.q_heads, self.heads, self.head_dim, self.page_size = q_heads, heads, head_dim, page_size
@@ -45,12 +53,16 @@ class AttentionBlock:
         self.pages, self.lengths = {}, {}  # per sequence
         self.width = -(-max_tokens // page_size)
         self.device = device
+        self.positions = {}  # of a sequence's next token
+        self.table = None if rotary is None else capi.rotary_table(rotary, max_tokens)
+        self.budget, self.recent = budget, recent
+        self.weights = None if budget is None else torch.zeros((pages, heads, page_size), device=device)
 
     def forward(self, x, batch):
         """x bf16 [tokens, hidden]: the new tokens of the sequences in `batch`
         (pairs of a sequence's name and its number of new tokens), in order.
         Returns bf16 [tokens, hidden]."""
-        slots, table = [], torch.zeros((len(batch), self.width), dtype=torch.int32)
+        slots, places, table = [], [], torch.zeros((len(batch), self.width), dtype=torch.int32)
         for i, (name, n) in enumerate(batch):
             mine = self.pages.setdefault(name, [])
             begin = self.lengths.get(name, 0)
@@ -58,19 +70,29 @@ class AttentionBlock:
                 mine.append(self.free.pop())
             slots += [mine[t // self.page_size] * self.page_size + t % self.page_size for t in range(begin, begin + n)]
             self.lengths[name] = begin + n
+            at = self.positions.get(name, 0)
+            places += range(at, at + n)
+            self.positions[name] = at + n
             table[i, :len(mine)] = torch.tensor(mine, dtype=torch.int32)
         counts = torch.tensor([0] + [n for _, n in batch], dtype=torch.int32)
         offsets = counts.cumsum(0).to(torch.int32)
         lens = torch.tensor([self.lengths[name] for name, _ in batch], dtype=torch.int32)
-        slots, table, offsets, lens = (t.to(self.device, non_blocking=True)
-                                       for t in (torch.tensor(slots, dtype=torch.int64), table, offsets, lens))
+        slots, places, table, offsets, lens = (
+            t.to(self.device, non_blocking=True)
+            for t in (torch.tensor(slots, dtype=torch.int64), torch.tensor(places, dtype=torch.int64), table, offsets, lens))
 
         rows = capi.w8a16_gemm(x, *self.qkv).view(x.shape[0], self.q_heads + 2 * self.heads, self.head_dim)
         q, k, v = rows.split([self.q_heads, self.heads, self.heads], dim=1)
-        capi.kv_cache_store(k, v, slots, self.codes, self.params)
-        out = capi.kv_cache_attention(q, self.codes, self.params, table, lens, q_offsets=offsets,
-                                      max_q=max(n for _, n in batch))
+        if self.table is None:
+            capi.kv_cache_store(k, v, slots, self.codes, self.params)
+        else:
+            q = capi.kv_cache_store_rotary(q, k, v, self.table, slots, self.codes, self.params, positions=places)
+        max_q = max(n for _, n in batch)
+        out = capi.kv_cache_attention(q, self.codes, self.params, table, lens, q_offsets=offsets, max_q=max_q)
         self.last_q = q
+        if self.budget is not None:
+            capi.kv_cache_weights(q, self.codes, self.params, table, lens, self.weights, q_offsets=offsets, max_q=max_q,
+                                  previous=self.weights)
         return capi.w8a16_gemm(out.view(x.shape[0], -1), *self.o), out
 
     def read(self, name):
@@ -80,9 +102,26 @@ class AttentionBlock:
                              dtype=torch.int64, device=self.device)
         return capi.kv_cache_load(self.codes, self.params, slots, self.head_dim)
 
+    def cut(self, names):
+        """Brings the sequences down to the budget, and gives back the pages that they then no longer need."""
+        names = [n for n in names if self.lengths[n] > self.budget]
+        if not names:
+            return
+        table = torch.zeros((len(names), self.width), dtype=torch.int32)
+        for i, name in enumerate(names):
+            table[i, :len(self.pages[name])] = torch.tensor(self.pages[name], dtype=torch.int32)
+        lens = torch.tensor([self.lengths[n] for n in names], dtype=torch.int32)
+        capi.kv_cache_evict(self.codes, self.params, self.weights, table.to(self.device), lens.to(self.device), self.budget,
+                            first=min(4, self.budget - self.recent), last=self.recent)
+        for name in names:
+            self.lengths[name] = self.budget
+            keep = -(-self.budget // self.page_size)
+            self.free += self.pages[name][keep:]
+            self.pages[name] = self.pages[name][:keep]
+
     def release(self, name):
         self.free += self.pages.pop(name)
-        del self.lengths[name]
+        del self.lengths[name], self.positions[name]
 
 
 def plain_attention(q, k, v):
@@ -95,9 +134,9 @@ def plain_attention(q, k, v):
                         v.repeat_interleave(group, 1))
 
 
-def main(hidden=2560, q_heads=32, heads=8, head_dim=128, bits=4, prompts=(300, 77), steps=5):
+def main(hidden=2560, q_heads=32, heads=8, head_dim=128, bits=4, prompts=(300, 77), steps=5, rotary=None, budget=None):
     """Worst relative error of an attention output over the run."""
-    block = AttentionBlock(hidden, q_heads, heads, head_dim, bits=bits)
+    block = AttentionBlock(hidden, q_heads, heads, head_dim, bits=bits, rotary=rotary, budget=budget)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     worst = 0.0
@@ -113,6 +152,9 @@ def main(hidden=2560, q_heads=32, heads=8, head_dim=128, bits=4, prompts=(300, 7
             ref = plain_attention(block.last_q[at:at + n], k, v)
             worst = max(worst, float((out[at:at + n].double() - ref).norm() / ref.norm()))
             at += n
+        if budget is not None:
+            block.cut(names)
+            assert all(block.lengths[n] <= budget for n in names)
     assert capi.i8ql_get_device_error() == capi.I8QL_OK
     for name in names:
         block.release(name)
@@ -122,3 +164,5 @@ def main(hidden=2560, q_heads=32, heads=8, head_dim=128, bits=4, prompts=(300, 7
 if __name__ == "__main__":
     for bits in (4, 8):
         print(f"{bits}-bit cache: attention over it within {main(bits=bits):.2e} of plain attention over its values")
+        far = main(bits=bits, rotary=capi.rotary_frequencies(128, 1e6), budget=128)
+        print(f"  with rotary positions, contexts cut to 128 tokens: {far:.2e}")

@@ -17,8 +17,11 @@ def weights(q, codes, scale, low, n_q, window, softmax_scale, centre):
     seen [n]: tokens that some row sees.
 
     A logit is off by at most delta_j = 2^-18 |softmax_scale| (s_j sum_d |q_d|
-    |c_jd - z| + |low_j + z s_j| sum_d |q_d|) (exact products, D / 16 fp32
-    accumulations, the scaling, 2^-22 each), and by 2^-21 of the row's largest
+    C_jd + L_j sum_d |q_d|): the products of query elements and codes are exact,
+    up to 2 D / 16 fp32 accumulations and the scaling are off by 2^-23 of the
+    magnitudes that they add each, whose sum is that, whether the kernel's codes
+    count from 0 (c, with low_j) or from the middle (c - z, with low_j + z s_j):
+    C_jd and L_j are the larger of the two.  And by 2^-21 of the row's largest
     logit (differences of rounded logits, maxima and logarithms of sums).  A
     weight p_j = e^x_j / sum_k e^x_k then by at most a factor e^(delta_j + ln
     sum_k p_k e^delta_k); exp2 adds 2^-21 of it, the fp32 sums of the row's
@@ -28,8 +31,9 @@ def weights(q, codes, scale, low, n_q, window, softmax_scale, centre):
     k = kv_cache.values(codes, scale, low)
     q = np.asarray(q, np.float64)
     sums, bound, seen = np.zeros((heads, n)), np.zeros((heads, n)), np.zeros(n, bool)
-    s64, mid = np.abs(scale.astype(np.float64)), np.abs(low.astype(np.float64) + centre * scale.astype(np.float64))
-    off = np.abs(codes.astype(np.float64) - centre)
+    s64, low64, c64 = (x.astype(np.float64) for x in (scale, low, codes))
+    mid = np.maximum(np.abs(low64), np.abs(low64 + centre * s64))
+    off, s64 = np.maximum(c64, np.abs(c64 - centre)), np.abs(s64)
     group = hq // heads
     for i in range(n_q):
         p = n - n_q + i

@@ -433,6 +433,35 @@ def test_other_stream_and_graph(nqs):
     assert capi.i8ql_get_device_error() == capi.I8QL_OK
 
 
+def test_past_32_bits():
+    """Pages more than 2^32 bytes of codes into the cache give what the first pages give."""
+    heads, d, bits, page, pages = 8, 128, 8, 256, 8300
+    codes, params = capi.kv_cache_alloc(pages, heads, page, d, bits)
+    assert codes.numel() > 1 << 32
+    weights = torch.zeros((pages, heads, page), device="cuda")
+    table = capi.rotary_table(capi.rotary_frequencies(d), 1000)
+    torch.manual_seed(0)
+    k, v = (torch.randn((700, heads, d), device="cuda").to(torch.bfloat16) for _ in range(2))
+    got = []
+    for first in (0, pages - 6):
+        own = torch.arange(first, first + 3, dtype=torch.int32, device="cuda")[None]
+        slots = first * page + torch.arange(700, device="cuda")
+        capi.kv_cache_store_rotary(None, k, v, table, slots, codes, params)
+        lens = torch.tensor([700], dtype=torch.int32, device="cuda")
+        sums = []
+        for nq in (1, 2, 9, 40):
+            q = torch.randn((nq, 32, d), generator=torch.Generator(device="cuda").manual_seed(nq), device="cuda").to(torch.bfloat16)
+            capi.kv_cache_weights(q, codes, params, own, lens, weights, q_offsets=torch.tensor([0, nq], dtype=torch.int32).cuda(),
+                                  max_q=nq)
+            sums.append(weights[first:first + 3].clone())
+        new, kept = capi.kv_cache_evict(codes, params, weights, own, lens, 300, first=4, last=50, new_table=own + 3)
+        capi.kv_cache_evict(codes, params, weights, own, lens, 200, first=4, last=50)
+        back = capi.kv_cache_load(codes, params, torch.cat([(first + 3) * page + torch.arange(300), first * page + torch.arange(200)]).cuda(), d)
+        got.append((*sums, kept, *back))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_run_together(interleaved, bits):
