@@ -40,7 +40,7 @@ namespace {
 constexpr int kTile = 128;   // tokens a block works on at a time
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 32;   // most tiles of a block of the second kernel
+constexpr int kChunk = 16;   // most tiles of a block of the second kernel
 template <int D, int BITS>
 constexpr int kStages = D * BITS == 128 * 8 ? 3 : 4;
 // All in one:
@@ -265,18 +265,6 @@ struct Keys {
                     }
             }
     }
-
-    // The same in log2 units.
-    template <int HALVES>
-    __device__ __forceinline__ void scaled_logits(const Queries<D, BITS, HALVES>& q, int token, float (&s)[2][HALVES][4]) const {
-        logits<true>(q, token, s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) s[i][x][y] *= q.unit[x][y % 2];
-    }
 };
 
 // A warp's tokens on their way: a ring of STAGES steps of 32 tokens, WARPS * 32 tokens
@@ -449,19 +437,40 @@ __device__ __forceinline__ void join_stats(float& m, float& l, float om, float o
     m = to;
 }
 
-// Adds a step's logits to a lane's (m, l).
-template <int HALVES>
-__device__ __forceinline__ void add_logits(float (&m)[HALVES][2], float (&l)[HALVES][2], const float (&s)[2][HALVES][4]) {
+// Adds a step's logits to a lane's (m, l).  m is what l is relative to; it is raised where a
+// logit exceeds it by more than the slack (rare).  It begins at kNothing, finite, so that
+// what is not seen (-inf) has weight 0 beside it.
+constexpr float kNothing = -3.402823466e38f;
+constexpr float kSlack = 8.0f;
+template <int D, int BITS, int HALVES>
+__device__ __forceinline__ void add_logits(float (&m)[HALVES][2], float (&l)[HALVES][2], const float (&s)[2][HALVES][4],
+                                           const Queries<D, BITS, HALVES>& q) {
+    float top[HALVES][2];
+    bool over = false;
 #pragma unroll
     for (int x = 0; x < HALVES; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const float top = fmaxf(fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y]));
-            const float to = fmaxf(m[x][y], top);
-            const float sum = (weight_of(s[0][x][y], to) + weight_of(s[0][x][2 + y], to)) +
-                              (weight_of(s[1][x][y], to) + weight_of(s[1][x][2 + y], to));
-            l[x][y] = fmaf(l[x][y], weight_of(m[x][y], to), sum);
-            m[x][y] = to;
+            top[x][y] = fmaxf(max3(s[0][x][y], s[0][x][2 + y], s[1][x][y]), s[1][x][2 + y]) * q.unit[x][y];
+            over = over || top[x][y] > m[x][y] + kSlack;
+        }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                if (top[x][y] > m[x][y] + kSlack) {
+                    l[x][y] *= exp2_approx(m[x][y] - top[x][y]);
+                    m[x][y] = top[x][y];
+                }
+    }
+#pragma unroll
+    for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const float u = q.unit[x][y], to = -m[x][y];
+            l[x][y] += (exp2_approx(fmaf(s[0][x][y], u, to)) + exp2_approx(fmaf(s[0][x][2 + y], u, to))) +
+                       (exp2_approx(fmaf(s[1][x][y], u, to)) + exp2_approx(fmaf(s[1][x][2 + y], u, to)));
         }
 }
 
@@ -479,6 +488,25 @@ __device__ __forceinline__ void warp_stats(float (&m)[HALVES][2], float (&l)[HAL
                            __shfl_xor_sync(0xffffffffu, l[x][y], d));
             if (g == 0) part[8 * x + 2 * t + y] = make_float2(m[x][y], l[x][y]);
         }
+}
+
+// Sums of four neighbours, tokens j .. j + 3 at place `to`, of which those of begin .. end - 1
+// are written, and those before `older` added to what they had.
+__device__ __forceinline__ void store_weights(const KvWeightsParams& p, int64_t to, int j, int begin, int end, int older,
+                                              const float (&sum)[4]) {
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < older) w = *reinterpret_cast<const float4*>(p.previous + to);
+    const float before[4] = {w.x, w.y, w.z, w.w};
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (j + k < older ? before[k] : 0.0f) + sum[k];
+    if (j >= begin && j + 4 <= end) {
+        *reinterpret_cast<float4*>(p.weights + to) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k >= begin && j + k < end) p.weights[to + k] = v[k];
+    }
 }
 
 // All in one, while a cluster's shared memory holds the logits: a cluster takes one
@@ -624,11 +652,6 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
         const int64_t page = kv_page(p.a.cache, table, j >> p.a.cache.page_shift, p.a.err);
         if (page < 0) continue;
         const int64_t to = kv_weight(p.a.cache, page, h, j & mask);
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < older) w = *reinterpret_cast<const float4*>(p.previous + to);
-        if (j + 1 >= older) w.y = 0.0f;
-        if (j + 2 >= older) w.z = 0.0f;
-        if (j + 3 >= older) w.w = 0.0f;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; 2 * r < rows; ++r) {
             const float4 a = *reinterpret_cast<const float4*>(logits + r * stride + i);
@@ -639,18 +662,23 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
             sum.z = fmaf(c.y, f.y, fmaf(c.x, f.x, sum.z));
             sum.w = fmaf(c.w, f.y, fmaf(c.z, f.x, sum.w));
         }
-        w = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
-        if (j >= begin && j + 4 <= end) {
-            *reinterpret_cast<float4*>(p.weights + to) = w;
-        } else {
-            const float v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (j + k >= begin && j + k < end) p.weights[to + k] = v[k];
-        }
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        store_weights(p, to, j, begin, end, older, v);
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// The tokens that all of a block's rows see.
+struct Edges {
+    int lo, hi;
+    __device__ __forceinline__ Edges(const KvAttnParams& p, const KvSeq& seq, int row0, int rows) {
+        const int base = seq.len - seq.nq;
+        hi = base + row0 / p.G;
+        lo = p.window > 0 ? (int)max(base + (row0 + rows - 1) / p.G + 1 - p.window, (int64_t)0) : 0;
+    }
+    // Whether they are a warp's 32 from `token` on.
+    __device__ __forceinline__ bool whole(int token) const { return token >= lo && token + 31 <= hi; }
+};
 
 // (m, l) over a part of the tokens, for a block of rows.
 template <int D, int BITS, int HALVES>
@@ -679,23 +707,37 @@ __global__ void __launch_bounds__(kThreads) kv_stats_kernel(const KvWeightsParam
     for (int x = 0; x < HALVES; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            m[x][y] = -INFINITY;
+            m[x][y] = kNothing;
             l[x][y] = 0.0f;
         }
     if (first < last) {
-        Queries<D, BITS, HALVES> q;
-        q.load(p.a, seq, h, row0, rows);
         const int32_t* table = p.a.table + b * p.a.table_width;
-        int token = (span.first + first) * kTile + warp * 32 + g;
         KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, span.first + first, span.first + last, span.begin,
                                                           span.end);
-        for (int i = first; i < last; ++i, token += kTile) {
+        Queries<D, BITS, HALVES> q;
+        q.load(p.a, seq, h, row0, rows);
+        int token = (span.first + first) * kTile + warp * 32 + g;
+        const Edges edges(p.a, seq, row0, rows);
+        auto step = [&](auto edge) {
             Keys<D, BITS> now;
             ring.take(now);
             float s[2][HALVES][4];
-            now.scaled_logits(q, token, s);
-            add_logits<HALVES>(m, l, s);
+            now.template logits<decltype(edge)::value>(q, token, s);
+            add_logits<D, BITS, HALVES>(m, l, s, q);
+        };
+        for (int i = first; i < last; ++i, token += kTile) {
+            if (edges.whole(token - g))
+                step(std::false_type{});
+            else
+                step(std::true_type{});
         }
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) m[x][y] = m[x][y] == kNothing ? -INFINITY : m[x][y];
+    } else {
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x) m[x][0] = m[x][1] = -INFINITY;
     }
     warp_stats<HALVES>(m, l, part[warp]);
     __syncthreads();
@@ -713,7 +755,7 @@ template <int D, int BITS, int HALVES>
 __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams p) {
     constexpr int ROWS = 8 * HALVES;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float sums[kChunk * kTile];
+    __shared__ __align__(16) float sums[kChunk * kTile];
     __shared__ float2 stats[ROWS];  // (m, 1 / l)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int64_t tiles_all = ((p.a.table_width << p.a.cache.page_shift) + kTile - 1) / kTile;
@@ -738,6 +780,10 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
         const int first = max(span.first, tile0), last = min((span.end + kTile - 1) / kTile, tile0 + tiles);
         if (first >= last) continue;  // (the same for the whole block)
         const int row0 = rb * ROWS, rows = min(ROWS, seq.nq * p.a.G - row0);
+        // keys, rows and their statistics wait together
+        KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, first, last, span.begin, span.end);
+        Queries<D, BITS, HALVES> q;
+        q.load(p.a, seq, h, row0, rows);
         __syncthreads();
         if (threadIdx.x < ROWS) {
             float m = -INFINITY, l = 0.0f;
@@ -751,44 +797,56 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
             stats[threadIdx.x] = make_float2(m == -INFINITY ? 0.0f : m, l > 0.0f ? 1.0f / l : 0.0f);
         }
         __syncthreads();
-        Queries<D, BITS, HALVES> q;
-        q.load(p.a, seq, h, row0, rows);
         float2 st[HALVES][2];
 #pragma unroll
         for (int x = 0; x < HALVES; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) st[x][y] = stats[8 * x + 2 * t + y];
         int token = first * kTile + warp * 32 + g;
-        KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, first, last, span.begin, span.end);
-        for (int i = first; i < last; ++i, token += kTile) {
+        const Edges edges(p.a, seq, row0, rows);
+        float* to = sums + (first - tile0) * kTile + warp * 32 + g;
+        auto step = [&](auto edge) {
             Keys<D, BITS> now;
             ring.take(now);
             float s[2][HALVES][4];
-            now.scaled_logits(q, token, s);
+            now.template logits<decltype(edge)::value>(q, token, s);
+            float sum[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float sum = 0.0f;
+                sum[k] = 0.0f;
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        sum = fmaf(exp2_approx(s[k / 2][x][2 * (k % 2) + y] - st[x][y].x), st[x][y].y, sum);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (t == 0) sums[(i - tile0) * kTile + warp * 32 + g + 8 * k] += sum;
+                        sum[k] = fmaf(exp2_approx(fmaf(s[k / 2][x][2 * (k % 2) + y], q.unit[x][y], -st[x][y].x)), st[x][y].y, sum[k]);
             }
+            // over the four lanes of a token: each ends with one of its four tokens
+            const bool odd = t & 1, high = t & 2;
+            float a = odd ? sum[0] : sum[1], b = odd ? sum[2] : sum[3];
+            a = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, a, 1);
+            b = (odd ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, b, 1);
+            const float c = __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
+            to[8 * t] += (high ? b : a) + c;
+        };
+        for (int i = first; i < last; ++i, token += kTile, to += kTile) {
+            if (edges.whole(token - g))
+                step(std::false_type{});
+            else
+                step(std::true_type{});
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tiles * kTile; i += kThreads) {
+    // four tokens a thread at a time, which lie in one page
+    const int older = p.previous != nullptr ? seq.len - seq.nq : 0, mask = (1 << p.a.cache.page_shift) - 1;
+#pragma unroll 2
+    for (int i = threadIdx.x * 4; i < tiles * kTile; i += 4 * kThreads) {
         const int j = tile0 * kTile + i;
-        if (j >= seq.len) break;
-        if (j < begin) continue;
+        if (j + 4 <= begin || j >= seq.len) continue;
         const int64_t page = kv_page(p.a.cache, table, j >> p.a.cache.page_shift, p.a.err);
         if (page < 0) continue;
-        const int64_t to = kv_weight(p.a.cache, page, h, j & ((1 << p.a.cache.page_shift) - 1));
-        const float before = p.previous != nullptr && j < seq.len - seq.nq ? p.previous[to] : 0.0f;
-        p.weights[to] = before + sums[i];
+        const float4 sum = *reinterpret_cast<const float4*>(sums + i);
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        store_weights(p, kv_weight(p.a.cache, page, h, j & mask), j, begin, seq.len, older, v);
     }
 }
 
