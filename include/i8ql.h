@@ -536,8 +536,9 @@ i8ql_status i8ql_kv_attention_workspace(int64_t B, int64_t T_q, int64_t Hq, int6
  * Inputs: freqs fp64 [F], radians a position (finite; scaling for long contexts
  * is in them), 8-byte aligned; positions int64 [P] (any sign) or NULL.
  * Output: table fp32 [P, 2F], 16-byte aligned.  The angle's fraction of a turn
- * is exact to |p| 2^-64, so cosine and sine are within 2^-23 of their value
- * (before the amplitude's rounding) for |p| < 2^31.  F <= I8QL_ROTARY_MAX_D / 2.
+ * is exact to |p| 2^-64 (frequencies of either sign, up to 2^32), so a value is
+ * within 2^-22 amplitude of the formula's for |p| < 2^31.
+ * F <= I8QL_ROTARY_MAX_D / 2.
  */
 #define I8QL_ROTARY_MAX_D 512
 i8ql_status rotary_table(const double* freqs, const int64_t* positions, float* table, int64_t P, int64_t F,

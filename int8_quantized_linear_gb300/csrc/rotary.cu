@@ -42,9 +42,10 @@ __global__ void __launch_bounds__(kTableThreads) rotary_table_kernel(const doubl
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
     const double f = __ldg(freqs + i);
     const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
-    const double whole = floor(hi);
-    // (2^64 frac: both parts below 2^64 in magnitude, their sum taken mod 2^64)
-    const unsigned long long u = (unsigned long long)((hi - whole) * 0x1p64) + (unsigned long long)llrint(lo * 0x1p64);
+    // (exact for either sign: of what truncation leaves, the magnitude, below 2^64)
+    const double part = hi - trunc(hi);
+    const unsigned long long whole = (unsigned long long)rint(fabs(part) * 0x1p64);
+    const unsigned long long u = (part < 0.0 ? 0ull - whole : whole) + (unsigned long long)llrint(lo * 0x1p64);
     // (positions in order: the next angle is a step further; no product)
     const uint32_t step = gridDim.x * side, first = blockIdx.x * side + r;
     uint64_t turn = (uint64_t)first * u;

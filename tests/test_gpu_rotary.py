@@ -67,6 +67,20 @@ def test_table(n, f):
     assert ((s - want).abs() <= 2.0 ** -21 * want).all()
 
 
+# Frequencies of either sign, to the same bound (see test_table), whatever their size.
+def test_table_signs():
+    freqs = np.array([-1e-4, -3e-13, -0.7, -6.3, -1e5, 2e5, 1e-13, -1.0])
+    at = np.array([0, 1, -1, (1 << 31) - 1, -(1 << 31) + 1, 77777])
+    got = capi.rotary_table(torch.from_numpy(freqs).cuda(), torch.from_numpy(at).cuda()).cpu().double()
+    assert float((got - torch.from_numpy(oracle.table(freqs, at))).abs().max()) <= 2.0 ** -22
+    # near 0 the sine keeps its relative precision: 2^-55 turns that are cut off, of 2^-32.6 and
+    # more, and the series' and products' roundings, 2^-22.4 + 2^-24 + 2^-24
+    small = torch.tensor([-1e-9, -3e-7], dtype=torch.float64)
+    s = capi.rotary_table(small.cuda(), 4).cpu().double()[:, 2:]
+    want = torch.sin(torch.arange(4, dtype=torch.float64)[:, None] * small)
+    assert ((s - want).abs() <= 2.0 ** -21 * want.abs()).all()
+
+
 @pytest.mark.parametrize("n", [0, 1, 5, 1000, 70001])
 def test_table_range(n):
     f = capi.rotary_frequencies(96, 10000.0)
