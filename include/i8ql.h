@@ -578,8 +578,9 @@ i8ql_status rotary_apply(const i8ql_bf16* x, int64_t x_stride, const float* tabl
  * No counterpart on the pages.  q and q_out bf16 [T, Hq, D] (strides and
  * aliasing as rotary_apply's x and out; Hq = 0: no queries, both ignored); k,
  * v, slots and the cache as kv_cache_store; table, positions and interleaved
- * as rotary_apply, rot a multiple of 16.  A negative slot stores nothing and
- * its query is turned all the same.  T * (Hq + H) < 2^30.
+ * as rotary_apply, rot a multiple of 16.  q_out must not overlap k or v.  A
+ * negative slot stores nothing and its query is turned all the same.
+ * T * (Hq + H) < 2^30.
  */
 i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf16* q_out, int64_t q_out_stride,
                                   const i8ql_bf16* k, const i8ql_bf16* v, int64_t k_stride, int64_t v_stride,

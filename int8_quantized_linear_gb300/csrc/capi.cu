@@ -565,17 +565,22 @@ i8ql_status kv_cache_attention(const i8ql_bf16* q, int64_t q_stride, const uint8
 
 namespace {
 
-// Whether token rows of n values at `a` and `b` (`rows` of them, their strides apart)
-// share memory without being the same rows.
-bool tangled(const i8ql_bf16* a, int64_t a_stride, const i8ql_bf16* b, int64_t b_stride, int64_t rows, int64_t n) {
-    if (a == b) return a_stride != b_stride && rows > 1;
-    const i8ql_bf16 *lo = a < b ? a : b, *hi = a < b ? b : a;
-    const int64_t lo_stride = a < b ? a_stride : b_stride;
-    const int64_t apart = hi - lo;
-    if (apart >= (rows - 1) * lo_stride + n) return false;
+// Whether token rows of a_n values at `a` and of b_n at `b` (`rows` of them, their strides
+// apart) share memory.
+bool meet(const i8ql_bf16* a, int64_t a_stride, int64_t a_n, const i8ql_bf16* b, int64_t b_stride, int64_t b_n,
+          int64_t rows) {
+    if (b < a) return meet(b, b_stride, b_n, a, a_stride, a_n, rows);
+    const int64_t apart = b - a;
+    if (apart >= (rows - 1) * a_stride + a_n) return false;
     if (a_stride != b_stride) return true;
     // (neighbours in rows of the same width do not meet)
-    return apart % a_stride < n || apart % a_stride > a_stride - n;
+    return apart % a_stride < a_n || apart % a_stride > a_stride - b_n;
+}
+
+// The same, but for the very same rows.
+bool tangled(const i8ql_bf16* a, int64_t a_stride, const i8ql_bf16* b, int64_t b_stride, int64_t rows, int64_t n) {
+    if (a == b) return a_stride != b_stride && rows > 1;
+    return meet(a, a_stride, n, b, b_stride, n, rows);
 }
 
 // A table of angles for T tokens' rows of D channels.
@@ -655,7 +660,10 @@ i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf1
     I8QL_TRY(check_matrix(codes, T));
     I8QL_TRY(check_matrix(params, T));
     if (T == 0) return I8QL_OK;
-    if (Hq > 0 && tangled(q, q_stride, q_out, q_out_stride, T, Hq * D)) return I8QL_ERR_INVALID_ARG;
+    if (Hq > 0 && (tangled(q, q_stride, q_out, q_out_stride, T, Hq * D) ||
+                   meet(q_out, q_out_stride, Hq * D, k, k_stride, H * D, T) ||
+                   meet(q_out, q_out_stride, Hq * D, v, v_stride, H * D, T)))
+        return I8QL_ERR_INVALID_ARG;
     LaunchEnv env;
     i8ql_status s;
     if (!launch_env(stream, &env, &s)) return s;
@@ -699,6 +707,10 @@ i8ql_status kv_cache_weights(const i8ql_bf16* q, int64_t q_stride, const uint8_t
     I8QL_TRY(check_matrix(weights, T_q));
     if (T_q == 0) return I8QL_OK;
     if (B == 0) return I8QL_ERR_INVALID_ARG;
+    // (previous weights are read while others are written: the same, or apart)
+    const int64_t places = num_pages * H * page_size;
+    if (previous != nullptr && previous != weights && previous < weights + places && weights < previous + places)
+        return I8QL_ERR_INVALID_ARG;
     LaunchEnv env;
     i8ql_status s;
     if (!launch_env(stream, &env, &s)) return s;

@@ -66,6 +66,18 @@ def test_weights_refusals(lib):
     assert g(4, 0, 32, 8, 128, 4, 64, 16, 0, ctypes.byref(n)) == capi.I8QL_OK and n.value == 0
 
 
+def test_weights_refuse_overlapping_buffers(lib):
+    f = lib.kv_cache_weights
+    previous, size = F, 100 * 8 * 64 * 4
+    ok = (A, 4096, B, C, D, 16, E, None, previous, F, 4, 4, 32, 8, 128, 4, 64, 100, 1, 0, 0.1, A, 1 << 40, None)
+    for off in (16, size - 16):
+        assert f(*_with(ok, _9=F + off)) == INVALID
+        assert f(*_with(ok, _8=F + off)) == INVALID
+    if not torch.cuda.is_available():
+        for off in (0, size):
+            assert f(*_with(ok, _9=F + off)) == capi.I8QL_ERR_NO_DEVICE
+
+
 def test_evict_refusals(lib):
     f = lib.kv_cache_evict
     #     codes params weights table width lens new_table new_width new_lens kept B H D bits page pages budget first last stream

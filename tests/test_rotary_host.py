@@ -119,6 +119,23 @@ def test_store_rotary_refusals(lib):
         assert f(*_with(ok, _0=None, _2=None, _15=0)) == capi.I8QL_ERR_NO_DEVICE  # no queries
 
 
+def test_store_rotary_refuses_queries_over_keys(lib):
+    f = lib.kv_cache_store_rotary
+    # a fused projection of 32 + 8 + 8 heads of 128 channels
+    q, k, v, step = A, A + 2 * 4096, A + 2 * 5120, 6144
+    ok = (q, step, q, step, k, v, step, step, E, 100, F, B, C, D, 10, 32, 8, 128, 4, 64, 10, 128, 0, None)
+    for i in (4, 5):
+        assert f(*_with(ok, _2=B, _3=4096, **{f"_{i}": B + 2 * 4096})) == INVALID    # over the second row
+        assert f(*_with(ok, **{f"_{i}": A})) == INVALID
+        assert f(*_with(ok, **{f"_{i}": A + 2 * 4088})) == INVALID
+        assert f(*_with(ok, **{f"_{i}": A + 2 * (step + 4088)})) == INVALID
+        assert f(*_with(ok, _2=A + 2 * 8, **{f"_{i}": A})) == INVALID
+    if not torch.cuda.is_available():
+        nothing = capi.I8QL_ERR_NO_DEVICE
+        assert f(*ok) == nothing                      # in place, beside the keys
+        assert f(*_with(ok, _4=v, _5=k)) == nothing
+
+
 def test_binding_refusals(lib):
     x, table = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros((10, 64))
     with pytest.raises(ValueError, match="x must be a CUDA tensor"):
