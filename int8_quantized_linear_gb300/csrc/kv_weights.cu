@@ -785,16 +785,22 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
         Queries<D, BITS, HALVES> q;
         q.load(p.a, seq, h, row0, rows);
         __syncthreads();
-        if (threadIdx.x < ROWS) {
+        {  // several lanes a row
+            constexpr int kLanes = kThreads / ROWS;
+            const int r = threadIdx.x / kLanes;
             float m = -INFINITY, l = 0.0f;
-            if (threadIdx.x < rows) {
-                const int i = (row0 + threadIdx.x) / p.a.G;
-                const int64_t row = (seq.q0 + i) * ((int64_t)p.a.G * p.a.cache.H) + h * p.a.G + row0 + threadIdx.x - i * p.a.G;
-                const float2* part = p.stats + row * p.splits;
-                for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part[s].x);
-                for (int s = 0; s < p.splits; ++s) l = fmaf(part[s].y, weight_of(part[s].x, m), l);
+            if (r < rows) {
+                const int i = (row0 + r) / p.a.G;
+                const int64_t row = (seq.q0 + i) * ((int64_t)p.a.G * p.a.cache.H) + h * p.a.G + row0 + r - i * p.a.G;
+                for (int s = threadIdx.x % kLanes; s < p.splits; s += kLanes) {
+                    const float2 x = p.stats[row * p.splits + s];
+                    join_stats(m, l, x.x, x.y);
+                }
             }
-            stats[threadIdx.x] = make_float2(m == -INFINITY ? 0.0f : m, l > 0.0f ? 1.0f / l : 0.0f);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1)
+                join_stats(m, l, __shfl_xor_sync(0xffffffffu, m, d), __shfl_xor_sync(0xffffffffu, l, d));
+            if (threadIdx.x % kLanes == 0) stats[r] = make_float2(m == -INFINITY ? 0.0f : m, l > 0.0f ? 1.0f / l : 0.0f);
         }
         __syncthreads();
         float2 st[HALVES][2];
@@ -871,12 +877,13 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
     const int64_t one_tiles = (max_kv + kOneTile - 1) / kOneTile;
     // One launch: 96 sequences of 16384 tokens (4 bits, 8 x 128, four queries a head) 249 us
     // with 8 CTAs a cluster and 277 with 4; 48 of 32768, twice the logits a CTA, 283, and 450
-    // by the two kernels; 64 of 4096 with 16 rows 72 and 124.  With more rows its registers
-    // leave one block an SM: only where there is no more.
+    // by the two kernels.  With 16 rows two blocks run on an SM all the same: 64 of up to
+    // 4096 in 72 us with 4 CTAs, 126 with 8, 124 by the two kernels.  With 32 rows one does:
+    // only where there is no more.
     for (int64_t size = 1; size <= 8 && blocks == 1; size *= 2) {
         const int64_t chunk = (one_tiles + size - 1) / size;
         const size_t smem = (size_t)((rows + 1) / 2) * (size_t)(chunk * kOneTile + 8) * sizeof(float2);
-        if (smem > (size < 8 ? kFewLogits : kMostLogits)) continue;
+        if (smem > (size < 8 && w.halves == 1 ? kFewLogits : kMostLogits)) continue;
         if (size < 8 && base * size < wanted && size < one_tiles) continue;
         if (w.halves == 4 && base * size > 2 * sms) break;
         w.fused = true;

@@ -653,10 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                     if (SUM && set == 0) {
                         float top_m = -INFINITY, l = 0.0f;
                         if (live) {
-                            for (int s = 0; s < p.splits; ++s) top_m = fmaxf(top_m, p.stats[stat + s].x);
+#pragma unroll 4
                             for (int s = 0; s < p.splits; ++s) {
                                 const float2 x = p.stats[stat + s];
-                                l = fmaf(x.y, exp2_approx(x.x - (top_m == -INFINITY ? 0.0f : top_m)), l);
+                                const float to = fmaxf(top_m, x.x), shift = to == -INFINITY ? 0.0f : to;
+                                l = l * exp2_approx(top_m - shift) + x.y * exp2_approx(x.x - shift);
+                                top_m = to;
                             }
                         }
                         rf.minus_n[r_m] = l > 0.0f ? -(top_m + log2f(l)) : -INFINITY;
