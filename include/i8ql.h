@@ -604,9 +604,17 @@ i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf1
  * reused pages.  Tokens that no row of the call sees are left as they are.
  *
  * previous and weights: fp32 [num_pages, H, page_size], 16-byte aligned; the
- * same buffer, or two that do not overlap.  All in fp32 (products on the
- * codes, exact); rows that see no token add nothing.  A key row that is not
- * finite gives unspecified weights of its sequence and head where it is seen.
+ * same buffer, or two that do not overlap.  Rows that see no token add
+ * nothing.  A key row that is not finite gives unspecified weights of its
+ * sequence and head where it is seen.
+ * Precision: exponentials, sums and statistics in fp32.  A logit is scale times
+ * s_j (q . code_j) + low_j (sum of q), and off by up to 2^-18 |scale|
+ * times the same with magnitudes, which exceeds the logit where the two parts
+ * cancel.  Up to 64 rows (max_q * Hq / H) the products are exact but for fp32
+ * sums (and for elements of q 2^-28 of their row's largest).  With more, scale
+ * and low value are operands too: q's elements 2^-25 of the largest of 16
+ * neighbouring rows, and keys 2^-21 of the largest of 128 neighbouring tokens,
+ * lose bits.
  * max_q: the most query tokens of one sequence (more record
  * I8QL_ERR_BAD_INDEX); pages out of range record it too and are not written.
  * workspace as kv_cache_attention, i8ql_kv_weights_workspace bytes.  The

@@ -13,8 +13,14 @@
 // each kept token its slot.  A cluster of CTAs takes a sequence's head, each a run of
 // its tokens, which it reads once, into shared memory; histograms and counts are added up
 // through distributed shared memory.  Nothing depends on timing (the histogram's atomics
-// only count).  Moving is bound by bytes: kept rows of codes, scales and weights, read
-// and written once.
+// only count).  32 sequences of up to 16384 tokens with 8 heads, cut to 2048: 27.4 us, bound by
+// the instructions (issue slots 65 %) and the barriers between the passes; 70.7 with the
+// weights read from memory in four passes of 8 bits.
+//
+// Moving is bound by bytes: kept rows of codes, scales and weights, read and written
+// once: 128 channels of 4 bits, as above, 35.3 us.  A kept token's scales and weight are 4
+// bytes each, in sectors of their own, so that 130 MB are read for the 73 that are needed,
+// and 73 written: 5.7 TB/s.  (One, two or four rows a thread: 35 us each.)
 
 #include <cuda_runtime.h>
 

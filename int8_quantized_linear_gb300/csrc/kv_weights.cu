@@ -16,10 +16,17 @@
 // kept apart (2^(a - m) / l, not 2^(a - m - log2 l)): beside a large m the logarithm
 // would lose its bits.
 //
-// A weight needs its row's maximum and sum, which need all keys: two kernels
-// that both go over the keys.  The first leaves each row's (m, l) over a part of
-// the tokens, the second joins them and sums the weights of its tokens over all
-// rows, in order; no atomics.  Tokens that no row sees keep what they have.
+// A weight needs its row's maximum and sum, which need all keys.  While a cluster's
+// shared memory holds the logits of a cache head (one token's rows, contexts up to 32768
+// with four query heads), one launch reads the keys once: 96 sequences of 16384 tokens, 8 x
+// 128 channels, 4 bits, 249 us, of 143 for the bytes (3.8 TB/s; the products, the
+// exchange and the sums of a block follow each other, and four blocks an SM cover for it).
+// Otherwise two kernels both go over the keys.  The first leaves each row's (m, l) over
+// a part of the tokens, the second joins them and sums the weights of its tokens over all
+// rows, in order; no atomics.  16 sequences of up to 8191 tokens with 64 rows a
+// head (8 x 64 channels, 8 bits): 60 and 53 us, bound by the instructions beside
+// the products (unpacking per 32 rows, an exponential a logit and pass; issue slots 50 %).
+// Tokens that no row sees keep what they have.
 //
 // The layout of the products is that of kv_attention.cu: 16 tokens are the M rows
 // of an MMA (A: codes as they lie, a lane taking D / 4 neighbouring channels of
@@ -254,15 +261,18 @@ struct Keys {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const float scale = kv_scale(param[2 * i + z]), low = kv_low(param[2 * i + z]);
+                const uint64_t scale2 = pair_f32(scale, scale), low2 = pair_f32(low, low);
                 const int j = token + 16 * i + 8 * z;
 #pragma unroll
-                for (int x = 0; x < HALVES; ++x)
+                for (int x = 0; x < HALVES; ++x) {
+                    float* v = s[i][x] + 2 * z;
+                    split_f32(fma_f32x2(scale2, pair_f32(v[0], v[1]), mul_f32x2(low2, pair_f32(q.sum[x][0], q.sum[x][1]))),
+                              v[0], v[1]);
+                    if (EDGE) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float& v = s[i][x][2 * z + y];
-                        v = fmaf(scale, v, low * q.sum[x][y]);
-                        if (EDGE) v = j >= q.lo[x][y] && j <= q.hi[x][y] ? v : -INFINITY;
+                        for (int y = 0; y < 2; ++y) v[y] = j >= q.lo[x][y] && j <= q.hi[x][y] ? v[y] : -INFINITY;
                     }
+                }
             }
     }
 };
@@ -465,13 +475,17 @@ __device__ __forceinline__ void add_logits(float (&m)[HALVES][2], float (&l)[HAL
                 }
     }
 #pragma unroll
-    for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const float u = q.unit[x][y], to = -m[x][y];
-            l[x][y] += (exp2_approx(fmaf(s[0][x][y], u, to)) + exp2_approx(fmaf(s[0][x][2 + y], u, to))) +
-                       (exp2_approx(fmaf(s[1][x][y], u, to)) + exp2_approx(fmaf(s[1][x][2 + y], u, to)));
-        }
+    for (int x = 0; x < HALVES; ++x) {
+        const uint64_t u = pair_f32(q.unit[x][0], q.unit[x][1]), to = pair_f32(-m[x][0], -m[x][1]);
+        auto weights = [&](const float* v) {
+            float a, b;
+            split_f32(fma_f32x2(pair_f32(v[0], v[1]), u, to), a, b);
+            return pair_f32(exp2_approx(a), exp2_approx(b));
+        };
+        const uint64_t sum = add_f32x2(add_f32x2(weights(s[0][x]), weights(s[0][x] + 2)),
+                                       add_f32x2(weights(s[1][x]), weights(s[1][x] + 2)));
+        split_f32(add_f32x2(pair_f32(l[x][0], l[x][1]), sum), l[x][0], l[x][1]);
+    }
 }
 
 // The lanes' (m, l) of a warp, into part[row].
@@ -600,17 +614,21 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
         const float u0 = queries.unit[2 * r], u1 = queries.unit[2 * r + 1];
         const float m0 = mine[2 * r].x == -INFINITY ? 0.0f : -mine[2 * r].x;
         const float m1 = mine[2 * r + 1].x == -INFINITY ? 0.0f : -mine[2 * r + 1].x;
-        float l0 = 0.0f, l1 = 0.0f;
+        const uint64_t u = pair_f32(u0, u1), to = pair_f32(m0, m1);
+        uint64_t l = pair_f32(0.0f, 0.0f);
         float4* a = reinterpret_cast<float4*>(logits + r * stride);  // two tokens at a time
 #pragma unroll 4
         for (int i = threadIdx.x; i < tokens / 2; i += kOneThreads) {
             const float4 v = a[i];
-            const float4 e = make_float4(exp2_approx(fmaf(v.x, u0, m0)), exp2_approx(fmaf(v.y, u1, m1)),
-                                         exp2_approx(fmaf(v.z, u0, m0)), exp2_approx(fmaf(v.w, u1, m1)));
+            float4 e;
+            split_f32(fma_f32x2(pair_f32(v.x, v.y), u, to), e.x, e.y);
+            split_f32(fma_f32x2(pair_f32(v.z, v.w), u, to), e.z, e.w);
+            e = make_float4(exp2_approx(e.x), exp2_approx(e.y), exp2_approx(e.z), exp2_approx(e.w));
             a[i] = e;
-            l0 += e.x + e.z;
-            l1 += e.y + e.w;
+            l = add_f32x2(l, add_f32x2(pair_f32(e.x, e.y), pair_f32(e.z, e.w)));
         }
+        float l0, l1;
+        split_f32(l, l0, l1);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -652,17 +670,25 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
         const int64_t page = kv_page(p.a.cache, table, j >> p.a.cache.page_shift, p.a.err);
         if (page < 0) continue;
         const int64_t to = kv_weight(p.a.cache, page, h, j & mask);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint64_t sum[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = pair_f32(0.0f, 0.0f);
         for (int r = 0; 2 * r < rows; ++r) {
             const float4 a = *reinterpret_cast<const float4*>(logits + r * stride + i);
             const float4 c = *reinterpret_cast<const float4*>(logits + r * stride + i + 2);
-            const float2 f = *reinterpret_cast<const float2*>(factors + 2 * r);
-            sum.x = fmaf(a.y, f.y, fmaf(a.x, f.x, sum.x));
-            sum.y = fmaf(a.w, f.y, fmaf(a.z, f.x, sum.y));
-            sum.z = fmaf(c.y, f.y, fmaf(c.x, f.x, sum.z));
-            sum.w = fmaf(c.w, f.y, fmaf(c.z, f.x, sum.w));
+            const uint64_t f = *reinterpret_cast<const uint64_t*>(factors + 2 * r);
+            sum[0] = fma_f32x2(pair_f32(a.x, a.y), f, sum[0]);
+            sum[1] = fma_f32x2(pair_f32(a.z, a.w), f, sum[1]);
+            sum[2] = fma_f32x2(pair_f32(c.x, c.y), f, sum[2]);
+            sum[3] = fma_f32x2(pair_f32(c.z, c.w), f, sum[3]);
         }
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float even, odd;
+            split_f32(sum[k], even, odd);
+            v[k] = even + odd;
+        }
         store_weights(p, to, j, begin, end, older, v);
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -803,11 +829,13 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
             if (threadIdx.x % kLanes == 0) stats[r] = make_float2(m == -INFINITY ? 0.0f : m, l > 0.0f ? 1.0f / l : 0.0f);
         }
         __syncthreads();
-        float2 st[HALVES][2];
+        uint64_t minus_m[HALVES], factor[HALVES];
 #pragma unroll
-        for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) st[x][y] = stats[8 * x + 2 * t + y];
+        for (int x = 0; x < HALVES; ++x) {
+            const float2 even = stats[8 * x + 2 * t], odd = stats[8 * x + 2 * t + 1];
+            minus_m[x] = pair_f32(-even.x, -odd.x);
+            factor[x] = pair_f32(even.y, odd.y);
+        }
         int token = first * kTile + warp * 32 + g;
         const Edges edges(p.a, seq, row0, rows);
         float* to = sums + (first - tile0) * kTile + warp * 32 + g;
@@ -819,12 +847,17 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
             float sum[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                sum[k] = 0.0f;
+                uint64_t both = pair_f32(0.0f, 0.0f);
 #pragma unroll
-                for (int x = 0; x < HALVES; ++x)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        sum[k] = fmaf(exp2_approx(fmaf(s[k / 2][x][2 * (k % 2) + y], q.unit[x][y], -st[x][y].x)), st[x][y].y, sum[k]);
+                for (int x = 0; x < HALVES; ++x) {
+                    const float* v = s[k / 2][x] + 2 * (k % 2);
+                    float a, b;
+                    split_f32(fma_f32x2(pair_f32(v[0], v[1]), pair_f32(q.unit[x][0], q.unit[x][1]), minus_m[x]), a, b);
+                    both = fma_f32x2(pair_f32(exp2_approx(a), exp2_approx(b)), factor[x], both);
+                }
+                float a, b;
+                split_f32(both, a, b);
+                sum[k] = a + b;
             }
             // over the four lanes of a token: each ends with one of its four tokens
             const bool odd = t & 1, high = t & 2;
@@ -873,18 +906,19 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
     const int64_t rows = max_q * G;
     w.halves = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const int64_t blocks = (rows + 8 * w.halves - 1) / (8 * w.halves), tiles = (max_kv + kTile - 1) / kTile;
-    const int64_t wanted = 8 * (int64_t)sms, base = std::max<int64_t>(B * H * blocks, 1);
+    const int64_t base = std::max<int64_t>(B * H * blocks, 1);
     const int64_t one_tiles = (max_kv + kOneTile - 1) / kOneTile;
     // One launch: 96 sequences of 16384 tokens (4 bits, 8 x 128, four queries a head) 249 us
     // with 8 CTAs a cluster and 277 with 4; 48 of 32768, twice the logits a CTA, 283, and 450
     // by the two kernels.  With 16 rows two blocks run on an SM all the same: 64 of up to
     // 4096 in 72 us with 4 CTAs, 126 with 8, 124 by the two kernels.  With 32 rows one does:
-    // only where there is no more.
+    // only where there is no more.  Beginning a block costs more than an SM gains by a fourth:
+    // 24 of 4096 (8 rows, 8 bits) 46 us with 2 CTAs and 52 with 4, 16 of 1000 7.6 and 9.6.
     for (int64_t size = 1; size <= 8 && blocks == 1; size *= 2) {
         const int64_t chunk = (one_tiles + size - 1) / size;
         const size_t smem = (size_t)((rows + 1) / 2) * (size_t)(chunk * kOneTile + 8) * sizeof(float2);
         if (smem > (size < 8 && w.halves == 1 ? kFewLogits : kMostLogits)) continue;
-        if (size < 8 && base * size < wanted && size < one_tiles) continue;
+        if (size < 8 && 2 * base * size < 3 * (int64_t)sms && size < one_tiles) continue;
         if (w.halves == 4 && base * size > 2 * sms) break;
         w.fused = true;
         w.splits = (int)size;
@@ -893,7 +927,12 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
         w.stats_blocks = w.sum_blocks = base * size;
         return w;
     }
-    w.splits = (int)std::min<int64_t>(std::min<int64_t>(64, tiles), std::max<int64_t>(1, (wanted + base - 1) / base));
+    // (two chunks of 16 tokens over 8192, 64 rows a head: 20 and 29 us with three blocks an SM in
+    // each kernel, 29 and 50 with eight; 16 of 16384 with 32 rows 73 + 95 and 89 + 105.  The
+    // first kernel with up to 8 rows, five blocks of which run on an SM: 8 of 131072 tokens 100
+    // us with eight blocks, 112 with three)
+    const int64_t wanted = 3 * (int64_t)sms, wanted_stats = (w.halves == 1 ? 8 : 3) * (int64_t)sms;
+    w.splits = (int)std::min<int64_t>(std::min<int64_t>(64, tiles), std::max<int64_t>(1, (wanted_stats + base - 1) / base));
     w.chunk = (int)std::min<int64_t>(kChunk, std::max<int64_t>(1, B * H * tiles / wanted));
     w.stats_blocks = B * H * blocks * w.splits;
     w.sum_blocks = B * H * ((tiles + w.chunk - 1) / w.chunk);
