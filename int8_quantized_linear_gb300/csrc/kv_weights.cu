@@ -19,13 +19,14 @@
 // A weight needs its row's maximum and sum, which need all keys.  While a cluster's
 // shared memory holds the logits of a cache head (one token's rows, contexts up to 32768
 // with four query heads), one launch reads the keys once: 96 sequences of 16384 tokens, 8 x
-// 128 channels, 4 bits, 249 us, of 143 for the bytes (3.8 TB/s; the products, the
+// 128 channels, 4 bits, 248 us, of 143 for the bytes (3.8 TB/s; the products, the
 // exchange and the sums of a block follow each other, and four blocks an SM cover for it).
 // Otherwise two kernels both go over the keys.  The first leaves each row's (m, l) over
 // a part of the tokens, the second joins them and sums the weights of its tokens over all
 // rows, in order; no atomics.  16 sequences of up to 8191 tokens with 64 rows a
-// head (8 x 64 channels, 8 bits): 60 and 53 us, bound by the instructions beside
-// the products (unpacking per 32 rows, an exponential a logit and pass; issue slots 50 %).
+// head (16 heads x 64 channels, 8 bits): 57 and 52 us, bound by the instructions beside
+// the products (unpacking per 32 rows, an exponential a logit and pass; issue slots 50 %, 11
+// warps an SM) and by the beginnings and ends of blocks.
 // Tokens that no row sees keep what they have.
 //
 // The layout of the products is that of kv_attention.cu: 16 tokens are the M rows
@@ -908,10 +909,10 @@ WeightsPlan weights_plan(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_
     const int64_t blocks = (rows + 8 * w.halves - 1) / (8 * w.halves), tiles = (max_kv + kTile - 1) / kTile;
     const int64_t base = std::max<int64_t>(B * H * blocks, 1);
     const int64_t one_tiles = (max_kv + kOneTile - 1) / kOneTile;
-    // One launch: 96 sequences of 16384 tokens (4 bits, 8 x 128, four queries a head) 249 us
-    // with 8 CTAs a cluster and 277 with 4; 48 of 32768, twice the logits a CTA, 283, and 450
-    // by the two kernels.  With 16 rows two blocks run on an SM all the same: 64 of up to
-    // 4096 in 72 us with 4 CTAs, 126 with 8, 124 by the two kernels.  With 32 rows one does:
+    // One launch: 96 sequences of 16384 tokens (4 bits, 8 x 128, four queries a head) 248 us
+    // with 8 CTAs a cluster and 277 with 4; 48 of 32768, twice the logits a CTA, 288, and 342
+    // by the two kernels for as many tokens.  With 16 rows two blocks run on an SM all the same: 64 of up to
+    // 4096 in 73 us with 4 CTAs, 126 with 8; 16 of 4000 in 29, and 39 by the two kernels.  With 32 rows one does:
     // only where there is no more.  Beginning a block costs more than an SM gains by a fourth:
     // 24 of 4096 (8 rows, 8 bits) 46 us with 2 CTAs and 52 with 4, 16 of 1000 7.6 and 9.6.
     for (int64_t size = 1; size <= 8 && blocks == 1; size *= 2) {
