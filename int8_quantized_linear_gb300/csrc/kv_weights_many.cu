@@ -32,7 +32,7 @@
 // adds those up: no atomics, the same bits whatever the timing.
 //
 // Two chunks of 2048 tokens over 8192 (32 query heads, 8 cache heads, 128 channels, 4 bits):
-// 312 and 387 us and 7 for the joining, 243 GFLOP a pass, 780 and 630 TFLOP/s.  Bound by
+// 312 and 376 us and 7 for the joining, 243 GFLOP a pass, 780 and 645 TFLOP/s.  Bound by
 // the roles together: the products alone (nothing unpacked, no softmax) take 240 us a
 // pass, the softmax alone 221 and 283.  Measured and dropped: 256 rows a product in the
 // second pass (397 against 376 us), three stages with 8 warps unpacking every tile and
@@ -116,8 +116,6 @@ __device__ __forceinline__ Work find_work(const KvWeightsParams& p) {
         const int chunk = (int)(at % p.chunks);
         at /= p.chunks;
         w.chunk0 = chunk * p.chunk;
-        w.part = (int)(at % p.groups);
-        at /= p.groups;
     } else {
         w.part = (int)(at % p.splits);
         at /= p.splits;
@@ -125,7 +123,10 @@ __device__ __forceinline__ Work find_work(const KvWeightsParams& p) {
     w.h = (int)(at % p.a.cache.H);
     at /= p.a.cache.H;
     if constexpr (SUM) {
-        w.b = at;
+        // (late rows see most: first, of all sequences; 8192 tokens over themselves 474 us with
+        // the early rows first, 420 so)
+        w.part = p.groups - 1 - (int)(at / p.a.B);
+        w.b = at % p.a.B;
         w.seq = many_sequence(p, w.b);
         const int blocks = kv_blocks<kRows>(p.a, w.seq);
         w.rb0 = (int)((int64_t)blocks * w.part / p.groups);
