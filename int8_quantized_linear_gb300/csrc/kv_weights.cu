@@ -12,7 +12,11 @@
 // element makes up for by a 16th.  So unpacking is masks alone, five instructions for
 // eight 4-bit codes (and nine to make centred integers of them: see kv_math.cuh).
 // q is scaled by a power of two per row that brings its largest element to 2^14;
-// elements 2^-28 of that round.  Logits, maxima and sums are fp32.  Maximum and sum are
+// elements 2^-28 of that round.  Logits, maxima and sums are fp32.  What a product counts is
+// a power of two: c's mantissa is multiplied into the scales and the sum of q.  So a maximum
+// is a logit without rounding, and an exponent a - m, taken in one step from the product, is 0
+// for the largest, however large the logits are.  (With the mantissa in that step an exponent
+// misses what m was rounded by, which leaves fp32 where logits reach 2^31.)  Maximum and sum are
 // kept apart (2^(a - m) / l, not 2^(a - m - log2 l)): beside a large m the logarithm
 // would lose its bits.
 //
@@ -36,6 +40,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kv_tc.cuh"
@@ -75,16 +80,23 @@ __device__ __forceinline__ KvSeq weights_sequence(const KvWeightsParams& p, int6
     return s;
 }
 
+// What a product counts, in log2 units, where the row's largest element has the exponent e.
+// (Not 0: what is not seen, -inf, times 0 would be no number.)
+__device__ __forceinline__ float product_unit(const KvScale& scale, int e) {
+    return pow2(min(max(e - 14 + 24 + scale.exponent, -126), 127));
+}
+
 // A lane's share of 8 HALVES query rows.
 template <int D, int BITS, int HALVES>
 struct Queries {
     uint32_t f[D / 16][HALVES][2];  // B operand: rows g + 8 x, permuted as the keys' unpacking pairs channels
     // of rows 2t + y + 8 x, whose logits the lane holds:
-    float sum[HALVES][2];          // the scaled row's sum, times 2^-24
-    float unit[HALVES][2];         // what a product counts, in log2 units
+    float sum[HALVES][2];          // the scaled row's sum, times 2^-24 and c's mantissa
+    float unit[HALVES][2];         // what a product counts, in log2 units: a power of two
     int hi[HALVES][2], lo[HALVES][2];  // the tokens the row sees: lo .. hi (none: hi < lo)
 
-    __device__ __forceinline__ void load(const KvAttnParams& p, const KvSeq& seq, int h, int row0, int rows) {
+    __device__ __forceinline__ void load(const KvAttnParams& p, const KvScale& scale, const KvSeq& seq, int h, int row0,
+                                         int rows) {
         const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
         const int base = seq.len - seq.nq;
 #pragma unroll
@@ -133,9 +145,8 @@ struct Queries {
             }
             total += __shfl_xor_sync(0xffffffffu, total, 1);
             total += __shfl_xor_sync(0xffffffffu, total, 2);
-            // (not 0: what is not seen, -inf, times 0 would be no number)
-            const float u = fmaxf(pow2(e - 14) * (fabsf(p.scale_log2) * 0x1p24f), 0x1p-126f);
-            total *= 0x1p-24f;
+            const float u = product_unit(scale, e);
+            total *= 0x1p-24f * scale.mantissa;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int from = 4 * (2 * t + y);  // a lane that loaded row 2t + y
@@ -159,7 +170,7 @@ struct SharedQueries {
     int hi[ROWS], lo[ROWS];
 
     template <int WARPS>
-    __device__ __forceinline__ void make(const KvAttnParams& p, const KvSeq& seq, int h, int rows) {
+    __device__ __forceinline__ void make(const KvAttnParams& p, const KvScale& scale, const KvSeq& seq, int h, int rows) {
         const int lane = threadIdx.x % 32;
 #pragma unroll
         for (int r = threadIdx.x / 32; r < ROWS; r += WARPS) {
@@ -191,9 +202,8 @@ struct SharedQueries {
                                                       pack_f16(y[6], y[7]));
             }
             if (lane == 0) {
-                sum[r] = total * 0x1p-24f;
-                // (not 0: what is not seen, -inf, times 0 would be no number)
-                unit[r] = fmaxf(pow2(e - 14) * (fabsf(p.scale_log2) * 0x1p24f), 0x1p-126f);
+                sum[r] = total * (0x1p-24f * scale.mantissa);
+                unit[r] = product_unit(scale, e);
                 const int at = seq.len - seq.nq + i;
                 hi[r] = live ? at : -1;
                 lo[r] = p.window > 0 ? (int)max(at + 1 - p.window, (int64_t)0) : 0;
@@ -236,7 +246,8 @@ struct Keys {
     // Logits, in units of their rows, of tokens g + 16 i (+ 8) and rows 2t, 2t + 1 (+ 8 x).
     // EDGE: some row does not see some token: -inf there.
     template <bool EDGE, int HALVES>
-    __device__ __forceinline__ void logits(const Queries<D, BITS, HALVES>& q, int token, float (&s)[2][HALVES][4]) const {
+    __device__ __forceinline__ void logits(const Queries<D, BITS, HALVES>& q, float mantissa, int token,
+                                           float (&s)[2][HALVES][4]) const {
         constexpr int kPairs = 16 / BITS;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -261,7 +272,7 @@ struct Keys {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                const float scale = kv_scale(param[2 * i + z]), low = kv_low(param[2 * i + z]);
+                const float scale = kv_scale(param[2 * i + z]) * mantissa, low = kv_low(param[2 * i + z]);
                 const uint64_t scale2 = pair_f32(scale, scale), low2 = pair_f32(low, low);
                 const int j = token + 16 * i + 8 * z;
 #pragma unroll
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
 #pragma unroll
         for (int x = 0; x < HALVES; ++x) top[x][0] = top[x][1] = -INFINITY;
         KeyRing<D, BITS, kOneWarps, kOneStages> ring(p.a, table, smem, h, tile0, tile1, begin, end);
-        queries.template make<kOneWarps>(p.a, seq, h, rows);
+        queries.template make<kOneWarps>(p.a, p.scale, seq, h, rows);
         __syncthreads();
         Queries<D, BITS, HALVES> q;
         queries.load(q);
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(kOneThreads, HALVES == 1 ? 4 : HALVES == 2 ? 2
             Keys<D, BITS> now;
             ring.take(now);
             float s[2][HALVES][4];
-            now.template logits<decltype(edge)::value>(q, token, s);
+            now.template logits<decltype(edge)::value>(q, p.scale.mantissa, token, s);
 #pragma unroll
             for (int x = 0; x < HALVES; ++x) {
                 if (8 * x + 2 * t < rows) {
@@ -742,14 +753,14 @@ __global__ void __launch_bounds__(kThreads) kv_stats_kernel(const KvWeightsParam
         KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, span.first + first, span.first + last, span.begin,
                                                           span.end);
         Queries<D, BITS, HALVES> q;
-        q.load(p.a, seq, h, row0, rows);
+        q.load(p.a, p.scale, seq, h, row0, rows);
         int token = (span.first + first) * kTile + warp * 32 + g;
         const Edges edges(p.a, seq, row0, rows);
         auto step = [&](auto edge) {
             Keys<D, BITS> now;
             ring.take(now);
             float s[2][HALVES][4];
-            now.template logits<decltype(edge)::value>(q, token, s);
+            now.template logits<decltype(edge)::value>(q, p.scale.mantissa, token, s);
             add_logits<D, BITS, HALVES>(m, l, s, q);
         };
         for (int i = first; i < last; ++i, token += kTile) {
@@ -810,7 +821,7 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
         // keys, rows and their statistics wait together
         KeyRing<D, BITS, kWarps, kStages<D, BITS>> ring(p.a, table, smem, h, first, last, span.begin, span.end);
         Queries<D, BITS, HALVES> q;
-        q.load(p.a, seq, h, row0, rows);
+        q.load(p.a, p.scale, seq, h, row0, rows);
         __syncthreads();
         {  // several lanes a row
             constexpr int kLanes = kThreads / ROWS;
@@ -844,7 +855,7 @@ __global__ void __launch_bounds__(kThreads) kv_sum_kernel(const KvWeightsParams 
             Keys<D, BITS> now;
             ring.take(now);
             float s[2][HALVES][4];
-            now.template logits<decltype(edge)::value>(q, token, s);
+            now.template logits<decltype(edge)::value>(q, p.scale.mantissa, token, s);
             float sum[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -988,6 +999,9 @@ cudaError_t launch_kv_weights(KvWeightsParams p, int64_t D, int64_t bits, void* 
     p.stats = static_cast<float2*>(workspace);
     p.splits = w.splits;
     p.chunk = w.chunk;
+    // (1 <= mantissa < 2; a scale of 0: 0)
+    p.scale.mantissa = 2.0f * std::frexp(std::fabs(p.a.scale_log2), &p.scale.exponent);
+    --p.scale.exponent;
     if (D == 64) return bits == 4 ? launch_rows<64, 4>(p, w, env) : launch_rows<64, 8>(p, w, env);
     return bits == 4 ? launch_rows<128, 4>(p, w, env) : launch_rows<128, 8>(p, w, env);
 }

@@ -6,6 +6,12 @@
 
 namespace i8ql {
 
+// |softmax scale * log2 e| = mantissa * 2^exponent.
+struct KvScale {
+    float mantissa;
+    int exponent;
+};
+
 struct KvWeightsParams {
     KvAttnParams a;         // (out and the parts of its join unused)
     int64_t max_q;          // the most query tokens a sequence may have
@@ -14,6 +20,7 @@ struct KvWeightsParams {
     float2* stats;          // [T_q * Hq][splits]: a row's (maximum, sum) over a part of the tokens
     int splits;             // (one launch: CTAs of a cluster)
     int chunk;              // tiles of a block that sums (one launch: at most, of a CTA)
+    KvScale scale;          // (few query rows)
     // many query rows only:
     int chunks;             // blocks of the tiles
     int groups;             // of row blocks that are summed together
