@@ -615,6 +615,9 @@ i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf1
  * and low value are operands too: q's elements 2^-25 of the largest of 16
  * neighbouring rows, and keys 2^-21 of the largest of 128 neighbouring tokens,
  * lose bits.
+ * Logits may be large: what they are off by is as above, but a row's weights sum
+ * to 1 while its logits stay in fp32's range (|softmax_scale| log2 e D times the
+ * largest |q| and |k| up to 2^127; beyond, they are unspecified).
  * max_q: the most query tokens of one sequence (more record
  * I8QL_ERR_BAD_INDEX); pages out of range record it too and are not written.
  * workspace as kv_cache_attention, i8ql_kv_weights_workspace bytes.  The

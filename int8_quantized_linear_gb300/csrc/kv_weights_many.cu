@@ -25,7 +25,17 @@
 // 2^21 below it lose bits.  A row of Q is scaled to 2^14 (first pass) or its 16 rows
 // together are (second pass, where rows are columns: rows 2^14 below the largest of
 // their 16 keep 2^-25 of it).  In the second pass a row's maximum and sum are
-// one number, n_i = m_i + log2 l_i, rounded to 2^-24 of it, as the logits themselves are.
+// one number, n_i = m_i + log2 l_i, rounded to 2^-24 of it, while no maximum of its half
+// exceeds kNear.
+//
+// Large logits: a row's sum is relative to a reference r, an fp32 number near its maximum, and
+// an exponent is taken in one step, c x - r with the product not rounded.  So both passes mean
+// the same by it, but the largest exponent is not 0: it is what r was rounded by, which a sum
+// has room for up to logits of 2^28.  Beyond, a row is far: r is the largest of its products
+// q k themselves, which is taken off the others before the scale is multiplied in, so that the
+// largest has the exponent 0, however large it is.  Tiles where logits could come near that
+// (their exponents say so), and halves with large maxima in the second pass, go through
+// functions of their own.  (The question costs the first pass 2 % with 128 channels of 4 bits.)
 //
 // The second pass leaves sums over up to 128-row halves of a group of row blocks per
 // token in a workspace (a thread adds to its own place, in order), and a third kernel
@@ -49,6 +59,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "kv_tc.cuh"
 #include "kv_weights.cuh"
@@ -170,10 +181,39 @@ __device__ __forceinline__ Part find_part(const KvWeightsParams& p, const Work& 
     return r;
 }
 
-// A row's sum so far, relative to 2^ref; nothing yet: ref is -inf.
+// A row's sum so far, relative to 2^ref; nothing yet: ref is -inf.  A negative sum: of a far
+// row, whose ref is a product q k.
 struct RowStats {
     float ref, sum;
 };
+constexpr float kNear = 4096.0f;
+constexpr float kFar = 0x1p28f;
+// Of a row's unit and a tile whose exponents add up to no more, what S counts is below 2^-6, and S
+// is below 2^32 (128 channels of 2^15 x 2^8, and as much for the offsets): logits below 2^26.
+constexpr int kFarExp = 127 + 127;
+constexpr float kMostFloat = 3.402823466e38f;
+
+// Products off by a power of two, 2^shift (|shift| <= 252), as they are, or the largest number.
+struct Shift {
+    float a, b;
+    __device__ __forceinline__ explicit Shift(int shift) : a(pow2(shift >> 1)), b(pow2(shift - (shift >> 1))) {}
+    __device__ __forceinline__ float operator()(uint32_t x) const {
+        return fminf(fmaxf(__uint_as_float(x) * a * b, -kMostFloat), kMostFloat);
+    }
+};
+
+// A reference is far scale + near.
+__device__ __forceinline__ float far_part(const RowStats& r) { return r.sum < 0.0f ? r.ref : 0.0f; }
+__device__ __forceinline__ float near_part(const RowStats& r) { return r.sum < 0.0f ? 0.0f : r.ref; }
+
+// A row's sum over two sets of tokens.
+__device__ __forceinline__ RowStats join_rows(const RowStats& a, const RowStats& b, float scale) {
+    if (b.ref == -INFINITY) return a;
+    if (a.ref == -INFINITY) return b;
+    const float d = fmaf(far_part(b) - far_part(a), scale, near_part(b) - near_part(a));
+    const RowStats high = d > 0.0f ? b : a, low = d > 0.0f ? a : b;
+    return {high.ref, copysignf(fmaf(fabsf(low.sum), exp2_approx(-fabsf(d)), fabsf(high.sum)), high.sum)};
+}
 
 // Raises a row's reference to the maximum.
 __device__ __forceinline__ void raise(RowStats& r, float to) {
@@ -183,9 +223,8 @@ __device__ __forceinline__ void raise(RowStats& r, float to) {
 
 // A tile of S of a row that sees all its tokens.  The exponents are relative to what the
 // sum is: where one exceeds the slack (rare: the first time, and then as larger logits
-// come), the reference is raised and all is done again.  Once: a reference is a rounded
-// number and an exponent is not rounded before it is taken off, so beside references from
-// 2^28 on an exponent exceeds the slack however often that is done.  (Asked once a tile: a vote
+// come), the reference is raised and all is done again.  Once: what a reference is rounded by
+// would exceed the slack from 2^28 on, however often that is done.  (Asked once a tile: a vote
 // after every 32 columns keeps the next ones from being loaded, 295 against 221 us for
 // the softmax alone of two chunks of 2048 tokens over 8192.)
 __device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, float unit) {
@@ -221,6 +260,46 @@ __device__ __forceinline__ void add_tokens(RowStats& r, uint32_t s_at, float uni
     }
 }
 
+// A tile of a warp with far rows, or whose logits could make some: products off by 2^shift,
+// of which the row sees lo .. hi.
+__device__ __noinline__ RowStats add_far_tokens(RowStats r, uint32_t s_at, int shift, float scale, int token, int lo, int hi) {
+    const Shift product(shift);
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        uint32_t x[32];
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int tok = token + q * 32 + j;
+            top = tok <= hi && tok >= lo ? fmaxf(top, product(x[j])) : top;
+        }
+    }
+    float far = far_part(r), near = near_part(r), sum = fabsf(r.sum);
+    if (top > -INFINITY && (r.ref == -INFINITY || fmaf(top - far, scale, -near) > 0.0f)) {
+        const float logit = top * scale;
+        const bool large = !(fabsf(logit) < kFar);
+        const float to_far = large ? top : 0.0f, to_near = large ? 0.0f : logit;
+        sum = r.ref == -INFINITY ? 0.0f : sum * exp2_approx(fmaf(far - to_far, scale, near - to_near));
+        far = to_far;
+        near = to_near;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int q = 0; q < kTile / 32; ++q) {
+        uint32_t x[32];
+        tmem_ld32(s_at + q * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int tok = token + q * 32 + j;
+            sum += tok <= hi && tok >= lo ? exp2_approx(fmaf(product(x[j]) - far, scale, -near)) : 0.0f;
+        }
+    }
+    return far != 0.0f ? RowStats{far, -sum} : RowStats{near, sum};
+}
+
 // A tile where some row does not see some token: this one sees lo .. hi.
 __device__ __noinline__ RowStats add_some_tokens(RowStats r, uint32_t s_at, float unit, int token, int lo, int hi) {
 #pragma unroll 1
@@ -232,25 +311,31 @@ __device__ __noinline__ RowStats add_some_tokens(RowStats r, uint32_t s_at, floa
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const int tok = token + q * 32 + j;
-            x[j] = __float_as_uint(tok <= hi && tok >= lo ? __uint_as_float(x[j]) * unit : -INFINITY);
+            x[j] = __float_as_uint(tok <= hi && tok >= lo ? __uint_as_float(x[j]) : -INFINITY);
             top = fmaxf(top, __uint_as_float(x[j]));
         }
+        top = top > -INFINITY ? top * unit : top;
         if (top > r.ref + kSlack || (r.ref == -INFINITY && top > -INFINITY)) raise(r, top);
         const float ref = r.ref == -INFINITY ? 0.0f : -r.ref;
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum += exp2_approx(__uint_as_float(x[j]) + ref);
+        for (int j = 0; j < 32; ++j) {
+            const float v = __uint_as_float(x[j]);
+            sum += v > -INFINITY ? exp2_approx(fmaf(v, unit, ref)) : 0.0f;
+        }
         r.sum += sum;
     }
     return r;
 }
 
 // What the softmax needs of a half's rows: what a product counts (in log2 units, times
-// the tile's), where rows are columns -n, and the last token that the row sees.
+// the tile's), where rows are columns -n, and the last token that the row sees; for large
+// logits what products are off by, as a power of two, and n in its parts.
 constexpr int kGroup = 16;  // rows that share a unit where they are columns: those a warp takes up
 struct RowFactors {
     float unit[kTile], minus_n[kTile];
-    int hi[kTile];
+    int hi[kTile], shift[kTile];
+    float far[kTile], near[kTile], minus_log[kTile];
 };
 
 // The sum of 32 rows' weights of a token.
@@ -281,6 +366,28 @@ __device__ __forceinline__ void add_rows(uint64_t (&sum)[2], uint32_t s_at, cons
     }
 }
 
+// The sum of all rows' weights of a token in a half with large maxima, its tile's products off
+// by 2^shift.  (No weight exceeds 1: a product may come out above the largest of the
+// first pass where its row has lost bits.)
+__device__ __noinline__ float add_far_rows(uint32_t s_at, const RowFactors& f, int columns, int shift, float scale, int token,
+                                           int64_t window) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < columns * 32; c0 += 32) {
+        uint32_t x[32];
+        tmem_ld32(s_at + c0, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const Shift product(f.shift[c0 + j / kGroup * kGroup] + shift);
+            const int hi = f.hi[c0 + j];
+            const float v = fmaf(product(x[j]) - f.far[c0 + j], scale, -f.near[c0 + j]) + f.minus_log[c0 + j];
+            sum += token <= hi && (window == 0 || token > hi - window) ? exp2_approx(fminf(v, 0.0f)) : 0.0f;
+        }
+    }
+    return sum;
+}
+
 // fp16 parts of x: x = hi + lo but for 2^-22 of it.
 __device__ __forceinline__ void split_f16(float x, uint32_t& hi, uint32_t& lo) {
     const __half h = __float2half_rn(x);
@@ -299,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
     __shared__ int tile_exp[kInfo];        // a tile is held times 2^(134 - tile_exp)
     __shared__ uint32_t factors[2][kTile];  // a token's scale, twice, as halves
     __shared__ __align__(16) RowFactors row_factors[2];
+    __shared__ __align__(16) int large_rows[2][4];  // SUM: which warps' rows have large maxima among them
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -657,27 +765,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                             sts16(smem_at + C::kOffMoreQ + row * 128 + (((2 * m + w) ^ (row & 7)) << 4), w ? 0 : q_hi | q_lo << 16,
                                   w ? 0 : q_hi, 0, 0);
                         }
-                        if (w == 0) rf.unit[row] = pow2(e - 14) * fabsf(p.a.scale_log2);
+                        if (w == 0) {
+                            rf.unit[row] = pow2(e - 14) * fabsf(p.a.scale_log2);
+                            rf.shift[row] = e - 14;
+                        }
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&q_full[m]);
                     if (SUM && set == 0) {
                         float top_m = -INFINITY, l = 0.0f;
+                        bool far = false;
                         if (live) {
 #pragma unroll 4
                             for (int s = 0; s < p.splits; ++s) {
                                 const float2 x = p.stats[stat + s];
+                                far = far || x.y < 0.0f;
                                 const float to = fmaxf(top_m, x.x), shift = to == -INFINITY ? 0.0f : to;
                                 l = l * exp2_approx(top_m - shift) + x.y * exp2_approx(x.x - shift);
                                 top_m = to;
                             }
                         }
-                        rf.minus_n[r_m] = l > 0.0f ? -(top_m + log2f(l)) : -INFINITY;
+                        RowStats all = {top_m, l};
+                        if (__any_sync(0xffffffffu, far)) {  // (rare)
+                            all = {-INFINITY, 0.0f};
+#pragma unroll 1
+                            for (int s = 0; live && s < p.splits; ++s) {
+                                const float2 x = p.stats[stat + s];
+                                all = join_rows(all, RowStats{x.x, x.y}, fabsf(p.a.scale_log2));
+                            }
+                        }
+                        const bool nothing = all.ref == -INFINITY;
+                        const float near = nothing ? 0.0f : near_part(all);
+                        const float minus_log = nothing ? -INFINITY : -log2f(fabsf(all.sum));
+                        rf.minus_n[r_m] = minus_log - near;
+                        rf.far[r_m] = far_part(all);
+                        rf.near[r_m] = near;
+                        rf.minus_log[r_m] = minus_log;
+                        const bool large = all.sum < 0.0f || !(fabsf(near) < kNear);
+                        const int some_large = __any_sync(0xffffffffu, large);
+                        if (lane == 0) large_rows[m][warp % 4] = some_large;
                         rf.hi[r_m] = live ? hi : -1;
                     }
                 }
                 half_sync();
                 const float own_unit = SUM ? 1.0f : rf.unit[r_m];
+                // tiles of larger exponents take the functions for large logits: first pass, as the warp's
+                // units are (from its first far row on all tiles); second, all where some maximum of the half is large
+                int most_exp;
+                if constexpr (SUM) {
+                    const int4 some = *reinterpret_cast<const int4*>(large_rows[m]);
+                    most_exp = (some.x | some.y | some.z | some.w) != 0 ? -1 : 255;
+                } else {
+                    most_exp = kFarExp - (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(own_unit)) >> 23);
+                }
                 // tokens [all_lo, all_hi] are seen by every row of the half
                 const int all_hi = base + (r.row0 + m * 128) / p.a.G;
                 const int last = r.row0 + min(r.rows, m * 128 + 128) - 1;
@@ -700,17 +840,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                         const bool edge = token + kTile - 1 > all_hi || token < all_lo;
                         const float unit = own_unit * pow2(tile_exp[k % kInfo] - 134);
                         if constexpr (SUM) {
-                            uint64_t sum[2] = {0, 0};
+                            float all;
+                            if (__builtin_expect(most_exp < 0, 0)) {
+                                all = add_far_rows(s_at, rf, columns, tile_exp[k % kInfo] - 134, fabsf(p.a.scale_log2),
+                                                   token + r_m, p.a.window);
+                            } else {
+                                uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-                            for (int q = 0; q < columns; ++q) {
-                                if (edge)
-                                    add_rows<true>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, p.a.window);
-                                else
-                                    add_rows<false>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, 0);
+                                for (int q = 0; q < columns; ++q) {
+                                    if (edge)
+                                        add_rows<true>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, p.a.window);
+                                    else
+                                        add_rows<false>(sum, s_at + q * 32, rf, q * 32, unit, token + r_m, 0);
+                                }
+                                float a, b;
+                                split_f32(add_f32x2(sum[0], sum[1]), a, b);
+                                all = a + b;
                             }
-                            float a, b;
-                            split_f32(add_f32x2(sum[0], sum[1]), a, b);
-                            part[(int64_t)tile * kTile] = before + (a + b);
+                            part[(int64_t)tile * kTile] = before + all;
+                        } else if (__builtin_expect(tile_exp[k % kInfo] > most_exp, 0)) {
+                            stats = add_far_tokens(stats, s_at, rf.shift[r_m] + tile_exp[k % kInfo] - 134,
+                                                   fabsf(p.a.scale_log2), token, edge ? lo : 0, edge ? hi : INT_MAX);
+                            if (__any_sync(0xffffffffu, stats.sum < 0.0f)) most_exp = -1;
                         } else if (edge) {
                             stats = add_some_tokens(stats, s_at, unit, token, lo, hi);
                         } else {
@@ -731,13 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_weights_many_kernel(const KvWe
                 }
                 half_sync();
                 if (set == 0 && live) {
-                    RowStats other = {rf.unit[r_m], rf.minus_n[r_m]};
-                    if (other.ref > stats.ref) {
-                        const RowStats swap = stats;
-                        stats = other;
-                        other = swap;
-                    }
-                    if (other.ref > -INFINITY) stats.sum = fmaf(other.sum, exp2_approx(other.ref - stats.ref), stats.sum);
+                    stats = join_rows(stats, RowStats{rf.unit[r_m], rf.minus_n[r_m]}, fabsf(p.a.scale_log2));
                     p.stats[stat + work.part] = make_float2(stats.ref, stats.sum);
                 }
             }

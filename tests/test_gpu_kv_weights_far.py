@@ -159,3 +159,82 @@ def test_few_rows_of_any_scale(form, scale):
         c = Cache(lens, hq, heads, 64, 4, page, nqs, seed=form, wide=wide)
         rescale(c, 0, far)
         check_rows(c, c.weigh(scale=scale), 2.0 ** -19 + 2.0 ** -12)
+
+
+# Many query rows: both halves of a row block and one, several row blocks, several parts of the tokens, and a table so wide
+# that row blocks share their sums.  (lens, queries, query heads, heads, page, pages more in the table, window)
+MANY = [
+    ([900, 300], [150, 60], 4, 2, 32, 0, 0),
+    ([700, 131], [90, 131], 8, 2, 16, 0, 0),
+    ([1500], [600], 3, 1, 64, 0, 0),
+    ([1330, 40], [1030, 33], 4, 1, 256, 4096, 0),
+    ([6000, 300], [17, 20], 16, 4, 64, 0, 0),
+    ([1500, 300], [200, 70], 4, 2, 32, 0, 100),
+]
+
+
+def near(far):
+    """How far logits up to 2^12 may be off in a row's exponents, relative to each other: products rounded to 2^-24 of
+    them where some row does not see some token, reference and logarithm of the sum rounded as one number."""
+    return 2.0 ** -23 * min(2.0 ** (far + 5), 2.0 ** 13)
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 128), (4, 64), (8, 64)])
+@pytest.mark.parametrize("far", SIZES)
+@pytest.mark.parametrize("form", range(len(MANY)))
+def test_many_rows(form, far, bits, d):
+    lens, nqs, hq, heads, page, wide, window = MANY[form]
+    c = Cache(lens, hq, heads, d, bits, page, nqs, seed=form, wide=wide)
+    rescale(c, 0, far)
+    w = c.weigh(window)
+    if window:
+        seen = [np.arange(n) >= n - nq + 1 - window for n, nq in zip(lens, nqs)]
+        for i in range(len(lens)):
+            assert (of(c, w, i)[:, ~seen[i]] == -5.0).all()
+        w = torch.where(w == -5.0, torch.zeros(()).cuda(), w)
+    # (and logarithms and exponentials to 2^-19)
+    check_rows(c, w, 2.0 ** -18 + near(far))
+    assert far < 20 or window or check_pinned(c, w, d ** -0.5) > 0.5
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("far", SIZES)
+@pytest.mark.parametrize("form", [0, 1, 2, 3, 4])
+def test_many_rows_of_equal_keys(form, far, bits, d):
+    lens, nqs, hq, heads, page, wide, _ = MANY[form]
+    c = Cache(lens, hq, heads, d, bits, page, nqs, seed=form, wide=wide)
+    rescale(c, 0, far)
+    equal_keys(c, 0)
+    w, want = of(c, c.weigh(), 0), uniform(c, 0)
+    assert (np.abs(w / want - 1) <= 2.0 ** -18 + near(far) + (4 + lens[0] + nqs[0] * hq // heads) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("scale", [-0.1, 1e-30, 1e-3, 1e4, 3e30])
+@pytest.mark.parametrize("form", [0, 2, 4])
+def test_many_rows_of_any_scale(form, scale):
+    lens, nqs, hq, heads, page, wide, _ = MANY[form]
+    for far in (0, 60, 100):
+        if abs(scale) * 2.0 ** far > 2.0 ** 115:  # (logits past fp32 are nobody's)
+            continue
+        c = Cache(lens, hq, heads, 64, 4, page, nqs, seed=form, wide=wide)
+        rescale(c, 0, far)
+        check_rows(c, c.weigh(scale=scale), 2.0 ** -18 + near(12))
+
+
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+def test_many_rows_near_and_far_together(bits, d):
+    """Rows whose logits lie on both sides of where references are kept in another way, in one warp and one group, and
+    rows that cross it from one tile to the next."""
+    c = Cache([1390, 300], 4, 2, d, bits, 32, [150, 60], seed=1)
+    by = 2.0 ** torch.arange(0, 15)[torch.arange(210) % 15]
+    c.q = (c.q.float() * by[:, None, None]).to(torch.bfloat16)
+    check_rows(c, c.weigh(), 2.0 ** -18 + near(12))
+    rising = 2.0 ** np.repeat(np.arange(11), 128)  # a tile's keys twice the last one's
+    for i, n in enumerate(c.lens):
+        codes, s, low = c.seqs[i]
+        j = np.arange(n)
+        pages, off = torch.from_numpy(c.table[i, j // 32]).long().cuda(), torch.from_numpy(j % 32).cuda()
+        c.params[pages, 0, :, off] *= torch.from_numpy(rising[:n]).to(torch.bfloat16).cuda()[:, None, None]
+        c.seqs[i] = (codes, s * rising[:n, None].astype(np.float32), low * rising[:n, None].astype(np.float32))
+    w = c.weigh()
+    check_rows(c, w, 2.0 ** -18 + near(12))
