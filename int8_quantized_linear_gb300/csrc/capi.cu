@@ -672,6 +672,17 @@ i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf1
                                             make_kv_cache(codes, params, H, page_size, num_pages), T, Hq, D, bits, env));
 }
 
+namespace {
+
+// What kv_cache_weights needs of workspace.  max_q is held to the query tokens there are: fewer rows can
+// mean a finer split of the tokens, so a bound above them would tell another size.
+int64_t weights_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t max_kv, int64_t& max_q, const LaunchEnv& env) {
+    max_q = max_q < T_q ? max_q : T_q;
+    return (int64_t)kv_weights_workspace(B, T_q, Hq / H, H, max_kv, max_q, env.sm_count);
+}
+
+}  // namespace
+
 i8ql_status i8ql_kv_weights_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_t H, int64_t D, int64_t bits,
                                       int64_t page_size, int64_t table_width, int64_t max_q, int64_t* bytes) {
     I8QL_TRY(check_kv(H, D, bits, page_size, 1));
@@ -682,7 +693,7 @@ i8ql_status i8ql_kv_weights_workspace(int64_t B, int64_t T_q, int64_t Hq, int64_
     LaunchEnv env;
     i8ql_status s;
     if (!launch_env(nullptr, &env, &s)) return s;
-    *bytes = (int64_t)kv_weights_workspace(B, T_q, Hq / H, H, table_width * page_size, max_q, env.sm_count);
+    *bytes = weights_workspace(B, T_q, Hq, H, table_width * page_size, max_q, env);
     return I8QL_OK;
 }
 
@@ -715,9 +726,8 @@ i8ql_status kv_cache_weights(const i8ql_bf16* q, int64_t q_stride, const uint8_t
     i8ql_status s;
     if (!launch_env(stream, &env, &s)) return s;
     const int64_t G = Hq / H, max_kv = table_width * page_size;
-    max_q = max_q < T_q ? max_q : T_q;
+    const int64_t need = weights_workspace(B, T_q, Hq, H, max_kv, max_q, env);
     if (!kv_weights_fits(B, G, H, max_kv, max_q, env.sm_count)) return I8QL_ERR_UNSUPPORTED;
-    const int64_t need = (int64_t)kv_weights_workspace(B, T_q, G, H, max_kv, max_q, env.sm_count);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need) return I8QL_ERR_WORKSPACE_LIMIT;
         if (!aligned(workspace, 16)) return I8QL_ERR_INVALID_ARG;
