@@ -707,7 +707,8 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, 
               n = original f / 2 pi: divided by factor up to n = low, as they
               are from n = high on, between them blended linearly in n
     "index"   the same, blended linearly in i between the (whole) indices that
-              turn `high` and `low` times
+              turn `high` (usually 32) and `low` times, which are held to 0 and
+              rot - 1: the second may lie behind the last pair
     """
     if rot <= 0 or rot % 2 or base <= 1.0 or factor < 1.0:
         raise ValueError("rot must be positive and even, base above 1, factor at least 1")
@@ -726,7 +727,7 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, 
         f = [x * ((1 - k) / factor + k) for x, k in zip(f, keep)]
     elif scaling == "index":
         at = lambda turns: n * math.log(original / (2 * math.pi * turns)) / math.log(base)  # noqa: E731
-        begin, end = max(math.floor(at(high)), 0), min(math.ceil(at(low)), n - 1)
+        begin, end = max(math.floor(at(high)), 0), min(math.ceil(at(low)), rot - 1)
         keep = [1 - min(max((i - begin) / max(end - begin, 1e-3), 0.0), 1.0) for i in range(n)]
         f = [x * ((1 - k) / factor + k) for x, k in zip(f, keep)]
     elif scaling not in (None, "base"):
