@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const KvEvict
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool sure = sures >> i & 1, tie = ties >> i & 1;
-            if (sure || (tie && t < left)) kept[s + min(t, left)] = j0 + g * 128 + lane * 4 + i;
+            // (weights that are read anew in each pass may have changed meanwhile: no slot past the row)
+            const uint32_t slot = s + min(t, left);
+            if ((sure || (tie && t < left)) && slot < (uint32_t)p.budget) kept[slot] = j0 + g * 128 + lane * 4 + i;
             s += sure;
             t += tie;
         }
