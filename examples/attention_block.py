@@ -38,6 +38,8 @@ class AttentionBlock:
                  rotary=None, budget=None, recent=16, device="cuda"):
         """rotary: frequencies (``rotary_frequencies``) of the rotary channels, or None.  budget: tokens a sequence
         keeps, its first 4 and its last `recent` among them, or None."""
+        if budget is not None and not 0 <= recent <= budget:
+            raise ValueError(f"the last {recent} tokens are not a part of a budget of {budget}")
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.q_heads, self.heads, self.head_dim, self.page_size = q_heads, heads, head_dim, page_size
