@@ -36,8 +36,9 @@ class AttentionBlock:
 
     def __init__(self, hidden, q_heads, heads, head_dim, *, bits=4, pages=64, page_size=64, max_tokens=4096, seed=0,
                  rotary=None, budget=None, recent=16, device="cuda"):
-        """rotary: frequencies (``rotary_frequencies``) of the rotary channels, or None.  budget: tokens a sequence
-        keeps, its first 4 and its last `recent` among them, or None."""
+        """max_tokens: the most that a sequence holds at a time.  rotary: frequencies (``rotary_frequencies``) of the
+        rotary channels, or None.  budget: tokens a sequence keeps, its first 4 and its last `recent` among them, or
+        None."""
         if budget is not None and not 0 <= recent <= budget:
             raise ValueError(f"the last {recent} tokens are not a part of a budget of {budget}")
         g = torch.Generator(device=device)
@@ -55,7 +56,8 @@ class AttentionBlock:
         self.pages, self.lengths = {}, {}  # per sequence
         self.width = -(-max_tokens // page_size)
         self.device = device
-        self.positions = {}  # of a sequence's next token
+        self.positions = {}  # of a sequence's next token; they go on where its length is cut
+        self.rotary = rotary
         self.table = None if rotary is None else capi.rotary_table(rotary, max_tokens)
         self.budget, self.recent = budget, recent
         self.weights = None if budget is None else torch.zeros((pages, heads, page_size), device=device)
@@ -64,6 +66,9 @@ class AttentionBlock:
         """x bf16 [tokens, hidden]: the new tokens of the sequences in `batch`
         (pairs of a sequence's name and its number of new tokens), in order.
         Returns bf16 [tokens, hidden]."""
+        end = max((self.positions.get(name, 0) + n for name, n in batch), default=0)
+        if self.table is not None and end > self.table.shape[0]:
+            self.table = capi.rotary_table(self.rotary, max(end, 2 * self.table.shape[0]))
         slots, places, table = [], [], torch.zeros((len(batch), self.width), dtype=torch.int32)
         for i, (name, n) in enumerate(batch):
             mine = self.pages.setdefault(name, [])
