@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_math.cuh"
 #include "kv_weights.cuh"
@@ -234,18 +235,27 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const KvEvict
             if (lane >= m) upto += o;
         }
         uint32_t s = sure_before + ((upto - mine) & 0xffff), t = ties_before + ((upto - mine) >> 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool sure = sures >> i & 1, tie = ties >> i & 1;
-            // (weights that are read anew in each pass may have changed meanwhile: no slot past the row)
-            const uint32_t slot = s + min(t, left);
-            if ((sure || (tie && t < left)) && slot < (uint32_t)p.budget) kept[slot] = j0 + g * 128 + lane * 4 + i;
-            s += sure;
-            t += tie;
-        }
         const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
         sure_before += all & 0xffff;
         ties_before += all >> 16;
+        // (weights that are read anew in each pass may have changed meanwhile: no slot past the row;
+        // asked once a group: of each token it costs 1.6 us of 27.5)
+        const uint32_t budget = (uint32_t)p.budget;
+        auto place = [&](auto held) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool sure = sures >> i & 1, tie = ties >> i & 1;
+                const uint32_t slot = s + min(t, left);
+                if ((sure || (tie && t < left)) && (!decltype(held)::value || slot < budget))
+                    kept[slot] = j0 + g * 128 + lane * 4 + i;
+                s += sure;
+                t += tie;
+            }
+        };
+        if (sure_before + min(ties_before, left) <= budget)
+            place(std::false_type{});
+        else
+            place(std::true_type{});
     }
     if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
