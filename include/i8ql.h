@@ -605,8 +605,8 @@ i8ql_status kv_cache_store_rotary(const i8ql_bf16* q, int64_t q_stride, i8ql_bf1
  *
  * previous and weights: fp32 [num_pages, H, page_size], 16-byte aligned; the
  * same buffer, or two that do not overlap.  Rows that see no token add
- * nothing.  A key row that is not finite gives unspecified weights of its
- * sequence and head where it is seen.
+ * nothing.  A key or query row that is not finite gives unspecified weights of
+ * its sequence and head where it is seen or sees.
  * Precision: exponentials, sums and statistics in fp32.  A logit is scale times
  * s_j (q . code_j) + low_j (sum of q), and off by up to 2^-18 |scale|
  * times the same with magnitudes, which exceeds the logit where the two parts

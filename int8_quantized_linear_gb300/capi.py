@@ -869,7 +869,9 @@ def kv_cache_weights(q, codes, params, page_table, kv_lens, weights, q_offsets=N
     [num_pages, heads, page_size]) = previous (the same; may be weights; None:
     nothing yet) of the tokens cached before this call's queries, plus the
     softmax weights of the query rows that see a token.  The other arguments as
-    kv_cache_attention's, max_q being the most query rows a sequence has.
+    kv_cache_attention's, max_q being the most query tokens a sequence has (with
+    q_offsets and without max_q all are taken for one sequence's: a batch of
+    single tokens should say 1).
     Tokens that no query sees keep their weights.  Returns weights."""
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, head_dim]")

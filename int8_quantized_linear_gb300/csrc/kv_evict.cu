@@ -13,7 +13,7 @@
 // each kept token its slot.  A cluster of CTAs takes a sequence's head, each a run of
 // its tokens, which it reads once, into shared memory; histograms and counts are added up
 // through distributed shared memory.  Nothing depends on timing (the histogram's atomics
-// only count).  32 sequences of up to 16384 tokens with 8 heads, cut to 2048: 27.4 us, bound by
+// only count).  32 sequences of up to 16384 tokens with 8 heads, cut to 2048: 28.0 us, bound by
 // the instructions (issue slots 65 %) and the barriers between the passes; 70.7 with the
 // weights read from memory in four passes of 8 bits.
 //
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const KvEvict
         sure_before += all & 0xffff;
         ties_before += all >> 16;
         // (weights that are read anew in each pass may have changed meanwhile: no slot past the row;
-        // asked once a group: of each token it costs 1.6 us of 27.5)
+        // asked once a group, 0.6 us of 28.0; of each token 1.6)
         const uint32_t budget = (uint32_t)p.budget;
         auto place = [&](auto held) {
 #pragma unroll

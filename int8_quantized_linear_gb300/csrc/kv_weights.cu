@@ -28,9 +28,9 @@
 // Otherwise two kernels both go over the keys.  The first leaves each row's (m, l) over
 // a part of the tokens, the second joins them and sums the weights of its tokens over all
 // rows, in order; no atomics.  16 sequences of up to 8191 tokens with 64 rows a
-// head (16 heads x 64 channels, 8 bits): 57 and 52 us, bound by the instructions beside
-// the products (unpacking per 32 rows, an exponential a logit and pass; issue slots 50 %, 11
-// warps an SM) and by the beginnings and ends of blocks.
+// head (16 heads x 64 channels, 8 bits): 58 and 52 us, bound by the instructions beside
+// the products (unpacking per 32 rows, an exponential a logit and pass; issue slots 40 and 50 %,
+// 8 and 11 warps an SM) and by the beginnings and ends of blocks.
 // Tokens that no row sees keep what they have.
 //
 // The layout of the products is that of kv_attention.cu: 16 tokens are the M rows

@@ -30,8 +30,8 @@ struct KvWeightsParams {
 
 // Query rows of a cache head up to which kv_weights.cu takes a call; the kernels for many of
 // them (kv_weights_many.cu) fill operand tiles of 256 rows, whatever there is.  With 64 rows, 16
-// sequences of up to 8191 tokens: 64 channels and 8 bits 109 us here and 211 there, 128
-// channels and 4 bits 161 and 214.
+// sequences of up to 8191 tokens: 64 channels and 8 bits 110 us here and 211 there, 128
+// channels and 4 bits 165 and 214.
 constexpr int64_t kKvWeightsFewRows = 64;
 size_t kv_weights_many_workspace(int64_t B, int64_t T_q, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);
 bool kv_weights_many_fits(int64_t B, int64_t G, int64_t H, int64_t max_kv, int64_t max_q, int sms);

@@ -35,17 +35,17 @@
 // q k themselves, which is taken off the others before the scale is multiplied in, so that the
 // largest has the exponent 0, however large it is.  Tiles where logits could come near that
 // (their exponents say so), and halves with large maxima in the second pass, go through
-// functions of their own.  (The question costs the first pass 2 % with 128 channels of 4 bits.)
+// functions of their own.  (The question costs the first pass up to 2 %.)
 //
 // The second pass leaves sums over up to 128-row halves of a group of row blocks per
 // token in a workspace (a thread adds to its own place, in order), and a third kernel
 // adds those up: no atomics, the same bits whatever the timing.
 //
 // Two chunks of 2048 tokens over 8192 (32 query heads, 8 cache heads, 128 channels, 4 bits):
-// 312 and 376 us and 7 for the joining, 243 GFLOP a pass, 780 and 645 TFLOP/s.  Bound by
+// 311 and 374 us and 7 for the joining, 243 GFLOP a pass, 780 and 650 TFLOP/s.  Bound by
 // the roles together: the products alone (nothing unpacked, no softmax) take 240 us a
 // pass, the softmax alone 221 and 283.  Measured and dropped: 256 rows a product in the
-// second pass (397 against 376 us), three stages with 8 warps unpacking every tile and
+// second pass (397 against 374 us), three stages with 8 warps unpacking every tile and
 // one for the exponents (343 and 396).
 //
 // Roles: 16 softmax warps, a set of 8 for the even steps and one for the odd ones, each
